@@ -14,7 +14,7 @@ import os
 from . import build as _build
 
 DG_OK, DG_ERR_INVALID_ARG, DG_ERR_MISALIGNED, DG_ERR_UNSUPPORTED = 0, 1, 2, 3
-DG_ERR_CUDA, DG_ERR_TIMEOUT, DG_ERR_NO_MEMORY = 4, 5, 6
+DG_ERR_CUDA, DG_ERR_TIMEOUT, DG_ERR_NO_MEMORY, DG_ERR_BAD_INDEX = 4, 5, 6, 7
 DG_OP_N, DG_OP_T = 0, 1
 DG_OUT_BF16, DG_OUT_F32 = 0, 1
 (DG_KERNEL_NONE, DG_KERNEL_SCALE, DG_KERNEL_SIMT_F32, DG_KERNEL_TC_BF16, DG_KERNEL_THIN_BF16,
@@ -26,7 +26,9 @@ EXPORTED = [
     "dg_raster_tile", "dg_streamk_start", "dg_model_traffic_bytes", "dg_model_local_bytes",
     "dg_version", "dg_set_fault_injection", "gemm_bf16_decode_noalloc", "gemm_bf16_gate_up_silu",
     "attention_bf16", "quantize_rows_e4m3", "gemm_fp8_e4m3", "dg_model_quant_traffic_bytes",
-    "gemm_bf16_decode_chain",
+    "gemm_bf16_decode_chain", "rmsnorm_residual_bf16", "rmsnorm_residual_e4m3",
+    "dg_kv4_block_bytes", "kv4_append", "kv4_gather", "dg_attention_kv4_workspace_bytes",
+    "attention_kv4", "dg_moe_workspace_bytes", "moe_bf16",
 ]
 
 
@@ -51,6 +53,16 @@ class dg_plan(ctypes.Structure):
 
 
 _lib = None
+
+
+class dg_kv4_cache(ctypes.Structure):
+    """The paged 4-bit key-value cache: data [pages, heads, dg_kv4_block_bytes(page_size, d)] bytes."""
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+    def __init__(self, data, pages, page_size, heads, d):
+        super().__init__(_ptr(data), pages, page_size, heads, d)
+        self.tensor = data  # the pages live as long as this handle
 
 
 def library_path() -> str:
@@ -83,9 +95,27 @@ def load(build_if_missing: bool = True):
                                    i64, i64, vp, i64, i64, vp]
     lib.gemm_bf16_decode_noalloc.argtypes = [i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64,
                                              i32, vp]
+    norm = [i64, i64, vp, i64, i32, vp, i64, i32, vp, i64, vp, f32, vp, i64]
+    lib.rmsnorm_residual_bf16.argtypes = norm + [vp]
+    lib.rmsnorm_residual_e4m3.argtypes = norm + [vp, vp]
+    pc = ctypes.POINTER(dg_kv4_cache)
+    lib.dg_kv4_block_bytes.argtypes = [i32, i32]
+    lib.dg_kv4_block_bytes.restype = i64
+    lib.kv4_append.argtypes = [pc, i64, vp, i64, vp, i64, vp, vp]
+    lib.kv4_gather.argtypes = [pc, i64, vp, vp, i64, vp, i64, vp]
+    lib.dg_attention_kv4_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
+    lib.dg_attention_kv4_workspace_bytes.restype = i64
+    lib.attention_kv4.argtypes = [pc, i64, i64, i64, f32, vp, i64, i64, vp, i64, vp, vp, i64, i64, vp,
+                                  i64, vp]
+    lib.dg_moe_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.dg_moe_workspace_bytes.restype = i64
+    lib.moe_bf16.argtypes = [i64, i64, i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64,
+                             vp, i64, i64, vp, i64, vp, i64, vp]
     for f in ("gemm_f32", "gemm_f32_strided_batched", "gemm_bf16", "gemm_bf16_strided_batched",
               "gemm_bf16_decode_noalloc", "gemm_bf16_gate_up_silu", "attention_bf16",
-              "quantize_rows_e4m3", "gemm_fp8_e4m3", "gemm_bf16_decode_chain"):
+              "quantize_rows_e4m3", "gemm_fp8_e4m3", "gemm_bf16_decode_chain",
+              "rmsnorm_residual_bf16", "rmsnorm_residual_e4m3", "kv4_append", "kv4_gather",
+              "attention_kv4", "moe_bf16"):
         getattr(lib, f).restype = ctypes.c_int
     lib.dg_status_string.argtypes = [ctypes.c_int]
     lib.dg_status_string.restype = ctypes.c_char_p
@@ -228,6 +258,73 @@ def attention_bf16(batch, Lq, Lkv, d, scale, causal, Q, ldq, strideQ, K, ldk, st
                             _ptr(K), ldk, strideK, _ptr(V), ldv, strideV, _ptr(O), ldo, strideO,
                             _stream(stream))
     return _ret(st, "attention_bf16", check)
+
+
+def rmsnorm_residual_bf16(rows, cols, X, ldx, x_type, R, ldr, r_type, H, ldh, gain, eps, Y, ldy,
+                          stream=None, check=True) -> int:
+    """h = X + R, H = round(h), Y = bf16(h * gain / sqrt(mean(h^2) + eps)), row by row."""
+    lib = load()
+    st = lib.rmsnorm_residual_bf16(rows, cols, _ptr(X), ldx, x_type, _ptr(R), ldr, r_type, _ptr(H),
+                                   ldh, _ptr(gain), eps, _ptr(Y), ldy, _stream(stream))
+    return _ret(st, "rmsnorm_residual_bf16", check)
+
+
+def rmsnorm_residual_e4m3(rows, cols, X, ldx, x_type, R, ldr, r_type, H, ldh, gain, eps, Q, ldq,
+                          scales, stream=None, check=True) -> int:
+    """rmsnorm_residual_bf16 with E4M3 codes Q and one float32 scale per row instead of Y."""
+    lib = load()
+    st = lib.rmsnorm_residual_e4m3(rows, cols, _ptr(X), ldx, x_type, _ptr(R), ldr, r_type, _ptr(H),
+                                   ldh, _ptr(gain), eps, _ptr(Q), ldq, _ptr(scales),
+                                   _stream(stream))
+    return _ret(st, "rmsnorm_residual_e4m3", check)
+
+
+def dg_kv4_block_bytes(page_size, d) -> int:
+    return load().dg_kv4_block_bytes(page_size, d)
+
+
+def kv4_append(cache, tokens, K, ldk, V, ldv, slots, stream=None, check=True) -> int:
+    """Quantises K and V rows to 4 bits and writes them to their slots of the cache."""
+    lib = load()
+    st = lib.kv4_append(ctypes.byref(cache), tokens, _ptr(K), ldk, _ptr(V), ldv, _ptr(slots),
+                        _stream(stream))
+    return _ret(st, "kv4_append", check)
+
+
+def kv4_gather(cache, tokens, slots, K, ldk, V, ldv, stream=None, check=True) -> int:
+    """Reads the slots' rows back as the BF16 values that their codes stand for."""
+    lib = load()
+    st = lib.kv4_gather(ctypes.byref(cache), tokens, _ptr(slots), _ptr(K), ldk, _ptr(V), ldv,
+                        _stream(stream))
+    return _ret(st, "kv4_gather", check)
+
+
+def dg_attention_kv4_workspace_bytes(batch, Lq, heads_q, heads_kv, d) -> int:
+    return load().dg_attention_kv4_workspace_bytes(batch, Lq, heads_q, heads_kv, d)
+
+
+def attention_kv4(cache, batch, Lq, heads_q, scale, Q, ldq, strideQ, page_table, ldt, lens, O, ldo,
+                  strideO, workspace, workspace_bytes, stream=None, check=True) -> int:
+    """Attention of each sequence's newest Lq tokens over the paged 4-bit cache."""
+    lib = load()
+    st = lib.attention_kv4(ctypes.byref(cache), batch, Lq, heads_q, scale, _ptr(Q), ldq, strideQ,
+                           _ptr(page_table), ldt, _ptr(lens), _ptr(O), ldo, strideO,
+                           _ptr(workspace), workspace_bytes, _stream(stream))
+    return _ret(st, "attention_kv4", check)
+
+
+def dg_moe_workspace_bytes(T, K, I, E, top) -> int:
+    return load().dg_moe_workspace_bytes(T, K, I, E, top)
+
+
+def moe_bf16(T, K, I, E, top, renorm, X, ldx, logits, ldl, Wg, ldwg, strideWg, Wu, ldwu, strideWu,
+             Wd, ldwd, strideWd, Y, ldy, workspace, workspace_bytes, stream=None, check=True) -> int:
+    """A mixture-of-experts layer for few tokens, from the router's logits on."""
+    lib = load()
+    st = lib.moe_bf16(T, K, I, E, top, 1 if renorm else 0, _ptr(X), ldx, _ptr(logits), ldl,
+                      _ptr(Wg), ldwg, strideWg, _ptr(Wu), ldwu, strideWu, _ptr(Wd), ldwd, strideWd,
+                      _ptr(Y), ldy, _ptr(workspace), workspace_bytes, _stream(stream))
+    return _ret(st, "moe_bf16", check)
 
 
 def status_string(status: int) -> str:

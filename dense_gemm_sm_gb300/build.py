@@ -23,8 +23,9 @@ LIB_NAME = "libdgemm_sm103a.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "sgemm_simt.cu", "gemm_tc.cu", "gemm_thin.cu", "gemm_thin_noalloc.cu",
-           "attention.cu", "quant.cu", "gemm_chain.cu"]
-HEADERS = ["dg_internal.h", "ptx.cuh", "tile_sched.h"]
+           "attention.cu", "quant.cu", "gemm_chain.cu", "serving_api.cu", "rmsnorm.cu", "kv4_cache.cu",
+           "kv4_attention.cu", "moe.cu"]
+HEADERS = ["dg_internal.h", "ptx.cuh", "serving.h", "tile_sched.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

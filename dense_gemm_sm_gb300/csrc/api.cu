@@ -21,6 +21,7 @@
 #include <utility>
 
 #include "dg_internal.h"
+#include "serving.h"
 #include "tile_sched.h"
 
 namespace dg {
@@ -34,8 +35,9 @@ constexpr int kRasterGroup = 8;
 constexpr int64_t kThinMaxM = 32;
 constexpr int kSimtCtasPerSmPlan = 2;  // occupancy of the SIMT kernel (launch bounds 256 x 2)
 
-// Device status word: kernels record the first bounded-wait expiry here.
-__device__ uint32_t g_status_word;
+// Device status words: [0] kernels record the first bounded-wait expiry here, [1] the first
+// index (page, slot, length) that lay outside its table.
+__device__ uint32_t g_status_word[2];
 
 std::mutex g_mu;
 uint32_t* g_status_ptr[kMaxDevices] = {};
@@ -618,6 +620,12 @@ cudaError_t launch_scale(void* C, bool c_f32, int64_t M, int64_t N, int64_t ldc,
   return cudaGetLastError();
 }
 
+cudaError_t serving_device(uint32_t** status, int* sms) {
+  int dev = 0;
+  const cudaError_t e = current_device(&dev);
+  return e != cudaSuccess ? e : device_info(dev, status, sms);
+}
+
 }  // namespace dg
 
 // ==================================================================== C ABI
@@ -919,6 +927,7 @@ const char* dg_status_string(dg_status s) {
     case DG_ERR_CUDA: return "DG_ERR_CUDA: a CUDA runtime call failed";
     case DG_ERR_TIMEOUT: return "DG_ERR_TIMEOUT: a kernel gave up a bounded wait";
     case DG_ERR_NO_MEMORY: return "DG_ERR_NO_MEMORY: workspace allocation failed";
+    case DG_ERR_BAD_INDEX: return "DG_ERR_BAD_INDEX: a page, slot or length outside its table was skipped";
   }
   return "unknown dg_status";
 }
@@ -931,13 +940,14 @@ dg_status dg_device_status(void* stream) {
   int sms = 0;
   if (device_info(dev, &status, &sms) != cudaSuccess) return DG_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return DG_ERR_CUDA;
-  uint32_t word = 0;
-  if (cudaMemcpy(&word, status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
+  uint32_t word[2] = {0, 0};
+  if (cudaMemcpy(word, status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
     return DG_ERR_CUDA;
-  if (word == 0) return DG_OK;
-  const uint32_t zero = 0;
-  if (cudaMemcpy(status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
+  if (word[0] == 0 && word[1] == 0) return DG_OK;
+  const uint32_t zero[2] = {0, 0};
+  if (cudaMemcpy(status, zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
     return DG_ERR_CUDA;
+  if (word[0] == 0) return DG_ERR_BAD_INDEX;
   // A CTA that gave up may have left split-K arrival counters non-zero.
   {
     std::lock_guard<std::mutex> lock(g_mu);

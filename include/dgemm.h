@@ -56,7 +56,9 @@ typedef enum {
   DG_ERR_UNSUPPORTED = 3,  /* shape the kernels do not cover (e.g. > 2^31-1 rows) */
   DG_ERR_CUDA = 4,         /* a CUDA runtime call failed (launch, allocation, query) */
   DG_ERR_TIMEOUT = 5,      /* a kernel gave up a bounded wait; results are invalid */
-  DG_ERR_NO_MEMORY = 6     /* workspace allocation failed */
+  DG_ERR_NO_MEMORY = 6,    /* workspace allocation failed */
+  DG_ERR_BAD_INDEX = 7     /* a kernel met a page, slot or length outside its table and
+                              skipped what it names (see dg_device_status) */
 } dg_status;
 
 typedef enum { DG_OP_N = 0, DG_OP_T = 1 } dg_op;
@@ -259,13 +261,153 @@ dg_status attention_bf16(int64_t batch, int64_t Lq, int64_t Lkv, int64_t d, floa
                          int64_t ldv, int64_t strideV, uint16_t* O, int64_t ldo, int64_t strideO,
                          void* stream);
 
+/* ----------------------------------------------------------------------
+ * Serving operators: what stands between the GEMMs of a decoder layer's token
+ * step.  They allocate nothing: scratch is the caller's `workspace`, so a call
+ * may be captured into a graph at once, and calls with different workspaces may
+ * overlap.  A workspace is ZERO-FILLED ONCE by the caller before its first use
+ * (of at least the bytes its size function gives, 256-byte aligned); a call
+ * leaves it ready for the next call of the same entry point, of any size that
+ * fits.  Two calls that share a workspace must be ordered (one stream).  After
+ * DG_ERR_TIMEOUT zero it again.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Residual addition and root-mean-square norm of each row:
+ *     h = X[i] + R[i],  H[i] = round(h),  y = h * gain / sqrt(mean(h^2) + eps),
+ *     rmsnorm_residual_bf16:  Y[i] = bf16(y)
+ *     rmsnorm_residual_e4m3:  amax = max |y|, scales[i] = amax / 448,
+ *                             Q[i] = E4M3(y * (448 / amax))
+ * with h, the mean and y in FP32 and one rounding per output (the norm is of the unrounded
+ * h).  Q and scales are what gemm_fp8_e4m3 reads, as quantize_rows_e4m3 writes them; a row
+ * of zeros gets codes 0 and scale 0, a row holding Inf or NaN unspecified codes.
+ *   - X: rows x cols of x_type (DG_OUT_BF16 or DG_OUT_F32), row stride ldx.  R and H: rows x
+ *     cols of r_type, strides ldr and ldh; H may be R (in place).  R and H both null: no
+ *     residual, h = X.  gain: cols BF16.  Y: BF16, ldy.  Q: bytes, ldq.
+ *   - Errors: negative sizes, short strides, null pointers (one of R and H alone), an eps
+ *     that is negative or not finite DG_ERR_INVALID_ARG; sizes over 2^31 - 1
+ *     DG_ERR_UNSUPPORTED; a pointer not aligned to its element DG_ERR_MISALIGNED.  rows == 0
+ *     or cols == 0: nothing.  Any other alignment is accepted (16-byte rows take the vector
+ *     path).
+ */
+dg_status rmsnorm_residual_bf16(int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                                dg_out x_type, const void* R, int64_t ldr, dg_out r_type, void* H,
+                                int64_t ldh, const uint16_t* gain, float eps, uint16_t* Y,
+                                int64_t ldy, void* stream);
+dg_status rmsnorm_residual_e4m3(int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                                dg_out x_type, const void* R, int64_t ldr, dg_out r_type, void* H,
+                                int64_t ldh, const uint16_t* gain, float eps, uint8_t* Q,
+                                int64_t ldq, float* scales, void* stream);
+
+/*
+ * A paged cache of keys and values in 4 bits.  Each row of d elements (one token, one head)
+ * has codes 0..15 and a BF16 scale and zero:
+ *     zero = min x,  scale = bf16((max x - min x) / 15),
+ *     code = clamp(round_half_even((x - zero) / scale), 0, 15),   x ~ zero + scale * code
+ * (IEEE FP32 operations; a constant row has scale 0 and codes 0; rows must be finite).
+ * data: [pages][heads][block], a block of dg_kv4_block_bytes(page_size, d) = page_size *
+ * (d + 8) bytes holding page_size / 16 records of 16 tokens:
+ *     16 x d/2 bytes        K codes, a token's row after the other, even column in the low half
+ *     [2][8][4][d/32][2][2] V codes: [token / 8][columns of d/8][token % 8 / 2][4 columns]
+ *                           [token % 2][2 bytes], columns in order from the low half
+ *     16 words, 16 words    K's and V's scale (low half) and zero (high half)
+ * so that one copy brings a whole record, and V's codes lie as the tensor-core operand wants
+ * them.  Token t of a page is slot page * page_size + t.  What unused slots hold is never
+ * interpreted.  page_size is a multiple of 16; d is 64 or 128; data 16-byte aligned.
+ */
+typedef struct {
+  uint8_t* data;
+  int64_t pages;
+  int32_t page_size, heads, d;
+} dg_kv4_cache;
+
+/* Bytes of one (page, head) block; 0 for a page size or d that the cache does not have. */
+int64_t dg_kv4_block_bytes(int32_t page_size, int32_t d);
+
+/*
+ * Writes K and V of `tokens` tokens to their slots (int64 on the device).  Element (i, h, c)
+ * of K at K[i * ldk + h * d + c], likewise V.  A negative slot is passed over; one past the
+ * cache is passed over and reported (DG_ERR_BAD_INDEX from dg_device_status).  Slots of one
+ * call are distinct.
+ * Errors: null pointers, short strides, a page size that is not a positive multiple of 16
+ * DG_ERR_INVALID_ARG; another d DG_ERR_UNSUPPORTED; data not 16-byte, slots not 8-byte or K
+ * or V not 2-byte aligned DG_ERR_MISALIGNED.  tokens == 0: nothing.
+ */
+dg_status kv4_append(const dg_kv4_cache* cache, int64_t tokens, const uint16_t* K, int64_t ldk,
+                     const uint16_t* V, int64_t ldv, const int64_t* slots, void* stream);
+
+/*
+ * Reads rows back: K and V get the BF16 values that the slots' codes stand for, zeros for a
+ * negative slot or one past the cache (the latter reported).  Layout and errors as kv4_append.
+ */
+dg_status kv4_gather(const dg_kv4_cache* cache, int64_t tokens, const int64_t* slots, uint16_t* K,
+                     int64_t ldk, uint16_t* V, int64_t ldv, void* stream);
+
+/*
+ * Attention of each sequence's newest Lq tokens over the cache ("Operator & Runtime" section
+ * 5.3.3's online softmax, K and V read in 4 bits):
+ *     O[b][i][h] = sum_j softmax_j(scale * Q[b][i][h] . K_j) V_j,   j <= lens[b] - Lq + i,
+ * K and V of head h / (heads_q / cache->heads).  The tokens are in the cache already: query i
+ * of sequence b sits at position lens[b] - Lq + i.  A query that sees no key (lens[b] - Lq + i
+ * < 0) gets 0.  FP32 scores, weights and sums; the weights times V's scale are rounded to BF16
+ * for the second product; O rounded once to BF16.
+ *   - Q: element (b, i, h, c) at Q[b * strideQ + i * ldq + h * d + c], likewise O.
+ *   - page_table: int32 [batch][ldt] on the device, entry (b, t) the page of tokens
+ *     [t * page_size, (t + 1) * page_size); entries past the length are not read.  lens:
+ *     int32 [batch] on the device.  A page outside the cache is treated as not visible, a
+ *     length outside [0, ldt * page_size] as the nearest bound; both are reported
+ *     (DG_ERR_BAD_INDEX from dg_device_status).
+ *   - workspace: see above; dg_attention_kv4_workspace_bytes (0 for sizes it does not take).
+ *   - Errors: heads_q not a multiple of the cache's heads, null pointers, overlapping strides,
+ *     a scale that is not finite and positive, a workspace that is too small
+ *     DG_ERR_INVALID_ARG; sizes over 65536 (batch, Lq, heads_q), batch * Lq * heads_q or ldt *
+ *     page_size over 2^31 - 1 DG_ERR_UNSUPPORTED; Q or O not 16-byte or workspace not 256-byte
+ *     aligned, ld or strides not multiples of 8 DG_ERR_MISALIGNED.  batch, Lq or heads_q == 0:
+ *     nothing.
+ */
+int64_t dg_attention_kv4_workspace_bytes(int64_t batch, int64_t Lq, int64_t heads_q,
+                                         int64_t heads_kv, int32_t d);
+dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, int64_t heads_q,
+                        float scale, const uint16_t* Q, int64_t ldq, int64_t strideQ,
+                        const int32_t* page_table, int64_t ldt, const int32_t* lens, uint16_t* O,
+                        int64_t ldo, int64_t strideO, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/*
+ * A mixture-of-experts layer for few tokens (T <= 64), from the router's logits on:
+ *     p = softmax(logits[t]) over the E experts, the `top` largest logits chosen (ties: the
+ *     lowest expert), w = p, or p over the sum of the chosen p when renorm is non-zero,
+ *     Z = bf16(SiLU(X[t] Wg[e]) * (X[t] Wu[e])),   Y[t] = bf16(sum over chosen e of w_e (Z Wd[e]))
+ * with FP32 sums and the activation on the unrounded sums (Z's rounding makes it an operand;
+ * gemm_bf16_gate_up_silu's two further roundings are not made).  A logit of -inf switches an
+ * expert off: it is never computed, and a row of nothing else gives Y = 0.  NaN logits rank
+ * as -inf.  +inf logits are not supported (unspecified weights).
+ *   - X: T x K BF16.  logits: T x E FP32, row stride ldl (gemm_bf16 with DG_OUT_F32 makes
+ *     them).  Wg, Wu: E matrices K x I, Wd: E matrices I x K, row-major BF16, row strides ldw,
+ *     expert strides strideW.  Y: T x K BF16.  Only chosen experts' weights are read.
+ *   - workspace: see above; dg_moe_workspace_bytes (0 for sizes it does not take).
+ *   - Errors: negative sizes, I == 0, top outside 1..E, short strides, null pointers, a
+ *     workspace that is too small DG_ERR_INVALID_ARG; T > 64, top > 16, E > 512 or K or I over
+ *     2^31 - 1 DG_ERR_UNSUPPORTED; X or a weight not 16-byte aligned, their strides not
+ *     multiples of 8, workspace not 256-byte aligned DG_ERR_MISALIGNED.  T == 0 or K == 0:
+ *     nothing.
+ */
+int64_t dg_moe_workspace_bytes(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top);
+dg_status moe_bf16(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top, int32_t renorm,
+                   const uint16_t* X, int64_t ldx, const float* logits, int64_t ldl,
+                   const uint16_t* Wg, int64_t ldwg, int64_t strideWg, const uint16_t* Wu,
+                   int64_t ldwu, int64_t strideWu, const uint16_t* Wd, int64_t ldwd,
+                   int64_t strideWd, uint16_t* Y, int64_t ldy, void* workspace,
+                   int64_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* dg_status_string(dg_status s);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's status
  * word.  Returns DG_ERR_TIMEOUT if a kernel gave up a bounded wait since the
- * last call, DG_ERR_CUDA if the stream reported an error, DG_OK otherwise.
+ * last call, DG_ERR_BAD_INDEX if one met an index outside its table (and none
+ * gave up a wait), DG_ERR_CUDA if the stream reported an error, DG_OK otherwise.
  * After a timeout the split-K workspace counters are re-zeroed.
  */
 dg_status dg_device_status(void* stream);
