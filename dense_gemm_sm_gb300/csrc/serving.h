@@ -64,6 +64,7 @@ struct Kv4AttnParams {
   const int32_t* lens;
   uint16_t* O; int64_t ldo, strideO;
   void* ws;
+  uint32_t* status;
   uint32_t* index_word;
 };
 int64_t kv4_attention_ws_bytes(int64_t batch, int64_t Lq, int64_t heads_q, int64_t heads_kv, int d);

@@ -174,6 +174,7 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
   p.table = page_table; p.ldt = ldt; p.lens = lens;
   p.O = O; p.ldo = ldo; p.strideO = strideO;
   p.ws = workspace;
+  p.status = status;
   p.index_word = status + 1;
   return from_cuda(launch_kv4_attention(p, d, sms, static_cast<cudaStream_t>(stream)));
 }
