@@ -152,11 +152,18 @@ def _ptr(x) -> int:
     return int(x)
 
 
+_torch = None
+
+
 def _stream(stream) -> int:
+    global _torch
     if stream is None:
-        import torch
-        if torch.cuda.is_available():
-            return int(torch.cuda.current_stream().cuda_stream)
+        if _torch is None:
+            import torch
+            _torch = torch
+        if _torch.cuda.is_available():
+            # The current stream's handle without a Stream object: 0.2 us instead of 2.9.
+            return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
         return 0
     if hasattr(stream, "cuda_stream"):
         return int(stream.cuda_stream)

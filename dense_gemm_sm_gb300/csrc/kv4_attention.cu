@@ -21,16 +21,17 @@
 //     as they lie (a lane 16 bytes, two key rows), V's codes lie in the cache in fragment order.
 //   * P goes from the first product's output layout to the second's operand layout by
 //     movmatrix, in registers.
-// Work: 64-key units of all (sequence, cache head, query block) items, in one row, cut evenly
-// over one CTA per SM whatever the lengths; the eight warps of a CTA take its units in turn,
-// each with its own ring of bulk copies (one per 16-token record, so pages of any multiple of
-// 16 do).  At the end of an item's piece the warps join their maxima, sums and outputs through
-// shared memory; an item cut between CTAs is joined, in CTA order, by the last of them to
-// arrive (so results do not depend on arrival).
+// Work: units of 64 (32) keys of all (sequence, cache head, query block) items, in one row, cut
+// evenly over the warps of one CTA per SM whatever the lengths: a warp walks its units with its
+// own ring of bulk copies (one per 16-token record, so pages of any multiple of 16 do) and
+// writes the items that lie whole in its share.  An item cut between warps of a CTA is joined
+// once, at the CTA's end, through shared memory; one cut between CTAs by the last of them to
+// arrive, in CTA order (so results do not depend on arrival).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "dg_internal.h"
 #include "ptx.cuh"
@@ -39,27 +40,28 @@
 namespace dg {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kUnit = 64;       // keys of a unit
-constexpr int kRecs = kUnit / kKv4Tokens;
 constexpr int kMaxCtas = 160;   // CTAs that the workspace has room for
-constexpr int kMaxRows = 32;    // query rows of a block
 // A CTA is given at least this many units, so that small calls use fewer CTAs and joins.
 constexpr int kMinUnits = 4;
-constexpr int64_t kPartFloats = kMaxRows * (128 + 2);
-constexpr int64_t kPartBytes = 2 * kMaxCtas * kPartFloats * 4;  // counters follow at this offset
+constexpr int64_t kCounterBytes = 1024;  // one ticket counter per CTA, then the parts
 
 template <int D, int NT>
 struct Cfg {
+  static constexpr int kUnit = NT == 4 ? 32 : 64;               // keys of a unit
+  static constexpr int kStep = 32;                              // keys of a softmax step
+  static constexpr int kRecs = kUnit / kKv4Tokens;
   static constexpr int kRec = kv4_record_bytes(D);
   static constexpr int kUnitBytes = kRecs * kRec;
-  static constexpr int kStages = D == 64 ? 4 : (NT == 4 ? 2 : 3);
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = NT == 4 ? 4 : (D == 64 || NT == 2 ? 3 : 2);
   static constexpr int kRing = kWarps * kStages * kUnitBytes;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kJoin = kWarps * 8 * 64 * 4;             // one slice: 8 rows x 64 columns per warp
-  static constexpr int kQ = NT == 4 ? NT * (D / 16) * 32 * 8 : 0;  // Q fragments (registers otherwise)
-  static constexpr int kSmem = kRing + kJoin + kQ;
+  static constexpr int kPart = kRows * (D + 2);                 // floats of a part: outputs, maxima, sums
+  static constexpr int kQ = NT == 4 ? NT * (D / 16) * 32 * 8 : 0;  // a warp's Q fragments (registers otherwise)
+  static constexpr int kSmem = kRing + kWarps * kQ;
+  static_assert(kWarps * kPart * 4 <= kRing, "the warps' last parts take the ring's place");
+  static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -124,17 +126,17 @@ __device__ __forceinline__ uint32_t take_ticket(uint32_t* a) {
   return old;
 }
 
-struct Shared {
-  uint64_t full[kWarps * 4];
-  uint32_t mask[kWarps * 4];   // records of the stage that were copied
-  float m[kWarps][kMaxRows], l[kWarps][kMaxRows], z[kWarps][kMaxRows];
-  int64_t scan[kThreads / 32];
-  int64_t start_b, start_off;
-  uint32_t abort, last;
-};
-
-__device__ __forceinline__ int64_t start_of(int64_t c, int64_t units, int64_t ctas) { return c * units / ctas; }
-__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t units, int64_t ctas) { return ((x + 1) * ctas - 1) / units; }
+// First unit of worker c, and the worker that has unit x; 32-bit where the products fit.
+constexpr int64_t kSmall = int64_t(1) << 20;  // units; workers <= 160 * 12
+__device__ __forceinline__ int64_t start_of(int64_t c, int64_t units, int64_t workers) {
+  if (units < kSmall) return static_cast<uint32_t>(c) * static_cast<uint32_t>(units) / static_cast<uint32_t>(workers);
+  return c * units / workers;
+}
+__device__ __forceinline__ int64_t worker_of(int64_t x, int64_t units, int64_t workers) {
+  if (units < kSmall)
+    return (static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(workers) - 1) / static_cast<uint32_t>(units);
+  return ((x + 1) * workers - 1) / units;
+}
 
 // Position in the row of all units: unit r is unit u of item `item` of sequence b.
 struct Walk {
@@ -143,22 +145,68 @@ struct Walk {
   int32_t len, units, item, u;
 };
 
+// An item that a warp has a part of.
+struct Cut {
+  int64_t b, first;  // sequence, the item's first unit
+  int32_t item, units;
+};
+
+// A running softmax-weighted sum of parts: maximum, sum of weights, four outputs.
+struct Sum {
+  float m = -INFINITY, l = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float mk, float lk, const float4& x) {
+    const float top = fmaxf(m, mk);
+    if (!(top > -INFINITY)) return;  // nothing seen yet
+    const float a = ex2(m - top), b = ex2(mk - top);
+    m = top;
+    l = l * a + lk * b;
+    v.x = v.x * a + x.x * b;
+    v.y = v.y * a + x.y * b;
+    v.z = v.z * a + x.z * b;
+    v.w = v.w * a + x.w * b;
+  }
+  __device__ __forceinline__ uint2 value() const {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    return make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+  }
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const Kv4AttnParams p, const int qblocks) {
+struct Shared {
+  static constexpr int kWarps = Cfg<D, NT>::kWarps;
+  uint64_t full[kWarps * 4];
+  uint32_t mask[kWarps * 4];   // records of the stage that were copied
+  int64_t scan[kWarps];
+  Cut head[kWarps], tail[kWarps];
+  uint8_t has_head[kWarps], has_tail[kWarps];
+  Cut fin[2];                  // items of other CTAs too, for which this CTA came last
+  uint32_t last[2];
+  int64_t start_b, start_off;
+  uint32_t abort;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+    kv4_attention_kernel(const Kv4AttnParams p, const int qblocks) {
   using C = Cfg<D, NT>;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads, kUnit = C::kUnit, kRecs = C::kRecs;
   constexpr int KS = D / 16;       // k steps of the first product
   constexpr int MT = D / 16;       // m tiles of the second
   constexpr int W = D / 32;        // words of a lane's share of a row
+  constexpr int RS = C::kStep / kKv4Tokens;  // records of a softmax step
+  constexpr uint32_t kOnes = 0x3F803F80u;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Shared sh;
+  __shared__ Shared<D, NT> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kUnitBytes;
-  float* join = reinterpret_cast<float*>(smem + C::kRing);
-  const uint32_t qfrag = smem_u32(smem) + C::kRing + C::kJoin;
+  const uint32_t qfrag = smem_u32(smem) + C::kRing + warp * C::kQ;
 
   if (lane == 0)
     for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&sh.full[warp * 4 + s]), 1);
   if (tid == 0) sh.abort = 0;
+  if (tid < 2) sh.last[tid] = 0;
+  if (tid < kWarps) sh.has_head[tid] = sh.has_tail[tid] = 0;
   fence_barrier_init();
   pdl_trigger();
   pdl_wait();
@@ -175,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const Kv4Att
   const int64_t per = (p.batch + kThreads - 1) / kThreads;
   const int64_t b_lo = tid * per, b_hi = b_lo + per < p.batch ? b_lo + per : p.batch;
   int64_t mine = 0;
+#pragma unroll 1
   for (int64_t b = b_lo; b < b_hi; ++b) {
     const int32_t n = p.lens[b];
     if (blockIdx.x == 0 && (n < 0 || n > cap)) atomicCAS(p.index_word, 0u, kDevBadIndex);
@@ -182,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const Kv4Att
   }
   mine *= ips;
   int64_t incl = mine;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(~0u, incl, o);
     if (lane >= o) incl += v;
@@ -190,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const Kv4Att
   if (lane == 31) sh.scan[warp] = incl;
   __syncthreads();
   int64_t total = 0, before = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += sh.scan[w];
     total += sh.scan[w];
@@ -198,41 +247,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const Kv4Att
   incl += before;
 
   // ---- sequences without a token
+#pragma unroll 1
   for (int64_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
     if (len_of(b) > 0) continue;
-    const int64_t n = p.Lq * p.group * p.heads * (D / 8);  // 16-byte words
-    for (int64_t i = tid; i < n; i += kThreads) {
-      const int64_t row = i / (p.group * p.heads * (D / 8)), c = i % (p.group * p.heads * (D / 8));
-      *reinterpret_cast<uint4*>(p.O + b * p.strideO + row * p.ldo + c * 8) = make_uint4(0, 0, 0, 0);
-    }
+    const int64_t words = static_cast<int64_t>(p.group) * p.heads * (D / 8);  // of 16 bytes, a query
+#pragma unroll 1
+    for (int64_t i = tid; i < p.Lq * words; i += kThreads)
+      *reinterpret_cast<uint4*>(p.O + b * p.strideO + i / words * p.ldo + i % words * 8) = make_uint4(0, 0, 0, 0);
   }
   int64_t ctas = (total + kMinUnits - 1) / kMinUnits;
   if (ctas > gridDim.x) ctas = gridDim.x;
   if (blockIdx.x >= ctas) return;  // whole CTAs
-  const int64_t r0 = start_of(blockIdx.x, total, ctas), r1 = start_of(blockIdx.x + 1, total, ctas);
+  const int64_t workers = ctas * kWarps;
+  const int64_t c0 = start_of(static_cast<int64_t>(blockIdx.x) * kWarps, total, workers);
 
-  if (r0 >= incl - mine && r0 < incl) {
+  if (c0 >= incl - mine && c0 < incl) {
     int64_t at = incl - mine, b = b_lo;
+#pragma unroll 1
     for (;; ++b) {
       const int64_t n = static_cast<int64_t>((len_of(b) + kUnit - 1) / kUnit) * ips;
-      if (r0 < at + n) break;
+      if (c0 < at + n) break;
       at += n;
     }
     sh.start_b = b;
-    sh.start_off = r0 - at;
+    sh.start_off = c0 - at;
   }
   __syncthreads();
-  Walk seg;
-  seg.r = r0;
-  seg.b = sh.start_b;
-  seg.len = len_of(seg.b);
-  seg.units = (seg.len + kUnit - 1) / kUnit;
-  seg.item = static_cast<int32_t>(sh.start_off / seg.units);
-  seg.u = static_cast<int32_t>(sh.start_off - static_cast<int64_t>(seg.item) * seg.units);
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t r0 = start_of(me, total, workers), r1 = start_of(me + 1, total, workers);
 
-  auto move_to = [&](Walk& w, int64_t r) {  // r < r1
+  auto move_to = [&](Walk& w, int64_t r) {  // r < total
     int64_t d = r - w.r;
     w.r = r;
+#pragma unroll 1
     while (d >= w.units - w.u) {
       d -= w.units - w.u;
       w.u = 0;
@@ -248,405 +295,525 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_kernel(const Kv4Att
     w.u += static_cast<int32_t>(d);
   };
 
-  // ---- this warp's copies: units r0 + warp, + 8, ...; the page of the next one is asked for
-  // ahead of its turn
-  Walk ahead = seg;
-  bool more = r0 + warp < r1;
-  int nrec = 0, rec_in = 0;
-  int32_t page = -1;
-  auto prepare = [&]() {
-    const int key0 = ahead.u * kUnit;
-    nrec = (ahead.len - key0 + kKv4Tokens - 1) / kKv4Tokens;
-    nrec = nrec < kRecs ? nrec : kRecs;
-    if (lane < nrec) {
-      const uint32_t k = key0 + kKv4Tokens * lane, pi = k / static_cast<uint32_t>(p.page_size);
-      rec_in = static_cast<int>(k - pi * p.page_size) / kKv4Tokens;
-      page = p.table[ahead.b * p.ldt + pi];
-    }
-  };
-  if (more) {
-    move_to(ahead, r0 + warp);
-    prepare();
-  }
-  uint32_t put = 0, got = 0;  // units asked for, units used
-  auto issue = [&]() {
-    const uint32_t s = put % C::kStages;
-    const uint32_t bar = smem_u32(&sh.full[warp * 4 + s]);
-    const bool in = lane < nrec, ok = in && page >= 0 && page < p.pages;
-    if (in && !ok) atomicCAS(p.index_word, 0u, kDevBadIndex);
-    const uint32_t mask = __ballot_sync(~0u, ok);
-    if (lane == 0) {
-      sh.mask[warp * 4 + s] = mask;
-      mbar_arrive_expect_tx(bar, __popc(mask) * C::kRec);
-    }
-    __syncwarp();
-    if (ok) {
-      const uint8_t* src = p.data + ((static_cast<int64_t>(page) * p.heads + ahead.item / qblocks) *
-                                         (p.page_size / kKv4Tokens) + rec_in) * C::kRec;
-      bulk_load(ring + s * C::kUnitBytes + lane * C::kRec, src, C::kRec, bar);
-    }
-    ++put;
-    more = ahead.r + kWarps < r1;
-    if (more) {
-      move_to(ahead, ahead.r + kWarps);
-      prepare();
-    }
-  };
-  for (int s = 0; s < C::kStages; ++s)
-    if (more) issue();
+  if (r0 < r1) {
+    Walk seg;
+    seg.r = c0;
+    seg.b = sh.start_b;
+    seg.len = len_of(seg.b);
+    seg.units = (seg.len + kUnit - 1) / kUnit;
+    seg.item = static_cast<int32_t>(sh.start_off / seg.units);
+    seg.u = static_cast<int32_t>(sh.start_off - static_cast<int64_t>(seg.item) * seg.units);
+    move_to(seg, r0);
 
-  // ---- segments: this CTA's piece of one item after the other
-  for (;;) {
-    const int64_t left = r1 - seg.r;
-    const int32_t n = seg.units - seg.u < left ? seg.units - seg.u : static_cast<int32_t>(left);
-    const int head = seg.item / qblocks;
-    const int row0 = (seg.item - head * qblocks) * C::kRows;
-    const uint16_t* qbase = p.Q + seg.b * p.strideQ + static_cast<int64_t>(head) * p.group * D;
-
-    // Q fragments: lane (g, t) takes query row g's elements [t d/4, + d/4).
-    uint32_t qf[NT <= 2 ? NT : 1][KS][2];
-    float qsum[NT][2];
-    int lim[NT][2];  // last key that a column's query sees
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + nt * 8 + g;
-      uint4 w[W];
-#pragma unroll
-      for (int j = 0; j < W; ++j) w[j] = make_uint4(0, 0, 0, 0);
-      if (row < rows_all) {
-        const uint4* src = reinterpret_cast<const uint4*>(qbase + static_cast<int64_t>(row / p.group) * p.ldq +
-                                                          (row % p.group) * D + t * (D / 4));
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j] = __ldg(src + j);
+    // ---- copies: the page of the next unit's records is asked for ahead of its turn
+    Walk ahead = seg;
+    int nrec = 0;
+    uint32_t rec_in = 0;
+    int32_t page = -1;
+    auto prepare = [&]() {
+      const int key0 = ahead.u * kUnit;
+      nrec = (ahead.len - key0 + kKv4Tokens - 1) / kKv4Tokens;
+      nrec = nrec < kRecs ? nrec : kRecs;
+      if (lane < nrec) {
+        // Records are whole: the page of record n is n / (page_size / 16), by multiplication.
+        const uint32_t n = static_cast<uint32_t>(key0) / kKv4Tokens + lane;
+        const uint32_t pi = p.page_magic ? __umulhi(n, p.page_magic) : n;
+        rec_in = n - pi * static_cast<uint32_t>(p.page_size / kKv4Tokens);
+        page = p.table[ahead.b * p.ldt + pi];
       }
-      float sum = 0.f;
+    };
+    prepare();
+    bool more = true;
+    uint32_t put = 0, got = 0;  // stages asked for and used: the slot, and its phase in bit 8
+    auto step = [&](uint32_t x) { return (x & 255u) + 1 == C::kStages ? (x & 256u) ^ 256u : x + 1; };
+    auto issue = [&]() {
+      const uint32_t s = put & 255u;
+      const uint32_t bar = smem_u32(&sh.full[warp * 4 + s]);
+      const bool in = lane < nrec, ok = in && page >= 0 && page < p.pages;
+      if (in && !ok) atomicCAS(p.index_word, 0u, kDevBadIndex);
+      const uint32_t mask = __ballot_sync(~0u, ok);
+      if (lane == 0) {
+        sh.mask[warp * 4 + s] = mask;
+        mbar_arrive_expect_tx(bar, __popc(mask) * C::kRec);
+      }
+      __syncwarp();
+      if (ok) {
+        const uint8_t* src = p.data + ((static_cast<int64_t>(page) * p.heads + ahead.item / qblocks) *
+                                           (p.page_size / kKv4Tokens) + rec_in) * C::kRec;
+        bulk_load(ring + s * C::kUnitBytes + lane * C::kRec, src, C::kRec, bar);
+      }
+      put = step(put);
+      more = ahead.r + 1 < r1;
+      if (more) {
+        move_to(ahead, ahead.r + 1);
+        prepare();
+      }
+    };
+#pragma unroll 1
+    for (int s = 0; s < C::kStages; ++s)
+      if (more) issue();
+
+    // ---- segments: this warp's piece of one item after the other
+#pragma unroll 1
+    for (;;) {
+      const int64_t left = r1 - seg.r;
+      const int32_t n = seg.units - seg.u < left ? seg.units - seg.u : static_cast<int32_t>(left);
+      const int head = seg.item / qblocks;
+      const int row0 = (seg.item - head * qblocks) * C::kRows;
+      const uint16_t* qbase = p.Q + seg.b * p.strideQ + static_cast<int64_t>(head) * p.group * D;
+
+      // Q fragments: lane (g, t) takes query row g's elements [t d/4, + d/4).
+      uint32_t qf[NT <= 2 ? NT : 1][KS][2];
+      float qsum[NT][2];
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        uint32_t f[4] = {__byte_perm(w[j].x, w[j].z, 0x5410), __byte_perm(w[j].x, w[j].z, 0x7632),
-                         __byte_perm(w[j].y, w[j].w, 0x5410), __byte_perm(w[j].y, w[j].w, 0x7632)};
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = row0 + nt * 8 + g;
+        uint4 w[W];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += lo_of(f[i]) + hi_of(f[i]);
-        if constexpr (NT <= 2) {
-          qf[nt][2 * j][0] = f[0];
-          qf[nt][2 * j][1] = f[1];
-          qf[nt][2 * j + 1][0] = f[2];
-          qf[nt][2 * j + 1][1] = f[3];
-        } else if (warp == nt) {
-          // One warp writes each tile; read by all after the barrier below.
-          const uint32_t a = qfrag + ((nt * KS + 2 * j) * 32 + lane) * 8;
-          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a), "r"(f[0]), "r"(f[1]) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a + 256), "r"(f[2]), "r"(f[3]) : "memory");
+        for (int j = 0; j < W; ++j) w[j] = make_uint4(0, 0, 0, 0);
+        if (row < rows_all) {
+          const uint4* src = reinterpret_cast<const uint4*>(qbase + static_cast<int64_t>(row / p.group) * p.ldq +
+                                                            (row % p.group) * D + t * (D / 4));
+#pragma unroll
+          for (int j = 0; j < W; ++j) w[j] = __ldg(src + j);
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const uint32_t f[4] = {__byte_perm(w[j].x, w[j].z, 0x5410), __byte_perm(w[j].x, w[j].z, 0x7632),
+                                 __byte_perm(w[j].y, w[j].w, 0x5410), __byte_perm(w[j].y, w[j].w, 0x7632)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum += lo_of(f[i]) + hi_of(f[i]);
+          if constexpr (NT <= 2) {
+            qf[nt][2 * j][0] = f[0];
+            qf[nt][2 * j][1] = f[1];
+            qf[nt][2 * j + 1][0] = f[2];
+            qf[nt][2 * j + 1][1] = f[3];
+          } else {  // read back by the same lane only
+            const uint32_t a = qfrag + ((nt * KS + 2 * j) * 32 + lane) * 8;
+            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a), "r"(f[0]), "r"(f[1]) : "memory");
+            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a + 256), "r"(f[2]), "r"(f[3]) : "memory");
+          }
+        }
+        sum += __shfl_xor_sync(~0u, sum, 1);
+        sum += __shfl_xor_sync(~0u, sum, 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) qsum[nt][e] = __shfl_sync(~0u, sum, (2 * t + e) * 4);
+      }
+
+      float o[NT][MT][4], m[NT][2], l[NT][2], z[NT][2];
+      float ps[NT][4];  // column sums of the rounded P, by a product with ones
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m[nt][e] = -INFINITY;
+          l[nt][e] = z[nt][e] = 0.f;
+          ps[nt][e] = ps[nt][2 + e] = 0.f;
         }
       }
-      sum += __shfl_xor_sync(~0u, sum, 1);
-      sum += __shfl_xor_sync(~0u, sum, 2);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        qsum[nt][e] = __shfl_sync(~0u, sum, (2 * t + e) * 4);
-        lim[nt][e] = seg.len - static_cast<int>(p.Lq) + (row0 + nt * 8 + 2 * t + e) / p.group;
-      }
-    }
-    if constexpr (NT == 4) __syncthreads();
 
-    float o[NT][MT][4], m[NT][2], l[NT][2], z[NT][2];
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const uint32_t slot = got & 255u;
+        mbar_wait(smem_u32(&sh.full[warp * 4 + slot]), got >> 8, &sh.abort, p.status, kDevTimeoutMma);
+        const uint32_t mask = sh.mask[warp * 4 + slot];
+#pragma unroll 1
+        for (int h = 0; h < kUnit / C::kStep; ++h) {
+          const uint32_t st = ring + slot * C::kUnitBytes + h * RS * C::kRec;
+          const int key0 = (seg.u + j) * kUnit + h * C::kStep;
+          const uint32_t have = mask >> (h * RS);
+          const bool whole = (have & ((1u << RS) - 1)) == (1u << RS) - 1 &&
+                             key0 + C::kStep <= seg.len - static_cast<int>(p.Lq) + 1;
+          // ---- S = K Q^T
+          float sc[RS][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+          for (int r = 0; r < RS; ++r) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+              for (int e = 0; e < 4; ++e) sc[r][nt][e] = 0.f;
+            uint32_t ka[W], kb[W];
+            lds(st + r * C::kRec + g * (D / 2) + t * (D / 8), ka);
+            lds(st + r * C::kRec + (g + 8) * (D / 2) + t * (D / 8), kb);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[nt][e] = -INFINITY;
-        l[nt][e] = z[nt][e] = 0.f;
-      }
-    }
-
-    // First unit of this segment that is this warp's.
-    const int skip = static_cast<int>((warp - (seg.r - r0)) & (kWarps - 1));
-    for (int j = skip; j < n; j += kWarps) {
-      const uint32_t s = got % C::kStages, ph = (got / C::kStages) & 1u;
-      mbar_wait(smem_u32(&sh.full[warp * 4 + s]), ph, &sh.abort, p.status, kDevTimeoutMma);
-      const uint32_t st = ring + s * C::kUnitBytes;
-      const uint32_t mask = sh.mask[warp * 4 + s];
-      const int key0 = (seg.u + j) * kUnit;
-
-      // ---- S = K Q^T over the unit's 64 keys
-      float sc[kRecs][NT][4];
+            for (int w = 0; w < W; ++w) {
+              const uint32_t a[4] = {expand<0>(ka[w]), expand<1>(ka[w]), expand<2>(ka[w]), expand<3>(ka[w])};
+              const uint32_t b[4] = {expand<0>(kb[w]), expand<1>(kb[w]), expand<2>(kb[w]), expand<3>(kb[w])};
 #pragma unroll
-      for (int r = 0; r < kRecs; ++r) {
+              for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                  uint32_t q0, q1;
+                  if constexpr (NT <= 2) {
+                    q0 = qf[nt][2 * w + i][0];
+                    q1 = qf[nt][2 * w + i][1];
+                  } else {
+                    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                                 : "=r"(q0), "=r"(q1)
+                                 : "r"(qfrag + ((nt * KS + 2 * w + i) * 32 + lane) * 8));
+                  }
+                  mma_bf16(sc[r][nt], a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], q0, q1);
+                }
+            }
+          }
+          // ---- scores in log2 units
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[r][nt][e] = 0.f;
-        uint32_t ka[W], kb[W];
-        lds(st + r * C::kRec + g * (D / 2) + t * (D / 8), ka);
-        lds(st + r * C::kRec + (g + 8) * (D / 2) + t * (D / 8), kb);
+          for (int r = 0; r < RS; ++r) {
+            const uint32_t pa = lds1(st + r * C::kRec + 16 * D + g * 4), pb = lds1(st + r * C::kRec + 16 * D + (g + 8) * 4);
+            const float s0 = lo_of(pa), s1 = lo_of(pb);
+            const float m0 = s0 * p.c_log2, m1 = s1 * p.c_log2;
+            const float a0 = fmaf(-128.f, s0, hi_of(pa)) * p.c_log2, a1 = fmaf(-128.f, s1, hi_of(pb)) * p.c_log2;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const uint32_t a[4] = {expand<0>(ka[w]), expand<1>(ka[w]), expand<2>(ka[w]), expand<3>(ka[w])};
-          const uint32_t b[4] = {expand<0>(kb[w]), expand<1>(kb[w]), expand<2>(kb[w]), expand<3>(kb[w])};
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+              for (int e = 0; e < 2; ++e) {
+                sc[r][nt][e] = fmaf(sc[r][nt][e], m0, a0 * qsum[nt][e]);
+                sc[r][nt][2 + e] = fmaf(sc[r][nt][2 + e], m1, a1 * qsum[nt][e]);
+              }
+          }
+          uint32_t vp[RS][2];
+#pragma unroll
+          for (int r = 0; r < RS; ++r) {
+            vp[r][0] = lds1(st + r * C::kRec + 16 * D + 64 + g * 4);
+            vp[r][1] = lds1(st + r * C::kRec + 16 * D + 64 + (g + 8) * 4);
+          }
+          if (!whole) {  // the last units, and pages outside the cache
+            asm volatile("" ::: "memory");  // a branch: few steps come here
+#pragma unroll
+            for (int r = 0; r < RS; ++r)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int k = key0 + r * kKv4Tokens + 8 * i + g;
+                const bool in = ((have >> r) & 1u) && k < seg.len;
+                if (!in) vp[r][i] = 0;  // a row that no query sees may hold anything
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int lim = seg.len - static_cast<int>(p.Lq) + (row0 + nt * 8 + 2 * t + e) / p.group;
+                    if (!in || k > lim) sc[r][nt][2 * i + e] = -INFINITY;
+                  }
+              }
+          }
+          // ---- running maximum (a column's keys lie across the lanes' g)
+          float use[NT][2];
+          bool grew = false;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float v = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
+#pragma unroll
+              for (int r = 1; r < RS; ++r) v = fmaxf(v, fmaxf(sc[r][nt][e], sc[r][nt][2 + e]));
+              v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+              grew |= v > m[nt][e];
+              use[nt][e] = fmaxf(m[nt][e], v);
+            }
+          if (__any_sync(~0u, grew)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // Nothing seen so far (-inf) has nothing to scale: the factor only must not be NaN.
+                const float f = m[nt][e] > -INFINITY ? ex2(m[nt][e] - use[nt][e]) : 0.f;
+                m[nt][e] = use[nt][e];
+                l[nt][e] *= f;
+                z[nt][e] *= f;
+                ps[nt][e] *= f;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                  o[nt][i][e] *= f;
+                  o[nt][i][2 + e] *= f;
+                }
+              }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) use[nt][e] = m[nt][e] > -INFINITY ? m[nt][e] : 0.f;
+          // ---- P, and O += V^T P^T record by record
+#pragma unroll
+          for (int r = 0; r < RS; ++r) {
+            const float s0 = lo_of(vp[r][0]), z0 = hi_of(vp[r][0]), s1 = lo_of(vp[r][1]), z1 = hi_of(vp[r][1]);
+            uint32_t b0[NT], b1[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              uint32_t q0, q1;
-              if constexpr (NT <= 2) {
-                q0 = qf[nt][2 * w + h][0];
-                q1 = qf[nt][2 * w + h][1];
-              } else {
-                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
-                             : "=r"(q0), "=r"(q1)
-                             : "r"(qfrag + ((nt * KS + 2 * w + h) * 32 + lane) * 8));
-              }
-              mma_bf16(sc[r][nt], a[2 * h], b[2 * h], a[2 * h + 1], b[2 * h + 1], q0, q1);
+              float w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = ex2(sc[r][nt][e] - use[nt][e & 1]);
+              l[nt][0] += w[0] + w[2];
+              l[nt][1] += w[1] + w[3];
+              z[nt][0] = fmaf(w[0], z0, fmaf(w[2], z1, z[nt][0]));
+              z[nt][1] = fmaf(w[1], z0, fmaf(w[3], z1, z[nt][1]));
+              b0[nt] = transpose8x8(pack2(w[0] * s0, w[1] * s0));
+              b1[nt] = transpose8x8(pack2(w[2] * s1, w[3] * s1));
+              mma_bf16(ps[nt], kOnes, kOnes, kOnes, kOnes, b0[nt], b1[nt]);
             }
-        }
-      }
-      // ---- scores in log2 units, masked where the unit is not all visible
-      const bool whole = mask == (1u << kRecs) - 1 && key0 + kUnit <= seg.len - static_cast<int>(p.Lq) + 1;
-      float top[NT][2];
+            uint32_t va[W], vb[W];
+            lds(st + r * C::kRec + 8 * D + lane * (D / 8), va);
+            lds(st + r * C::kRec + 8 * D + (32 + lane) * (D / 8), vb);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+            for (int w = 0; w < W; ++w) {
+              const uint32_t a[4] = {expand<0>(va[w]), expand<1>(va[w]), expand<2>(va[w]), expand<3>(va[w])};
+              const uint32_t b[4] = {expand<0>(vb[w]), expand<1>(vb[w]), expand<2>(vb[w]), expand<3>(vb[w])};
 #pragma unroll
-      for (int r = 0; r < kRecs; ++r) {
-        const uint32_t pa = lds1(st + r * C::kRec + 16 * D + g * 4), pb = lds1(st + r * C::kRec + 16 * D + (g + 8) * 4);
-        const float s0 = lo_of(pa), s1 = lo_of(pb);
-        const float m0 = s0 * p.c_log2, m1 = s1 * p.c_log2;
-        const float a0 = fmaf(-128.f, s0, hi_of(pa)) * p.c_log2, a1 = fmaf(-128.f, s1, hi_of(pb)) * p.c_log2;
+              for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            sc[r][nt][e] = fmaf(sc[r][nt][e], m0, a0 * qsum[nt][e]);
-            sc[r][nt][2 + e] = fmaf(sc[r][nt][2 + e], m1, a1 * qsum[nt][e]);
-            if (!whole) {
-              const int k = key0 + r * kKv4Tokens + g;
-              if (!((mask >> r) & 1u) || k > lim[nt][e]) sc[r][nt][e] = -INFINITY;
-              if (!((mask >> r) & 1u) || k + 8 > lim[nt][e]) sc[r][nt][2 + e] = -INFINITY;
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_bf16(o[nt][2 * w + i], a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], b0[nt], b1[nt]);
             }
-            top[nt][e] = fmaxf(top[nt][e], fmaxf(sc[r][nt][e], sc[r][nt][2 + e]));
           }
+        }
+        __syncwarp();  // all lanes have read the stage
+        got = step(got);
+        if (more) issue();
       }
-      // ---- running maximum over the unit (columns' keys lie across the lanes' g)
-      float use[NT][2];
-      bool grew = false;
+
+      // ---- the segment's sums; a whole item is written, a part kept for the join
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float v = top[nt][e];
-          v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-          grew |= v > m[nt][e];
-          top[nt][e] = fmaxf(m[nt][e], v);
-          use[nt][e] = top[nt][e] > -INFINITY ? top[nt][e] : 0.f;
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) {
+            l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], x);
+            z[nt][e] += __shfl_xor_sync(~0u, z[nt][e], x);
+          }
+          z[nt][e] = fmaf(-128.f, ps[nt][e], z[nt][e]);
         }
-      if (__any_sync(~0u, grew)) {
+      const bool ends = seg.u + n == seg.units;
+      if (seg.u == 0 && ends) {
+        uint16_t* obase = p.O + seg.b * p.strideO + static_cast<int64_t>(head) * p.group * D + g * (D / 8);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float f = ex2(m[nt][e] - use[nt][e]);
-            l[nt][e] *= f;
-            z[nt][e] *= f;
-            m[nt][e] = top[nt][e];
+            const int row = row0 + nt * 8 + 2 * t + e;
+            const float inv = l[nt][e] > 0.f ? 1.f / l[nt][e] : 0.f;
+            uint32_t w[MT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              o[nt][i][e] *= f;
-              o[nt][i][2 + e] *= f;
+            for (int i = 0; i < MT; ++i)
+              w[i] = pack2((o[nt][i][e] + z[nt][e]) * inv, (o[nt][i][2 + e] + z[nt][e]) * inv);
+            if (row < rows_all) {
+              uint4* dst = reinterpret_cast<uint4*>(obase + static_cast<int64_t>(row / p.group) * p.ldo + row % p.group * D);
+#pragma unroll
+              for (int i = 0; i < MT / 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
             }
           }
-      }
-      // ---- P, and O += V^T P^T record by record
-#pragma unroll
-      for (int r = 0; r < kRecs; ++r) {
-        const uint32_t pa = lds1(st + r * C::kRec + 16 * D + 64 + g * 4);
-        const uint32_t pb = lds1(st + r * C::kRec + 16 * D + 64 + (g + 8) * 4);
-        float s0 = lo_of(pa), z0 = hi_of(pa), s1 = lo_of(pb), z1 = hi_of(pb);
-        if (!whole) {  // a row that no query sees may hold anything
-          const int k = key0 + r * kKv4Tokens + g;
-          const bool have = (mask >> r) & 1u;
-          if (!have || k >= seg.len) s0 = z0 = 0.f;
-          if (!have || k + 8 >= seg.len) s1 = z1 = 0.f;
+      } else {
+        // The piece that ends an item begun by another warp goes to the workspace, this warp's
+        // last piece to the ring's place, once every warp is done with its ring.
+        float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kCounterBytes) + me * C::kPart;
+        if (!ends) {
+          __syncwarp();
+          part = reinterpret_cast<float*>(smem + warp * C::kStages * C::kUnitBytes);
+          static_assert(C::kPart * 4 <= C::kStages * C::kUnitBytes, "a warp's part fits its own ring");
         }
-        uint32_t b0[NT], b1[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float w[4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2(sc[r][nt][e] - use[nt][e & 1]);
-          const uint32_t x0 = pack2(w[0] * s0, w[1] * s0), x1 = pack2(w[2] * s1, w[3] * s1);
-          l[nt][0] += w[0] + w[2];
-          l[nt][1] += w[1] + w[3];
-          z[nt][0] = fmaf(-128.f, lo_of(x0) + lo_of(x1), fmaf(w[0], z0, fmaf(w[2], z1, z[nt][0])));
-          z[nt][1] = fmaf(-128.f, hi_of(x0) + hi_of(x1), fmaf(w[1], z0, fmaf(w[3], z1, z[nt][1])));
-          b0[nt] = transpose8x8(x0);
-          b1[nt] = transpose8x8(x1);
-        }
-        uint32_t va[W], vb[W];
-        lds(st + r * C::kRec + 8 * D + lane * (D / 8), va);
-        lds(st + r * C::kRec + 8 * D + (32 + lane) * (D / 8), vb);
+          for (int e = 0; e < 2; ++e) {
+            const int row = nt * 8 + 2 * t + e;
+            float4* dst = reinterpret_cast<float4*>(part + row * D + g * (D / 8));
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const uint32_t a[4] = {expand<0>(va[w]), expand<1>(va[w]), expand<2>(va[w]), expand<3>(va[w])};
-          const uint32_t b[4] = {expand<0>(vb[w]), expand<1>(vb[w]), expand<2>(vb[w]), expand<3>(vb[w])};
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_bf16(o[nt][2 * w + h], a[2 * h], a[2 * h + 1], b[2 * h], b[2 * h + 1], b0[nt], b1[nt]);
+            for (int i = 0; i < MT / 2; ++i)
+              dst[i] = make_float4(o[nt][2 * i][e] + z[nt][e], o[nt][2 * i][2 + e] + z[nt][e],
+                                   o[nt][2 * i + 1][e] + z[nt][e], o[nt][2 * i + 1][2 + e] + z[nt][e]);
+            if (g == 0) {
+              part[C::kRows * D + row] = m[nt][e];
+              part[C::kRows * D + C::kRows + row] = l[nt][e];
+            }
+          }
+        if (lane == 0) {
+          Cut* cut = ends ? &sh.head[warp] : &sh.tail[warp];
+          cut->b = seg.b;
+          cut->first = seg.r - seg.u;
+          cut->item = seg.item;
+          cut->units = seg.units;
+          (ends ? sh.has_head[warp] : sh.has_tail[warp]) = 1;
         }
       }
-      __syncwarp();  // all lanes have read the stage
-      ++got;
-      if (more) issue();
+      if (seg.r + n >= r1) break;
+      move_to(seg, seg.r + n);
     }
+  }
+  __syncthreads();
 
-    // ---- join the warps: maxima and sums first, then the outputs in slices of 8 rows x 64
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], x);
-          z[nt][e] += __shfl_xor_sync(~0u, z[nt][e], x);
-        }
-        if (g == 0) {
-          sh.m[warp][nt * 8 + 2 * t + e] = m[nt][e];
-          sh.l[warp][nt * 8 + 2 * t + e] = l[nt][e];
-        }
-      }
-    __syncthreads();
-    const bool all = seg.u == 0 && n == seg.units;
-    const int64_t item0 = seg.r - seg.u;  // the item's first unit
-    float* part = static_cast<float*>(p.ws) + (2 * blockIdx.x + (r0 >= item0 ? 0 : 1)) * kPartFloats;
-    uint16_t* obase = p.O + seg.b * p.strideO + static_cast<int64_t>(head) * p.group * D;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float f[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = nt * 8 + 2 * t + e;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh.m[w][row]);
-        f[e] = m[nt][e] > -INFINITY ? ex2(m[nt][e] - mx) : 0.f;
-      }
-#pragma unroll
-      for (int sl = 0; sl < D / 64; ++sl) {
-        // Columns g d/8 + 2 i, + 1 of m tile i: slice sl holds the groups g with g d/8 / 64 == sl.
-        if (g / (64 / (D / 8)) == sl) {
-          float* dst = join + warp * 512 + (2 * t) * 64 + (g * (D / 8) - sl * 64);
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              *reinterpret_cast<float2*>(dst + e * 64 + 2 * i) =
-                  make_float2((o[nt][i][e] + z[nt][e]) * f[e], (o[nt][i][2 + e] + z[nt][e]) * f[e]);
-        }
-        __syncthreads();
-        const int q = tid >> 5, c = (tid & 31) * 2;
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 v = *reinterpret_cast<const float2*>(join + w * 512 + q * 64 + c);
-          sum.x += v.x;
-          sum.y += v.y;
-        }
-        const int row = nt * 8 + q;
-        if (row0 + row < rows_all) {
-          float mx = -INFINITY, tl = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh.m[w][row]);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w)
-            tl += sh.m[w][row] > -INFINITY ? sh.l[w][row] * ex2(sh.m[w][row] - mx) : 0.f;
-          if (all) {
-            const float inv = tl > 0.f ? 1.f / tl : 0.f;
-            *reinterpret_cast<uint32_t*>(obase + static_cast<int64_t>((row0 + row) / p.group) * p.ldo +
-                                         (row0 + row) % p.group * D + sl * 64 + c) = pack2(sum.x * inv, sum.y * inv);
-          } else {
-            __stcg(reinterpret_cast<float2*>(part + row * D + sl * 64 + c), sum);
-            if (sl == 0 && c == 0) {
-              __stcg(part + C::kRows * D + row, mx);
-              __stcg(part + C::kRows * D + C::kRows + row, tl);
-            }
+  // ---- join: the parts in the order of their units are head 0, tail 0, head 1, tail 1, ...; a
+  // tail and what follows it, up to the next head, are one item.  A warp takes one run of them.
+  const int64_t cta_r0 = c0, cta_r1 = start_of(static_cast<int64_t>(blockIdx.x + 1) * kWarps, total, workers);
+  auto head_part = [&](int w) {
+    return reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.ws) + kCounterBytes) +
+           (static_cast<int64_t>(blockIdx.x) * kWarps + w) * C::kPart;
+  };
+  auto tail_part = [&](int w) { return reinterpret_cast<const float*>(smem + w * C::kStages * C::kUnitBytes); };
+  float* cta_parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kCounterBytes) +
+                     static_cast<int64_t>(kMaxCtas) * kWarps * C::kPart;
+  auto place = [&](const Cut& cut, int row, int c) {  // output of a row of the item, column c
+    const int head = cut.item / qblocks, rr = (cut.item - head * qblocks) * C::kRows + row;
+    return p.O + cut.b * p.strideO + static_cast<int64_t>(rr / p.group) * p.ldo +
+           (static_cast<int64_t>(head) * p.group + rr % p.group) * D + c;
+  };
+  auto rows_of = [&](const Cut& cut) {
+    const int left = rows_all - cut.item % qblocks * C::kRows;
+    return left < C::kRows ? left : C::kRows;
+  };
+  // Joins tails [ft, lt] (ft < 0: none), then head eh (< 0: none).
+  auto join = [&](int ft, int lt, int eh) {
+    const Cut cut = ft >= 0 ? sh.tail[ft] : sh.head[eh];
+    const bool here = cut.first >= cta_r0 && cut.first + cut.units <= cta_r1;
+    const int slot = cut.first >= cta_r0 ? 1 : 0;  // 0: the item began in an earlier CTA
+    float* out = cta_parts + (2 * static_cast<int64_t>(blockIdx.x) + slot) * C::kPart;
+    const int rows = rows_of(cut);
+#pragma unroll 1
+    for (int i = lane; i < rows * (D / 4); i += 32) {
+      const int row = i / (D / 4), c = i % (D / 4) * 4;
+      Sum s;
+      if (ft >= 0)
+#pragma unroll 1
+        for (int v = ft; v <= lt; ++v)
+          if (sh.has_tail[v]) {
+            const float* q = tail_part(v);
+            s.add(q[C::kRows * D + row], q[C::kRows * D + C::kRows + row],
+                  *reinterpret_cast<const float4*>(q + row * D + c));
           }
+      if (eh >= 0) {
+        const float* q = head_part(eh);
+        s.add(__ldcg(q + C::kRows * D + row), __ldcg(q + C::kRows * D + C::kRows + row),
+              __ldcg(reinterpret_cast<const float4*>(q + row * D + c)));
+      }
+      if (here) {
+        *reinterpret_cast<uint2*>(place(cut, row, c)) = s.value();
+      } else {
+        __stcg(reinterpret_cast<float4*>(out + row * D + c), s.v);
+        if (c == 0) {
+          __stcg(out + C::kRows * D + row, s.m);
+          __stcg(out + C::kRows * D + C::kRows + row, s.l);
         }
-        __syncthreads();
       }
     }
-    if (!all) {
-      uint32_t* counter = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.ws) + kPartBytes) + seg.b * ips + seg.item;
-      const int64_t c0 = cta_of(item0, total, ctas), c1 = cta_of(item0 + seg.units - 1, total, ctas);
-      if (tid == 0) {
-        const bool last = take_ticket(counter) == static_cast<uint32_t>(c1 - c0);
-        if (last) *counter = 0;  // every contributor has its ticket: ready for the next call
-        sh.last = last;
+    if (here) return;
+    // A CTA is the first one of at most one item that goes on after it: its counter is that
+    // item's.  The lanes' stores come before the ticket (release, after the warp's barrier).
+    __syncwarp();
+    if (lane == 0) {
+      const int64_t k0 = worker_of(cut.first, total, workers) / kWarps;
+      const int64_t k1 = worker_of(cut.first + cut.units - 1, total, workers) / kWarps;
+      uint32_t* counter = static_cast<uint32_t*>(p.ws) + k0;
+      if (take_ticket(counter) == static_cast<uint32_t>(k1 - k0)) {
+        *counter = 0;  // every contributor has its ticket: ready for the next call
+        sh.fin[slot] = cut;
+        sh.last[slot] = 1;
+      }
+    }
+  };
+  int ft = -1, lt = -1, runs = 0;
+#pragma unroll 1
+  for (int w = 0; w <= kWarps; ++w) {
+    const bool head = w < kWarps && sh.has_head[w];
+    if (head || (w == kWarps && ft >= 0)) {
+      if (runs++ % kWarps == warp) join(ft, lt, head ? w : -1);
+      ft = -1;
+    }
+    if (w < kWarps && sh.has_tail[w]) {
+      if (ft < 0) ft = w;
+      lt = w;
+    }
+  }
+  __syncthreads();
+
+  // ---- items cut between CTAs whose last part was this CTA's: every thread takes an output of
+  // four columns, groups of threads the CTAs in turn
+#pragma unroll 1
+  for (int slot = 0; slot < 2; ++slot) {
+    if (!sh.last[slot]) continue;
+    const Cut cut = sh.fin[slot];
+    const int64_t k0 = worker_of(cut.first, total, workers) / kWarps;
+    const int64_t k1 = worker_of(cut.first + cut.units - 1, total, workers) / kWarps;
+    const int outs = rows_of(cut) * (D / 4);
+    const int groups = outs < kThreads ? kThreads / outs : 1;
+    float* mid = reinterpret_cast<float*>(smem);  // [thread][6]
+#pragma unroll 1
+    for (int i = tid; i < groups * outs; i += kThreads) {
+      const int grp = i / outs, at = i - grp * outs, row = at / (D / 4), c = at % (D / 4) * 4;
+      Sum s;
+#pragma unroll 1
+      for (int64_t k = k0 + grp; k <= k1; k += 4 * groups) {
+        float mk[4], lk[4];
+        float4 v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int64_t kk = k + x * groups;
+          const float* q = cta_parts + (2 * kk + (kk == k0 ? 1 : 0)) * C::kPart;
+          const bool in = kk <= k1;
+          mk[x] = in ? __ldcg(q + C::kRows * D + row) : -INFINITY;
+          lk[x] = in ? __ldcg(q + C::kRows * D + C::kRows + row) : 0.f;
+          v[x] = in ? __ldcg(reinterpret_cast<const float4*>(q + row * D + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s.add(mk[x], lk[x], v[x]);
+      }
+      if (groups == 1) {
+        *reinterpret_cast<uint2*>(place(cut, row, c)) = s.value();
+      } else {
+        float* d = mid + tid * 6;
+        d[0] = s.m;
+        d[1] = s.l;
+        d[2] = s.v.x;
+        d[3] = s.v.y;
+        d[4] = s.v.z;
+        d[5] = s.v.w;
+      }
+    }
+    if (groups > 1) {  // uniform over the CTA
+      __syncthreads();
+      if (tid < outs) {
+        Sum s;
+        for (int x = 0; x < groups; ++x) {
+          const float* d = mid + (x * outs + tid) * 6;
+          s.add(d[0], d[1], make_float4(d[2], d[3], d[4], d[5]));
+        }
+        *reinterpret_cast<uint2*>(place(cut, tid / (D / 4), tid % (D / 4) * 4)) = s.value();
       }
       __syncthreads();
-      if (sh.last) {
-        const int rows = rows_all - row0 < C::kRows ? rows_all - row0 : C::kRows;
-        for (int i = tid; i < rows * (D / 4); i += kThreads) {
-          const int row = i / (D / 4), c = (i % (D / 4)) * 4;
-          auto part_of = [&](int64_t k) {
-            return static_cast<const float*>(p.ws) +
-                   (2 * k + (start_of(k, total, ctas) >= item0 ? 0 : 1)) * kPartFloats;
-          };
-          float mx = -INFINITY;
-#pragma unroll 8
-          for (int64_t k = c0; k <= c1; ++k) mx = fmaxf(mx, __ldcg(part_of(k) + C::kRows * D + row));
-          float tl = 0.f;
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int64_t k = c0; k <= c1; ++k) {
-            const float* src = part_of(k);
-            const float mk = __ldcg(src + C::kRows * D + row), lk = __ldcg(src + C::kRows * D + C::kRows + row);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + row * D + c));
-            const float f = mk > -INFINITY ? ex2(mk - mx) : 0.f;
-            tl = fmaf(lk, f, tl);
-            sum.x = fmaf(v.x, f, sum.x);
-            sum.y = fmaf(v.y, f, sum.y);
-            sum.z = fmaf(v.z, f, sum.z);
-            sum.w = fmaf(v.w, f, sum.w);
-          }
-          const float inv = tl > 0.f ? 1.f / tl : 0.f;
-          *reinterpret_cast<uint2*>(obase + static_cast<int64_t>((row0 + row) / p.group) * p.ldo +
-                                    (row0 + row) % p.group * D + c) =
-              make_uint2(pack2(sum.x * inv, sum.y * inv), pack2(sum.z * inv, sum.w * inv));
-        }
-      }
-      __syncthreads();  // sh.last is rewritten at the next segment's end
     }
-    if (seg.r + n >= r1) break;
-    move_to(seg, seg.r + n);
   }
 }
 
 template <int D, int NT>
 cudaError_t launch_variant(const Kv4AttnParams& p, int sms, cudaStream_t s) {
+  using C = Cfg<D, NT>;
   auto kern = kv4_attention_kernel<D, NT>;
   static std::atomic<uint64_t> attr_done{0};
-  const cudaError_t e = ensure_smem_attr(kern, Cfg<D, NT>::kSmem, attr_done);
+  const cudaError_t e = ensure_smem_attr(kern, C::kSmem, attr_done);
   if (e != cudaSuccess) return e;
   const int rows = static_cast<int>(p.Lq) * p.group;
-  const int qblocks = (rows + 8 * NT - 1) / (8 * NT);
-  return launch_pdl(kern, dim3(static_cast<unsigned>(sms < kMaxCtas ? sms : kMaxCtas)), dim3(kThreads),
-                    Cfg<D, NT>::kSmem, s, p, qblocks);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(sms < kMaxCtas ? sms : kMaxCtas)), dim3(C::kThreads), C::kSmem,
+                    s, p, (rows + C::kRows - 1) / C::kRows);
 }
 
 // Query rows of a block: the fewest tiles of 8 that hold them, at most 4.
 int tiles_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
+template <int D, int NT>
+constexpr int64_t ws_bytes() {
+  using C = Cfg<D, NT>;
+  return kCounterBytes + static_cast<int64_t>(kMaxCtas) * (C::kWarps + 2) * C::kPart * 4;
+}
+
 }  // namespace
 
-int64_t kv4_attention_ws_bytes(int64_t batch, int64_t Lq, int64_t heads_q, int64_t heads_kv, int d) {
-  (void)d;
-  const int64_t rows = Lq * (heads_q / heads_kv), per = 8 * tiles_of(rows);
-  return kPartBytes + batch * heads_kv * ((rows + per - 1) / per) * 4;
+int64_t kv4_attention_ws_bytes(int64_t Lq, int64_t heads_q, int64_t heads_kv, int d) {
+  const int nt = tiles_of(Lq * (heads_q / heads_kv));
+  if (d == 128) return nt == 1 ? ws_bytes<128, 1>() : nt == 2 ? ws_bytes<128, 2>() : ws_bytes<128, 4>();
+  return nt == 1 ? ws_bytes<64, 1>() : nt == 2 ? ws_bytes<64, 2>() : ws_bytes<64, 4>();
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) {

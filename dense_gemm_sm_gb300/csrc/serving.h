@@ -56,6 +56,7 @@ struct Kv4AttnParams {
   const uint8_t* data;
   int64_t pages;
   int32_t page_size, heads;         // heads: of the cache
+  uint32_t page_magic;              // n / (page_size / 16) = n * magic >> 32 for n < 2^24; 0: one record a page
   int64_t batch, Lq;
   int32_t group;                    // query heads per cache head
   float c_log2;                     // scale * log2(e)
@@ -67,7 +68,7 @@ struct Kv4AttnParams {
   uint32_t* status;
   uint32_t* index_word;
 };
-int64_t kv4_attention_ws_bytes(int64_t batch, int64_t Lq, int64_t heads_q, int64_t heads_kv, int d);
+int64_t kv4_attention_ws_bytes(int64_t Lq, int64_t heads_q, int64_t heads_kv, int d);
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------------ mixture of experts

@@ -60,7 +60,7 @@ dg_status check_cache(const dg_kv4_cache* c) {
   if (!c || c->pages < 0 || c->page_size <= 0 || c->heads <= 0 || c->d <= 0) return DG_ERR_INVALID_ARG;
   if (c->page_size % kKv4Tokens != 0) return DG_ERR_INVALID_ARG;
   if (c->d != 64 && c->d != 128) return DG_ERR_UNSUPPORTED;
-  if (c->page_size > 65536 || c->heads > 65536 || c->pages > INT32_MAX) return DG_ERR_UNSUPPORTED;
+  if (c->page_size > 4096 || c->heads > 65536 || c->pages > INT32_MAX) return DG_ERR_UNSUPPORTED;
   if (c->pages > 0 && !c->data) return DG_ERR_INVALID_ARG;
   if (!aligned(c->data, 16)) return DG_ERR_MISALIGNED;
   return DG_OK;
@@ -135,7 +135,7 @@ dg_status kv4_gather(const dg_kv4_cache* cache, int64_t tokens, const int64_t* s
 int64_t dg_attention_kv4_workspace_bytes(int64_t batch, int64_t Lq, int64_t heads_q, int64_t heads_kv, int32_t d) {
   if (batch <= 0 || Lq <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv != 0 || (d != 64 && d != 128))
     return 0;
-  return kv4_attention_ws_bytes(batch, Lq, heads_q, heads_kv, d);
+  return kv4_attention_ws_bytes(Lq, heads_q, heads_kv, d);
 }
 
 dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, int64_t heads_q, float scale,
@@ -154,10 +154,10 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
   if ((Lq > 1 && (ldq < width || ldo < width)) ||
       (batch > 1 && (strideQ < (Lq - 1) * ldq + width || strideO < (Lq - 1) * ldo + width)))
     return DG_ERR_INVALID_ARG;
-  const int64_t need = kv4_attention_ws_bytes(batch, Lq, heads_q, cache->heads, d);
+  const int64_t need = kv4_attention_ws_bytes(Lq, heads_q, cache->heads, d);
   if (!workspace || workspace_bytes < need) return DG_ERR_INVALID_ARG;
   if (heads_q > 65536 || Lq > 65536 || batch > 65536 || batch * Lq * heads_q > INT32_MAX ||
-      ldt * cache->page_size > INT32_MAX)
+      ldt > (int64_t(1) << 28) / cache->page_size)
     return DG_ERR_UNSUPPORTED;
   if (!aligned(Q, 16) || !aligned(O, 16) || ldq % 8 || ldo % 8 || strideQ % 8 || strideO % 8 ||
       !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(workspace, 256))
@@ -167,6 +167,10 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
   if (serving_device(&status, &sms) != cudaSuccess) return DG_ERR_CUDA;
   Kv4AttnParams p;
   p.data = cache->data; p.pages = cache->pages; p.page_size = cache->page_size; p.heads = cache->heads;
+  // floor(2^32 / d) + 1 divides exactly while n * d < 2^32: n < 2^24 records, d <= 256.
+  p.page_magic = cache->page_size == kKv4Tokens
+                     ? 0
+                     : static_cast<uint32_t>((int64_t(1) << 32) / (cache->page_size / kKv4Tokens) + 1);
   p.batch = batch; p.Lq = Lq;
   p.group = static_cast<int32_t>(heads_q / cache->heads);
   p.c_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);  // log2(e)

@@ -313,7 +313,8 @@ dg_status rmsnorm_residual_e4m3(int64_t rows, int64_t cols, const void* X, int64
  *     16 words, 16 words    K's and V's scale (low half) and zero (high half)
  * so that one copy brings a whole record, and V's codes lie as the tensor-core operand wants
  * them.  Token t of a page is slot page * page_size + t.  What unused slots hold is never
- * interpreted.  page_size is a multiple of 16; d is 64 or 128; data 16-byte aligned.
+ * interpreted.  page_size is a multiple of 16, at most 4096; d is 64 or 128; data
+ * 16-byte aligned.
  */
 typedef struct {
   uint8_t* data;
@@ -330,7 +331,7 @@ int64_t dg_kv4_block_bytes(int32_t page_size, int32_t d);
  * cache is passed over and reported (DG_ERR_BAD_INDEX from dg_device_status).  Slots of one
  * call are distinct.
  * Errors: null pointers, short strides, a page size that is not a positive multiple of 16
- * DG_ERR_INVALID_ARG; another d DG_ERR_UNSUPPORTED; data not 16-byte, slots not 8-byte or K
+ * DG_ERR_INVALID_ARG; another d or a larger page DG_ERR_UNSUPPORTED; data not 16-byte, slots not 8-byte or K
  * or V not 2-byte aligned DG_ERR_MISALIGNED.  tokens == 0: nothing.
  */
 dg_status kv4_append(const dg_kv4_cache* cache, int64_t tokens, const uint16_t* K, int64_t ldk,
@@ -360,8 +361,8 @@ dg_status kv4_gather(const dg_kv4_cache* cache, int64_t tokens, const int64_t* s
  *   - workspace: see above; dg_attention_kv4_workspace_bytes (0 for sizes it does not take).
  *   - Errors: heads_q not a multiple of the cache's heads, null pointers, overlapping strides,
  *     a scale that is not finite and positive, a workspace that is too small
- *     DG_ERR_INVALID_ARG; sizes over 65536 (batch, Lq, heads_q), batch * Lq * heads_q or ldt *
- *     page_size over 2^31 - 1 DG_ERR_UNSUPPORTED; Q or O not 16-byte or workspace not 256-byte
+ *     DG_ERR_INVALID_ARG; sizes over 65536 (batch, Lq, heads_q), batch * Lq * heads_q over
+ *     2^31 - 1 or ldt * page_size over 2^28 DG_ERR_UNSUPPORTED; Q or O not 16-byte or workspace not 256-byte
  *     aligned, ld or strides not multiples of 8 DG_ERR_MISALIGNED.  batch, Lq or heads_q == 0:
  *     nothing.
  */
