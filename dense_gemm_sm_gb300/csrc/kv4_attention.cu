@@ -43,18 +43,21 @@ namespace {
 constexpr int kMaxCtas = 160;   // CTAs that the workspace has room for
 // A CTA is given at least this many units, so that small calls use fewer CTAs and joins.
 constexpr int kMinUnits = 4;
+// The reference that weights are taken against (2^(score - reference)) follows the running
+// maximum only when that has outgrown it by this much: weights stay below 2^8, which FP32 sums
+// and BF16's exponent carry as well as weights below 1, and most steps scale nothing.
+constexpr float kSlack = 8.f;
 constexpr int64_t kCounterBytes = 1024;  // one ticket counter per CTA, then the parts
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kUnit = NT == 4 ? 32 : 64;               // keys of a unit
-  static constexpr int kStep = 32;                              // keys of a softmax step
+  static constexpr int kUnit = 32;                              // keys of a unit
   static constexpr int kRecs = kUnit / kKv4Tokens;
   static constexpr int kRec = kv4_record_bytes(D);
   static constexpr int kUnitBytes = kRecs * kRec;
-  static constexpr int kWarps = NT == 1 ? 12 : 8;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kStages = NT == 4 ? 4 : (D == 64 || NT == 2 ? 3 : 2);
+  static constexpr int kWarps = NT == 1 ? 15 : 7;               // that compute; one more issues the copies
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kStages = NT == 1 && D == 128 ? 3 : 4;
   static constexpr int kRing = kWarps * kStages * kUnitBytes;
   static constexpr int kRows = 8 * NT;
   static constexpr int kPart = kRows * (D + 2);                 // floats of a part: outputs, maxima, sums
@@ -83,11 +86,23 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-// Codes n of the pair of halves' n-th nibbles -> BF16 pair 128 + code.
-template <int N>
-__device__ __forceinline__ uint32_t expand(uint32_t w) {
-  return ((w >> (4 * N)) & 0x000F000Fu) | 0x43004300u;
-}
+// Codes n of the pair of halves' n-th nibbles -> BF16 pair 128 + code.  Mask and offset come in
+// registers: as two constants the AND and the OR are two instructions, and the logic pipe, which
+// takes one every other cycle, is what the kernel runs into (8 x 66k tokens: 921 instructions of
+// a 64-key unit on it, 541 of them these).
+struct Magic {
+  uint32_t mask, offset;
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask));
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(offset));
+  }
+  template <int N>
+  __device__ __forceinline__ uint32_t expand(uint32_t w) const {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w >> (4 * N)), "r"(mask), "r"(offset));  // (a & b) | c
+    return d;
+  }
+};
 
 template <int WORDS>
 __device__ __forceinline__ void lds(uint32_t a, uint32_t (&w)[WORDS]) {
@@ -98,6 +113,18 @@ __device__ __forceinline__ void lds(uint32_t a, uint32_t (&w)[WORDS]) {
   } else {
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
   }
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ uint32_t lds1(uint32_t a) {
@@ -126,28 +153,27 @@ __device__ __forceinline__ uint32_t take_ticket(uint32_t* a) {
   return old;
 }
 
-// First unit of worker c, and the worker that has unit x; 32-bit where the products fit.
-constexpr int64_t kSmall = int64_t(1) << 20;  // units; workers <= 160 * 12
-__device__ __forceinline__ int64_t start_of(int64_t c, int64_t units, int64_t workers) {
-  if (units < kSmall) return static_cast<uint32_t>(c) * static_cast<uint32_t>(units) / static_cast<uint32_t>(workers);
-  return c * units / workers;
-}
-__device__ __forceinline__ int64_t worker_of(int64_t x, int64_t units, int64_t workers) {
-  if (units < kSmall)
-    return (static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(workers) - 1) / static_cast<uint32_t>(units);
-  return ((x + 1) * workers - 1) / units;
-}
+// Units cut evenly over workers, the first `rem` of them one unit longer.  Units and workers
+// fit 31 bits.
+struct Split {
+  uint32_t q, rem;
+  __device__ __forceinline__ Split(uint32_t units, uint32_t workers) : q(units / workers), rem(units - q * workers) {}
+  __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * q + (c < rem ? c : rem); }
+  __device__ __forceinline__ uint32_t worker(uint32_t x) const {  // that has unit x
+    const uint32_t long_units = rem * (q + 1);
+    return x < long_units ? x / (q + 1) : rem + (x - long_units) / q;
+  }
+};
 
 // Position in the row of all units: unit r is unit u of item `item` of sequence b.
 struct Walk {
-  int64_t r;
-  int64_t b;
+  uint32_t r, b;
   int32_t len, units, item, u;
 };
 
 // An item that a warp has a part of.
 struct Cut {
-  int64_t b, first;  // sequence, the item's first unit
+  uint32_t b, first;  // sequence, the item's first unit
   int32_t item, units;
 };
 
@@ -175,14 +201,14 @@ struct Sum {
 template <int D, int NT>
 struct Shared {
   static constexpr int kWarps = Cfg<D, NT>::kWarps;
-  uint64_t full[kWarps * 4];
+  uint64_t full[kWarps * 4], empty[kWarps * 4];
   uint32_t mask[kWarps * 4];   // records of the stage that were copied
-  int64_t scan[kWarps];
+  Walk start[kWarps];
   Cut head[kWarps], tail[kWarps];
   uint8_t has_head[kWarps], has_tail[kWarps];
   Cut fin[2];                  // items of other CTAs too, for which this CTA came last
   uint32_t last[2];
-  int64_t start_b, start_off;
+  int32_t runs, run_first[kWarps + 1], run_last[kWarps + 1], run_head[kWarps + 1];
   uint32_t abort;
 };
 
@@ -194,90 +220,73 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   constexpr int KS = D / 16;       // k steps of the first product
   constexpr int MT = D / 16;       // m tiles of the second
   constexpr int W = D / 32;        // words of a lane's share of a row
-  constexpr int RS = C::kStep / kKv4Tokens;  // records of a softmax step
   constexpr uint32_t kOnes = 0x3F803F80u;
+  const Magic magic;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared<D, NT> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kUnitBytes;
   const uint32_t qfrag = smem_u32(smem) + C::kRing + warp * C::kQ;
 
-  if (lane == 0)
-    for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&sh.full[warp * 4 + s]), 1);
+  if (lane == 0 && warp < kWarps)
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&sh.full[warp * 4 + s]), 1);
+      mbar_init(smem_u32(&sh.empty[warp * 4 + s]), 1);
+    }
   if (tid == 0) sh.abort = 0;
   if (tid < 2) sh.last[tid] = 0;
   if (tid < kWarps) sh.has_head[tid] = sh.has_tail[tid] = 0;
   fence_barrier_init();
+  __syncthreads();
   pdl_trigger();
   pdl_wait();
 
-  const int64_t cap = p.ldt * p.page_size;
-  auto len_of = [&](int64_t b) -> int32_t {
+  const int32_t cap = static_cast<int32_t>(p.ldt * p.page_size);
+  auto len_of = [&](uint32_t b) -> int32_t {
     const int32_t n = p.lens[b];
-    return n < 0 ? 0 : (n > cap ? static_cast<int32_t>(cap) : n);
+    return n < 0 ? 0 : (n > cap ? cap : n);
   };
   const int ips = p.heads * qblocks;  // items of a sequence
   const int rows_all = static_cast<int>(p.Lq) * p.group;
+  const uint32_t batch = static_cast<uint32_t>(p.batch);
 
-  // ---- every CTA adds up the units; a thread takes a run of sequences
-  const int64_t per = (p.batch + kThreads - 1) / kThreads;
-  const int64_t b_lo = tid * per, b_hi = b_lo + per < p.batch ? b_lo + per : p.batch;
-  int64_t mine = 0;
+  // ---- every warp adds up the units for itself; a lane takes a run of sequences
+  const uint32_t per = (batch + 31) / 32, b_lo = lane * per, b_hi = min(b_lo + per, batch);
+  uint32_t mine = 0;
 #pragma unroll 1
-  for (int64_t b = b_lo; b < b_hi; ++b) {
+  for (uint32_t b = b_lo; b < b_hi; ++b) {
     const int32_t n = p.lens[b];
     if (blockIdx.x == 0 && (n < 0 || n > cap)) atomicCAS(p.index_word, 0u, kDevBadIndex);
-    mine += (len_of(b) + kUnit - 1) / kUnit;
+    mine += static_cast<uint32_t>(min(max(n, 0), cap) + kUnit - 1) / kUnit;
   }
   mine *= ips;
-  int64_t incl = mine;
-#pragma unroll 1
+  uint32_t incl = mine;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(~0u, incl, o);
+    const uint32_t v = __shfl_up_sync(~0u, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) sh.scan[warp] = incl;
-  __syncthreads();
-  int64_t total = 0, before = 0;
-#pragma unroll 1
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sh.scan[w];
-    total += sh.scan[w];
-  }
-  incl += before;
+  const uint32_t total = __shfl_sync(~0u, incl, 31);
 
   // ---- sequences without a token
 #pragma unroll 1
-  for (int64_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
+  for (uint32_t b = blockIdx.x; b < batch; b += gridDim.x) {
     if (len_of(b) > 0) continue;
-    const int64_t words = static_cast<int64_t>(p.group) * p.heads * (D / 8);  // of 16 bytes, a query
+    const int words = p.group * p.heads * (D / 8);  // of 16 bytes, a query
 #pragma unroll 1
     for (int64_t i = tid; i < p.Lq * words; i += kThreads)
       *reinterpret_cast<uint4*>(p.O + b * p.strideO + i / words * p.ldo + i % words * 8) = make_uint4(0, 0, 0, 0);
   }
-  int64_t ctas = (total + kMinUnits - 1) / kMinUnits;
-  if (ctas > gridDim.x) ctas = gridDim.x;
+  const uint32_t ctas = min((total + kMinUnits - 1) / kMinUnits, gridDim.x);
   if (blockIdx.x >= ctas) return;  // whole CTAs
-  const int64_t workers = ctas * kWarps;
-  const int64_t c0 = start_of(static_cast<int64_t>(blockIdx.x) * kWarps, total, workers);
+  const Split split(total, ctas * kWarps);
+  // The units of this warp, and of the warp that a lane of the copying warp works for.
+  const bool copies = warp == kWarps;
+  const uint32_t me = blockIdx.x * kWarps + (copies ? min(lane, kWarps - 1) : warp);
+  const uint32_t r0 = split.start(me), r1 = split.start(me + 1);
 
-  if (c0 >= incl - mine && c0 < incl) {
-    int64_t at = incl - mine, b = b_lo;
-#pragma unroll 1
-    for (;; ++b) {
-      const int64_t n = static_cast<int64_t>((len_of(b) + kUnit - 1) / kUnit) * ips;
-      if (c0 < at + n) break;
-      at += n;
-    }
-    sh.start_b = b;
-    sh.start_off = c0 - at;
-  }
-  __syncthreads();
-  const int64_t me = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  const int64_t r0 = start_of(me, total, workers), r1 = start_of(me + 1, total, workers);
-
-  auto move_to = [&](Walk& w, int64_t r) {  // r < total
-    int64_t d = r - w.r;
+  auto move_to = [&](Walk& w, uint32_t r) {  // r < total
+    int32_t d = static_cast<int32_t>(r - w.r);
     w.r = r;
 #pragma unroll 1
     while (d >= w.units - w.u) {
@@ -292,75 +301,106 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         w.units = (w.len + kUnit - 1) / kUnit;
       }
     }
-    w.u += static_cast<int32_t>(d);
+    w.u += d;
   };
 
-  if (r0 < r1) {
-    Walk seg;
-    seg.r = c0;
-    seg.b = sh.start_b;
+  Walk seg;
+  if (!copies && r0 < r1) {
+    // The lane whose sequences hold unit r0 finds the sequence and what lies before it there.
+    const int owner = __ffs(__ballot_sync(~0u, r0 < incl)) - 1;
+    uint32_t at = incl - mine, b0 = b_lo;
+    if (lane == owner)
+#pragma unroll 1
+      for (;; ++b0) {
+        const uint32_t n = static_cast<uint32_t>((len_of(b0) + kUnit - 1) / kUnit) * ips;
+        if (r0 < at + n) break;
+        at += n;
+      }
+    seg.r = r0;
+    seg.b = __shfl_sync(~0u, b0, owner);
+    const uint32_t off = r0 - __shfl_sync(~0u, at, owner);
     seg.len = len_of(seg.b);
     seg.units = (seg.len + kUnit - 1) / kUnit;
-    seg.item = static_cast<int32_t>(sh.start_off / seg.units);
-    seg.u = static_cast<int32_t>(sh.start_off - static_cast<int64_t>(seg.item) * seg.units);
-    move_to(seg, r0);
+    seg.item = off / static_cast<uint32_t>(seg.units);
+    seg.u = off - seg.item * seg.units;
+    if (lane == 0) sh.start[warp] = seg;
+  }
+  __syncthreads();
 
-    // ---- copies: the page of the next unit's records is asked for ahead of its turn
-    Walk ahead = seg;
-    int nrec = 0;
-    uint32_t rec_in = 0;
-    int32_t page = -1;
-    auto prepare = [&]() {
-      const int key0 = ahead.u * kUnit;
-      nrec = (ahead.len - key0 + kKv4Tokens - 1) / kKv4Tokens;
-      nrec = nrec < kRecs ? nrec : kRecs;
-      if (lane < nrec) {
-        // Records are whole: the page of record n is n / (page_size / 16), by multiplication.
-        const uint32_t n = static_cast<uint32_t>(key0) / kKv4Tokens + lane;
-        const uint32_t pi = p.page_magic ? __umulhi(n, p.page_magic) : n;
-        rec_in = n - pi * static_cast<uint32_t>(p.page_size / kKv4Tokens);
-        page = p.table[ahead.b * p.ldt + pi];
-      }
-    };
-    prepare();
-    bool more = true;
-    uint32_t put = 0, got = 0;  // stages asked for and used: the slot, and its phase in bit 8
-    auto step = [&](uint32_t x) { return (x & 255u) + 1 == C::kStages ? (x & 256u) ^ 256u : x + 1; };
-    auto issue = [&]() {
-      const uint32_t s = put & 255u;
-      const uint32_t bar = smem_u32(&sh.full[warp * 4 + s]);
-      const bool in = lane < nrec, ok = in && page >= 0 && page < p.pages;
-      if (in && !ok) atomicCAS(p.index_word, 0u, kDevBadIndex);
-      const uint32_t mask = __ballot_sync(~0u, ok);
-      if (lane == 0) {
-        sh.mask[warp * 4 + s] = mask;
-        mbar_arrive_expect_tx(bar, __popc(mask) * C::kRec);
-      }
-      __syncwarp();
-      if (ok) {
-        const uint8_t* src = p.data + ((static_cast<int64_t>(page) * p.heads + ahead.item / qblocks) *
-                                           (p.page_size / kKv4Tokens) + rec_in) * C::kRec;
-        bulk_load(ring + s * C::kUnitBytes + lane * C::kRec, src, C::kRec, bar);
-      }
-      put = step(put);
-      more = ahead.r + 1 < r1;
-      if (more) {
-        move_to(ahead, ahead.r + 1);
-        prepare();
-      }
-    };
+  if (copies) {
+    // ---- a lane fills the ring of the warp of its number: the bookkeeping of all rings is done
+    // once for all of them, not in every computing warp (where it took a tenth of the time)
+    if (lane < kWarps && r0 < r1) {
+      Walk at = sh.start[lane];
+      const uint32_t to = smem_u32(smem) + lane * C::kStages * C::kUnitBytes;
+      const int32_t page_recs = p.page_size / kKv4Tokens;
+      int nrec;
+      uint32_t rec_in[kRecs];
+      int32_t page[kRecs];
+      auto look_up = [&]() {  // the pages of the next unit's records
+        const uint32_t n = static_cast<uint32_t>(at.u) * kRecs;
+        nrec = (at.len - at.u * kUnit + kKv4Tokens - 1) / kKv4Tokens;
+        nrec = nrec < kRecs ? nrec : kRecs;
+#pragma unroll
+        for (int i = 0; i < kRecs; ++i) {
+          // Records are whole: the page of record n is n / (page_size / 16), by multiplication.
+          const uint32_t pi = p.page_magic ? __umulhi(n + i, p.page_magic) : n + i;
+          rec_in[i] = n + i - pi * page_recs;
+          page[i] = i < nrec ? p.table[static_cast<int64_t>(at.b) * p.ldt + pi] : -1;
+        }
+      };
+      look_up();
+      uint32_t put = 0;  // slot, and its phase in bit 8
+      uint32_t fresh = C::kStages;  // slots never used
+      uint64_t since = 0;
 #pragma unroll 1
-    for (int s = 0; s < C::kStages; ++s)
-      if (more) issue();
-
+      for (;;) {
+        const uint32_t s = put & 255u;
+        if (fresh == 0 && !mbar_test(smem_u32(&sh.empty[lane * 4 + s]), (put >> 8) ^ 1u)) {
+          __nanosleep(40);
+          const uint64_t now = globaltimer_ns();
+          if (since == 0) since = now;
+          if (now - since > kWaitLimitNs || *static_cast<volatile uint32_t*>(&sh.abort)) {
+            sh.abort = 1;
+            atomicCAS(p.status, 0u, kDevTimeoutProducer);
+            break;
+          }
+          continue;
+        }
+        since = 0;
+        if (fresh) --fresh;
+        const uint32_t bar = smem_u32(&sh.full[lane * 4 + s]);
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < kRecs; ++i) {
+          if (page[i] >= 0 && page[i] < p.pages) mask |= 1u << i;
+          else if (i < nrec) atomicCAS(p.index_word, 0u, kDevBadIndex);
+        }
+        sh.mask[lane * 4 + s] = mask;
+        mbar_arrive_expect_tx(bar, __popc(mask) * C::kRec);
+        const int64_t head = at.item / qblocks;
+        // Pages of whole units: one copy; otherwise one a record.
+#pragma unroll
+        for (int i = 0; i < kRecs; ++i) {
+          if (!((mask >> i) & 1u) || (p.one_copy && i > 0)) continue;
+          const uint8_t* src = p.data + ((static_cast<int64_t>(page[i]) * p.heads + head) * page_recs + rec_in[i]) * C::kRec;
+          bulk_load(to + s * C::kUnitBytes + i * C::kRec, src, p.one_copy ? nrec * C::kRec : C::kRec, bar);
+        }
+        put = s + 1 == C::kStages ? (put & 256u) ^ 256u : put + 1;
+        if (at.r + 1 >= r1) break;
+        move_to(at, at.r + 1);
+        look_up();
+      }
+    }
+  } else if (r0 < r1) {
+    uint32_t got = 0;  // stage in use: the slot, and its phase in bit 8
     // ---- segments: this warp's piece of one item after the other
 #pragma unroll 1
     for (;;) {
-      const int64_t left = r1 - seg.r;
-      const int32_t n = seg.units - seg.u < left ? seg.units - seg.u : static_cast<int32_t>(left);
+      const int32_t n = min(seg.units - seg.u, static_cast<int32_t>(r1 - seg.r));
       const int head = seg.item / qblocks;
       const int row0 = (seg.item - head * qblocks) * C::kRows;
-      const uint16_t* qbase = p.Q + seg.b * p.strideQ + static_cast<int64_t>(head) * p.group * D;
+      const uint16_t* qbase = p.Q + static_cast<int64_t>(seg.b) * p.strideQ + static_cast<int64_t>(head) * p.group * D;
 
       // Q fragments: lane (g, t) takes query row g's elements [t d/4, + d/4).
       uint32_t qf[NT <= 2 ? NT : 1][KS][2];
@@ -421,18 +461,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       for (int j = 0; j < n; ++j) {
         const uint32_t slot = got & 255u;
         mbar_wait(smem_u32(&sh.full[warp * 4 + slot]), got >> 8, &sh.abort, p.status, kDevTimeoutMma);
-        const uint32_t mask = sh.mask[warp * 4 + slot];
-#pragma unroll 1
-        for (int h = 0; h < kUnit / C::kStep; ++h) {
-          const uint32_t st = ring + slot * C::kUnitBytes + h * RS * C::kRec;
-          const int key0 = (seg.u + j) * kUnit + h * C::kStep;
-          const uint32_t have = mask >> (h * RS);
-          const bool whole = (have & ((1u << RS) - 1)) == (1u << RS) - 1 &&
-                             key0 + C::kStep <= seg.len - static_cast<int>(p.Lq) + 1;
+        const uint32_t have = sh.mask[warp * 4 + slot];
+        {
+          const uint32_t st = ring + slot * C::kUnitBytes;
+          const int key0 = (seg.u + j) * kUnit;
+          const bool whole = have == (1u << kRecs) - 1 && key0 + kUnit <= seg.len - static_cast<int>(p.Lq) + 1;
           // ---- S = K Q^T
-          float sc[RS][NT][4];
+          float sc[kRecs][NT][4];
 #pragma unroll
-          for (int r = 0; r < RS; ++r) {
+          for (int r = 0; r < kRecs; ++r) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -442,8 +479,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             lds(st + r * C::kRec + (g + 8) * (D / 2) + t * (D / 8), kb);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-              const uint32_t a[4] = {expand<0>(ka[w]), expand<1>(ka[w]), expand<2>(ka[w]), expand<3>(ka[w])};
-              const uint32_t b[4] = {expand<0>(kb[w]), expand<1>(kb[w]), expand<2>(kb[w]), expand<3>(kb[w])};
+              const uint32_t a[4] = {magic.expand<0>(ka[w]), magic.expand<1>(ka[w]), magic.expand<2>(ka[w]), magic.expand<3>(ka[w])};
+              const uint32_t b[4] = {magic.expand<0>(kb[w]), magic.expand<1>(kb[w]), magic.expand<2>(kb[w]), magic.expand<3>(kb[w])};
 #pragma unroll
               for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -463,7 +500,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
           // ---- scores in log2 units
 #pragma unroll
-          for (int r = 0; r < RS; ++r) {
+          for (int r = 0; r < kRecs; ++r) {
             const uint32_t pa = lds1(st + r * C::kRec + 16 * D + g * 4), pb = lds1(st + r * C::kRec + 16 * D + (g + 8) * 4);
             const float s0 = lo_of(pa), s1 = lo_of(pb);
             const float m0 = s0 * p.c_log2, m1 = s1 * p.c_log2;
@@ -476,16 +513,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 sc[r][nt][2 + e] = fmaf(sc[r][nt][2 + e], m1, a1 * qsum[nt][e]);
               }
           }
-          uint32_t vp[RS][2];
+          uint32_t vp[kRecs][2];
 #pragma unroll
-          for (int r = 0; r < RS; ++r) {
+          for (int r = 0; r < kRecs; ++r) {
             vp[r][0] = lds1(st + r * C::kRec + 16 * D + 64 + g * 4);
             vp[r][1] = lds1(st + r * C::kRec + 16 * D + 64 + (g + 8) * 4);
           }
           if (!whole) {  // the last units, and pages outside the cache
             asm volatile("" ::: "memory");  // a branch: few steps come here
 #pragma unroll
-            for (int r = 0; r < RS; ++r)
+            for (int r = 0; r < kRecs; ++r)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const int k = key0 + r * kKv4Tokens + 8 * i + g;
@@ -509,11 +546,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             for (int e = 0; e < 2; ++e) {
               float v = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
 #pragma unroll
-              for (int r = 1; r < RS; ++r) v = fmaxf(v, fmaxf(sc[r][nt][e], sc[r][nt][2 + e]));
+              for (int r = 1; r < kRecs; ++r) v = fmaxf(v, fmaxf(sc[r][nt][e], sc[r][nt][2 + e]));
               v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
               v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
               v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-              grew |= v > m[nt][e];
+              grew |= v > m[nt][e] + kSlack;
               use[nt][e] = fmaxf(m[nt][e], v);
             }
           if (__any_sync(~0u, grew)) {
@@ -540,7 +577,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             for (int e = 0; e < 2; ++e) use[nt][e] = m[nt][e] > -INFINITY ? m[nt][e] : 0.f;
           // ---- P, and O += V^T P^T record by record
 #pragma unroll
-          for (int r = 0; r < RS; ++r) {
+          for (int r = 0; r < kRecs; ++r) {
             const float s0 = lo_of(vp[r][0]), z0 = hi_of(vp[r][0]), s1 = lo_of(vp[r][1]), z1 = hi_of(vp[r][1]);
             uint32_t b0[NT], b1[NT];
 #pragma unroll
@@ -561,8 +598,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             lds(st + r * C::kRec + 8 * D + (32 + lane) * (D / 8), vb);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-              const uint32_t a[4] = {expand<0>(va[w]), expand<1>(va[w]), expand<2>(va[w]), expand<3>(va[w])};
-              const uint32_t b[4] = {expand<0>(vb[w]), expand<1>(vb[w]), expand<2>(vb[w]), expand<3>(vb[w])};
+              const uint32_t a[4] = {magic.expand<0>(va[w]), magic.expand<1>(va[w]), magic.expand<2>(va[w]), magic.expand<3>(va[w])};
+              const uint32_t b[4] = {magic.expand<0>(vb[w]), magic.expand<1>(vb[w]), magic.expand<2>(vb[w]), magic.expand<3>(vb[w])};
 #pragma unroll
               for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -572,8 +609,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
         }
         __syncwarp();  // all lanes have read the stage
-        got = step(got);
-        if (more) issue();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[warp * 4 + slot]));
+        got = slot + 1 == C::kStages ? (got & 256u) ^ 256u : got + 1;
       }
 
       // ---- the segment's sums; a whole item is written, a part kept for the join
@@ -590,7 +627,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
       const bool ends = seg.u + n == seg.units;
       if (seg.u == 0 && ends) {
-        uint16_t* obase = p.O + seg.b * p.strideO + static_cast<int64_t>(head) * p.group * D + g * (D / 8);
+        uint16_t* obase = p.O + static_cast<int64_t>(seg.b) * p.strideO + static_cast<int64_t>(head) * p.group * D + g * (D / 8);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -608,10 +645,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             }
           }
       } else {
-        // The piece that ends an item begun by another warp goes to the workspace, this warp's
-        // last piece to the ring's place, once every warp is done with its ring.
-        float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kCounterBytes) + me * C::kPart;
-        if (!ends) {
+        // The warp's last piece takes its ring's place, an earlier one (which ends an item that
+        // another warp began) a place in the workspace.
+        float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kCounterBytes) +
+                      static_cast<int64_t>(me) * C::kPart;
+        if (seg.r + n == r1) {
           __syncwarp();
           part = reinterpret_cast<float*>(smem + warp * C::kStages * C::kUnitBytes);
           static_assert(C::kPart * 4 <= C::kStages * C::kUnitBytes, "a warp's part fits its own ring");
@@ -637,7 +675,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           cut->first = seg.r - seg.u;
           cut->item = seg.item;
           cut->units = seg.units;
-          (ends ? sh.has_head[warp] : sh.has_tail[warp]) = 1;
+          (ends ? sh.has_head[warp] : sh.has_tail[warp]) = seg.r + n == r1 ? 2 : 1;  // 2: in the ring's place
         }
       }
       if (seg.r + n >= r1) break;
@@ -647,84 +685,102 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   __syncthreads();
 
   // ---- join: the parts in the order of their units are head 0, tail 0, head 1, tail 1, ...; a
-  // tail and what follows it, up to the next head, are one item.  A warp takes one run of them.
-  const int64_t cta_r0 = c0, cta_r1 = start_of(static_cast<int64_t>(blockIdx.x + 1) * kWarps, total, workers);
-  auto head_part = [&](int w) {
-    return reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.ws) + kCounterBytes) +
-           (static_cast<int64_t>(blockIdx.x) * kWarps + w) * C::kPart;
-  };
+  // tail and what follows it, up to the next head, are one item: a run.
+  const uint32_t cta_r0 = split.start(blockIdx.x * kWarps), cta_r1 = split.start((blockIdx.x + 1) * kWarps);
   auto tail_part = [&](int w) { return reinterpret_cast<const float*>(smem + w * C::kStages * C::kUnitBytes); };
+  auto head_part = [&](int w) {
+    return sh.has_head[w] == 2 ? tail_part(w)
+                               : reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.ws) + kCounterBytes) +
+                                     (static_cast<int64_t>(blockIdx.x) * kWarps + w) * C::kPart;
+  };
   float* cta_parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kCounterBytes) +
                      static_cast<int64_t>(kMaxCtas) * kWarps * C::kPart;
   auto place = [&](const Cut& cut, int row, int c) {  // output of a row of the item, column c
     const int head = cut.item / qblocks, rr = (cut.item - head * qblocks) * C::kRows + row;
-    return p.O + cut.b * p.strideO + static_cast<int64_t>(rr / p.group) * p.ldo +
+    return p.O + static_cast<int64_t>(cut.b) * p.strideO + static_cast<int64_t>(rr / p.group) * p.ldo +
            (static_cast<int64_t>(head) * p.group + rr % p.group) * D + c;
   };
   auto rows_of = [&](const Cut& cut) {
     const int left = rows_all - cut.item % qblocks * C::kRows;
     return left < C::kRows ? left : C::kRows;
   };
-  // Joins tails [ft, lt] (ft < 0: none), then head eh (< 0: none).
-  auto join = [&](int ft, int lt, int eh) {
+  if (warp == 0) {
+    // Bit w: warp w has a tail, a head.  A run ends at a head, or (the last) after the last
+    // warp; it begins at the first tail after the end of the one before, or is a head alone.
+    const uint32_t tails = __ballot_sync(~0u, lane < kWarps && sh.has_tail[lane < kWarps ? lane : 0]);
+    const uint32_t heads = __ballot_sync(~0u, lane < kWarps && sh.has_head[lane < kWarps ? lane : 0]);
+    const uint32_t upto = (2u << lane) - 1;  // warps 0 .. lane
+    const bool is_head = (heads >> lane) & 1u;
+    // The previous head's own tail belongs to the run that follows it.
+    const uint32_t before = heads & (upto >> 1);
+    const uint32_t own = tails & ~(before ? (1u << (31 - __clz(before))) - 1 : 0u);
+    const uint32_t run_tails = own & (upto >> 1);
+    if (is_head) {
+      const int run = __popc(before);
+      sh.run_first[run] = run_tails ? __ffs(run_tails) - 1 : -1;
+      sh.run_last[run] = 31 - __clz(run_tails);
+      sh.run_head[run] = lane;
+    }
+    if (lane == kWarps) {  // what is left after the last head
+      const int run = __popc(heads);
+      sh.run_first[run] = own ? __ffs(own) - 1 : -1;
+      sh.run_last[run] = 31 - __clz(own);
+      sh.run_head[run] = -1;
+      sh.runs = run + (own ? 1 : 0);
+    }
+  }
+  __syncthreads();
+  const int outs_max = (rows_all < C::kRows ? rows_all : C::kRows) * (D / 4);
+#pragma unroll 1
+  for (int i = tid; i < sh.runs * outs_max; i += kThreads) {
+    const int run = i / outs_max, at = i - run * outs_max, row = at / (D / 4), c = at % (D / 4) * 4;
+    const int ft = sh.run_first[run], lt = sh.run_last[run], eh = sh.run_head[run];
     const Cut cut = ft >= 0 ? sh.tail[ft] : sh.head[eh];
-    const bool here = cut.first >= cta_r0 && cut.first + cut.units <= cta_r1;
-    const int slot = cut.first >= cta_r0 ? 1 : 0;  // 0: the item began in an earlier CTA
-    float* out = cta_parts + (2 * static_cast<int64_t>(blockIdx.x) + slot) * C::kPart;
-    const int rows = rows_of(cut);
+    if (row >= rows_of(cut)) continue;
+    Sum s;
+    if (ft >= 0)
 #pragma unroll 1
-    for (int i = lane; i < rows * (D / 4); i += 32) {
-      const int row = i / (D / 4), c = i % (D / 4) * 4;
-      Sum s;
-      if (ft >= 0)
-#pragma unroll 1
-        for (int v = ft; v <= lt; ++v)
-          if (sh.has_tail[v]) {
-            const float* q = tail_part(v);
-            s.add(q[C::kRows * D + row], q[C::kRows * D + C::kRows + row],
-                  *reinterpret_cast<const float4*>(q + row * D + c));
-          }
-      if (eh >= 0) {
-        const float* q = head_part(eh);
-        s.add(__ldcg(q + C::kRows * D + row), __ldcg(q + C::kRows * D + C::kRows + row),
-              __ldcg(reinterpret_cast<const float4*>(q + row * D + c)));
+      for (int v = ft; v <= lt; ++v)
+        if (sh.has_tail[v]) {
+          const float* q = tail_part(v);
+          s.add(q[C::kRows * D + row], q[C::kRows * D + C::kRows + row],
+                *reinterpret_cast<const float4*>(q + row * D + c));
+        }
+    if (eh >= 0) {
+      const float* q = head_part(eh);
+      // Either memory; stores of this CTA's own warps, ordered by its barrier.
+      s.add(q[C::kRows * D + row], q[C::kRows * D + C::kRows + row], *reinterpret_cast<const float4*>(q + row * D + c));
+    }
+    if (cut.first >= cta_r0 && cut.first + cut.units <= cta_r1) {
+      *reinterpret_cast<uint2*>(place(cut, row, c)) = s.value();
+    } else {
+      // Slot 0: the item began in an earlier CTA.
+      float* out = cta_parts + (2 * static_cast<int64_t>(blockIdx.x) + (cut.first >= cta_r0 ? 1 : 0)) * C::kPart;
+      __stcg(reinterpret_cast<float4*>(out + row * D + c), s.v);
+      if (c == 0) {
+        __stcg(out + C::kRows * D + row, s.m);
+        __stcg(out + C::kRows * D + C::kRows + row, s.l);
       }
-      if (here) {
-        *reinterpret_cast<uint2*>(place(cut, row, c)) = s.value();
-      } else {
-        __stcg(reinterpret_cast<float4*>(out + row * D + c), s.v);
-        if (c == 0) {
-          __stcg(out + C::kRows * D + row, s.m);
-          __stcg(out + C::kRows * D + C::kRows + row, s.l);
+    }
+  }
+  __syncthreads();  // before the tickets: their release covers the CTA's stores
+  // Only the first and the last run can be of an item of other CTAs too.
+  if (tid == 0 || (tid == 32 && sh.runs > 1)) {
+    const int run = tid == 0 ? 0 : sh.runs - 1;
+    if (sh.runs > 0) {
+      const Cut cut = sh.run_first[run] >= 0 ? sh.tail[sh.run_first[run]] : sh.head[sh.run_head[run]];
+      if (cut.first < cta_r0 || cut.first + cut.units > cta_r1) {
+        // A CTA is the first one of at most one item that goes on after it: its counter is that
+        // item's.
+        const uint32_t k0 = split.worker(cut.first) / kWarps, k1 = split.worker(cut.first + cut.units - 1) / kWarps;
+        uint32_t* counter = static_cast<uint32_t*>(p.ws) + k0;
+        if (take_ticket(counter) == k1 - k0) {
+          *counter = 0;  // every contributor has its ticket: ready for the next call
+          const int slot = cut.first >= cta_r0 ? 1 : 0;
+          sh.fin[slot] = cut;
+          sh.last[slot] = 1;
         }
       }
-    }
-    if (here) return;
-    // A CTA is the first one of at most one item that goes on after it: its counter is that
-    // item's.  The lanes' stores come before the ticket (release, after the warp's barrier).
-    __syncwarp();
-    if (lane == 0) {
-      const int64_t k0 = worker_of(cut.first, total, workers) / kWarps;
-      const int64_t k1 = worker_of(cut.first + cut.units - 1, total, workers) / kWarps;
-      uint32_t* counter = static_cast<uint32_t*>(p.ws) + k0;
-      if (take_ticket(counter) == static_cast<uint32_t>(k1 - k0)) {
-        *counter = 0;  // every contributor has its ticket: ready for the next call
-        sh.fin[slot] = cut;
-        sh.last[slot] = 1;
-      }
-    }
-  };
-  int ft = -1, lt = -1, runs = 0;
-#pragma unroll 1
-  for (int w = 0; w <= kWarps; ++w) {
-    const bool head = w < kWarps && sh.has_head[w];
-    if (head || (w == kWarps && ft >= 0)) {
-      if (runs++ % kWarps == warp) join(ft, lt, head ? w : -1);
-      ft = -1;
-    }
-    if (w < kWarps && sh.has_tail[w]) {
-      if (ft < 0) ft = w;
-      lt = w;
     }
   }
   __syncthreads();
@@ -735,8 +791,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   for (int slot = 0; slot < 2; ++slot) {
     if (!sh.last[slot]) continue;
     const Cut cut = sh.fin[slot];
-    const int64_t k0 = worker_of(cut.first, total, workers) / kWarps;
-    const int64_t k1 = worker_of(cut.first + cut.units - 1, total, workers) / kWarps;
+    const uint32_t k0 = split.worker(cut.first) / kWarps, k1 = split.worker(cut.first + cut.units - 1) / kWarps;
     const int outs = rows_of(cut) * (D / 4);
     const int groups = outs < kThreads ? kThreads / outs : 1;
     float* mid = reinterpret_cast<float*>(smem);  // [thread][6]
@@ -745,13 +800,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const int grp = i / outs, at = i - grp * outs, row = at / (D / 4), c = at % (D / 4) * 4;
       Sum s;
 #pragma unroll 1
-      for (int64_t k = k0 + grp; k <= k1; k += 4 * groups) {
+      for (uint32_t k = k0 + grp; k <= k1; k += 4 * groups) {
         float mk[4], lk[4];
         float4 v[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int64_t kk = k + x * groups;
-          const float* q = cta_parts + (2 * kk + (kk == k0 ? 1 : 0)) * C::kPart;
+          const uint32_t kk = k + x * groups;
+          const float* q = cta_parts + (2 * static_cast<int64_t>(kk) + (kk == k0 ? 1 : 0)) * C::kPart;
           const bool in = kk <= k1;
           mk[x] = in ? __ldcg(q + C::kRows * D + row) : -INFINITY;
           lk[x] = in ? __ldcg(q + C::kRows * D + C::kRows + row) : 0.f;
@@ -795,8 +850,10 @@ cudaError_t launch_variant(const Kv4AttnParams& p, int sms, cudaStream_t s) {
   const cudaError_t e = ensure_smem_attr(kern, C::kSmem, attr_done);
   if (e != cudaSuccess) return e;
   const int rows = static_cast<int>(p.Lq) * p.group;
+  Kv4AttnParams q = p;
+  q.one_copy = p.page_size % C::kUnit == 0;
   return launch_pdl(kern, dim3(static_cast<unsigned>(sms < kMaxCtas ? sms : kMaxCtas)), dim3(C::kThreads), C::kSmem,
-                    s, p, (rows + C::kRows - 1) / C::kRows);
+                    s, q, (rows + C::kRows - 1) / C::kRows);
 }
 
 // Query rows of a block: the fewest tiles of 8 that hold them, at most 4.

@@ -159,6 +159,9 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
   if (heads_q > 65536 || Lq > 65536 || batch > 65536 || batch * Lq * heads_q > INT32_MAX ||
       ldt > (int64_t(1) << 28) / cache->page_size)
     return DG_ERR_UNSUPPORTED;
+  // The kernel counts units of 32 keys of all (sequence, head, 8 query rows) in 31 bits.
+  if (batch * cache->heads * ((Lq * (heads_q / cache->heads) + 7) / 8) > INT32_MAX / (ldt * cache->page_size / 32 + 1))
+    return DG_ERR_UNSUPPORTED;
   if (!aligned(Q, 16) || !aligned(O, 16) || ldq % 8 || ldo % 8 || strideQ % 8 || strideO % 8 ||
       !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(workspace, 256))
     return DG_ERR_MISALIGNED;

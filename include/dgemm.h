@@ -362,7 +362,8 @@ dg_status kv4_gather(const dg_kv4_cache* cache, int64_t tokens, const int64_t* s
  *   - Errors: heads_q not a multiple of the cache's heads, null pointers, overlapping strides,
  *     a scale that is not finite and positive, a workspace that is too small
  *     DG_ERR_INVALID_ARG; sizes over 65536 (batch, Lq, heads_q), batch * Lq * heads_q over
- *     2^31 - 1 or ldt * page_size over 2^28 DG_ERR_UNSUPPORTED; Q or O not 16-byte or workspace not 256-byte
+ *     2^31 - 1, ldt * page_size over 2^28 or, with ldt * page_size tokens in every sequence,
+ *     2^31 or more (sequence, cache head, 8 query rows, 32 tokens) DG_ERR_UNSUPPORTED; Q or O not 16-byte or workspace not 256-byte
  *     aligned, ld or strides not multiples of 8 DG_ERR_MISALIGNED.  batch, Lq or heads_q == 0:
  *     nothing.
  */
