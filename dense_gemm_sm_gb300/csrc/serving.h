@@ -86,7 +86,7 @@ struct MoeParams {
   void* ws;
   uint32_t* status;
 };
-int64_t moe_ws_bytes(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top);
+int64_t moe_ws_bytes(int64_t T, int64_t I, int64_t top);
 cudaError_t launch_moe(const MoeParams& p, int sms, cudaStream_t s);
 
 }  // namespace dg

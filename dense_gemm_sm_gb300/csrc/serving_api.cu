@@ -187,8 +187,8 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
 }
 
 int64_t dg_moe_workspace_bytes(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top) {
-  if (T <= 0 || K <= 0 || I <= 0 || E <= 0 || top <= 0 || top > E) return 0;
-  return moe_ws_bytes(T, K, I, E, top);
+  if (T <= 0 || K <= 0 || I <= 0 || E <= 0 || top <= 0 || top > E || T > 64 || top > 16) return 0;
+  return moe_ws_bytes(T, I, top);
 }
 
 dg_status moe_bf16(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top, int32_t renorm, const uint16_t* X,
@@ -203,7 +203,11 @@ dg_status moe_bf16(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top, int3
   if (ldx < K || ldl < E || ldwg < I || ldwu < I || ldwd < K || ldy < K) return DG_ERR_INVALID_ARG;
   if (E > 1 && (strideWg < K * ldwg || strideWu < K * ldwu || strideWd < I * ldwd)) return DG_ERR_INVALID_ARG;
   if (T > 64 || top > 16 || E > 512 || K > INT32_MAX || I > INT32_MAX) return DG_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < moe_ws_bytes(T, K, I, E, top)) return DG_ERR_INVALID_ARG;
+  {  // units of 64 x 64 (128) weights of the experts that T tokens can reach, counted in 31 bits
+    const int64_t reach = E < T * top ? E : T * top, kb = (K + 63) / 64, ib = (I + 63) / 64;
+    if (kb > INT32_MAX / ib / reach) return DG_ERR_UNSUPPORTED;
+  }
+  if (!workspace || workspace_bytes < moe_ws_bytes(T, I, top)) return DG_ERR_INVALID_ARG;
   if (!aligned(X, 16) || !aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(Wd, 16) || ldx % 8 || ldwg % 8 ||
       ldwu % 8 || ldwd % 8 || strideWg % 8 || strideWu % 8 || strideWd % 8 || !aligned(logits, 4) ||
       !aligned(Y, 2) || !aligned(workspace, 256))
