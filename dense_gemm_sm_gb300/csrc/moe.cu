@@ -7,17 +7,20 @@
 // With at most 64 tokens every weight of a chosen expert is used a few times: reading each
 // once from HBM bounds the layer.  Two kernels, one CTA per SM each, the second launched
 // programmatically behind the first:
-//   * up: every CTA routes all tokens itself (a warp per token; less than a launch costs), then
-//     the work of the active experts -- (expert, 64 columns of W_g and of W_u, 64 rows of K)
-//     units -- is cut evenly over the CTAs, whatever the experts' number;
-//   * down: (128 columns of W_d, expert, 64 rows of I) units, cut the same way.  A column tile
-//     sums over experts in FP32 in shared memory, one addition per expert and token.
+//   * up: (expert, 128 columns of W_g and of W_u, 64 rows of K) units of the active experts;
+//   * down: (128 columns of W_d, expert, 64 rows of I) units.  A column tile sums over experts in
+//     FP32 in shared memory, one addition per expert and token.
+// Both route all tokens in every CTA (a warp per token: about a microsecond, less than another
+// launch), and cut the units evenly over the CTAs, however many experts are active.  Tiles are
+// 128 columns, 256 bytes of each weight row: with 64 columns of W_g and 64 of W_u beside them
+// the up kernel streamed 4.9 TB/s where this form's rows of 256 bytes reach 6.
 // Units stream through a ring of TMA stages into tcgen05 with the weights as the 128-row
 // operand (as they lie, N contiguous) and the tokens as the narrow one: all T tokens in the
 // first product (rows of other experts are ignored: gathering them would cost more than their
 // columns), an expert's own rows, 16 at a time, in the second, whose input the first writes
-// sorted by expert.  A tile cut between CTAs is finished by the last of them to arrive, which
-// adds the parts in CTA order: results do not depend on arrival.
+// sorted by expert.  The down kernel fills its ring with weights before it waits for the first.
+// A tile cut between CTAs is finished by the last of them to arrive, which adds the parts in CTA
+// order: results do not depend on arrival.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,29 +36,19 @@ namespace {
 constexpr int kMaxCtas = 160;        // CTAs that the workspace has room for
 constexpr int kMaxT = 64, kMaxE = 512, kMaxTop = 16, kMaxPairs = kMaxT * kMaxTop;
 constexpr int BK = 64;               // rows of a unit
-constexpr uint32_t W_BYTES = 128 * BK * 2;
-constexpr int kUpThreads = 512;      // routing: a warp per token
-constexpr int kDownThreads = 192;
+constexpr uint32_t W_BYTES = 128 * BK * 2;  // of one matrix
+constexpr int kThreads = 512;        // routing: a warp per token
+constexpr int kWarps = kThreads / 32;
 constexpr int kPrefetch = 10;        // units of W_d that the up kernel asks L2 for, per CTA
 
-// What the up kernel tells the down kernel.
-struct Routes {
-  int32_t active;                    // experts with at least one token
-  int32_t expert[kMaxE];             // in ascending order
-  int32_t off[kMaxE + 1];            // their first rows of Z
-  int32_t token[kMaxPairs];          // of a row of Z
-  float weight[kMaxPairs];
-};
-
-// Workspace: counters (zero between calls), routes, Z, parts of cut tiles.
-constexpr int64_t kCounters = 2 * kMaxCtas;
+// Workspace: counters (zero between calls), parts of cut tiles, Z (rows sorted by expert).
+constexpr int64_t kPartsAt = 2048;
+static_assert(2 * kMaxCtas * 4 <= kPartsAt, "counters");
 constexpr int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
-constexpr int64_t kRoutesAt = up256(kCounters * 4);
-constexpr int64_t kPartsAt = kRoutesAt + up256(sizeof(Routes));
 constexpr int ntok_of(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
-constexpr int64_t part_floats(int64_t T) { return ntok_of(T) * 128; }
-constexpr int64_t z_at(int64_t T) { return kPartsAt + 2 * kMaxCtas * part_floats(T) * 4; }
-constexpr int64_t ldz_of(int64_t I) { return (I + 7) / 8 * 8; }
+constexpr __host__ __device__ int64_t part_floats(int ntok) { return ntok * 256; }
+constexpr int64_t z_at(int64_t T) { return kPartsAt + 2 * kMaxCtas * part_floats(ntok_of(T)) * 4; }
+constexpr __host__ __device__ int64_t ldz_of(int64_t I) { return (I + 7) / 8 * 8; }
 
 // Units cut evenly over workers, the first `rem` of them one unit longer.
 struct Split {
@@ -83,8 +76,11 @@ __device__ __forceinline__ void prefetch_l2_3d(const CUtensorMap* map, int32_t x
                : "memory");
 }
 
-struct Maps {
-  CUtensorMap a, a2, b;  // up: W_g, W_u, X; down: W_d, -, Z
+struct UpMaps {
+  CUtensorMap wg, wu, x, wd;  // wd: to ask L2 for its head
+};
+struct DownMaps {
+  CUtensorMap wd, z;
 };
 
 template <int STAGES>
@@ -93,6 +89,7 @@ struct Pipe {
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem_base, abort, is_last, seg_ok;
+  int32_t job;  // down: the column tile to join, -1 for none left
   __device__ void init() {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -116,104 +113,106 @@ struct Pipe {
   }
 };
 
-template <int NTOK>
-struct Cfg {
-  static constexpr int kStages = NTOK == 64 ? 7 : 8;
-  static constexpr uint32_t kX = NTOK * BK * 2;
-  static constexpr uint32_t kRing = kStages * (W_BYTES + kX);
-  static constexpr uint32_t kTmem = NTOK == 16 ? 32 : 2 * NTOK;
-  static constexpr int kHalf = NTOK < 32 ? NTOK : 32;  // tokens in registers at a time
-};
-
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
-  uint32_t r[N];
-  if constexpr (N == 16) tmem_ld_32x32b_x16(taddr, r);
-  else tmem_ld_32x32b_x32(taddr, r);
-  tmem_ld_wait();
-#pragma unroll
-  for (int t = 0; t < N; ++t) v[t] = __uint_as_float(r[t]);
+// One column of the accumulator: a value per lane.
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, float& v) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+  v = __uint_as_float(r);
 }
 
 // ------------------------------------------------------------------ routing
-struct RouteShared {
+struct Routes {
   uint32_t mask[kMaxE][2];             // tokens of an expert
-  int32_t id[kMaxT][kMaxTop];          // -1: none
+  int16_t id[kMaxT][kMaxTop];          // -1: none
   float w[kMaxT][kMaxTop];
-  int32_t pos[kMaxE];                  // an active expert's first row of Z
-  int32_t expert[kMaxE], off[kMaxE + 1];
-  int32_t scan[2][kUpThreads / 32];
+  int16_t pos[kMaxE];                  // an active expert's first row of Z
+  int16_t expert[kMaxE], off[kMaxE + 1];  // active experts in ascending order, their first rows
+  uint8_t token[kMaxPairs];            // of a row of Z
+  float weight[kMaxPairs];
+  int32_t scan[2][kWarps];
   int32_t active;
 };
 
-// All threads of the up kernel.  A lane holds the logits of experts lane, lane + 32, ... as
-// integers in the order of their values, 0 for an expert that is off (-inf, NaN).
-__device__ void route(const MoeParams& p, RouteShared& sh) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// The chosen experts of tokens warp, warp + kWarps, ...; KE * 32 >= E.  A lane holds the logits
+// of experts lane, lane + 32, ... as integers in the order of their values, 0 for an expert that
+// is off (-inf, NaN); the largest is taken `top` times.
+template <int KE>
+__device__ __forceinline__ void choose(const MoeParams& p, Routes& sh, int warp, int lane) {
   const int T = static_cast<int>(p.T), E = static_cast<int>(p.E), top = p.top;
-  for (int i = tid; i < 2 * E; i += kUpThreads) (&sh.mask[0][0])[i] = 0;
-  __syncthreads();
-#pragma unroll 1
-  for (int t = warp; t < T; t += kUpThreads / 32) {
-    const float* row = p.logits + t * p.ldl;
-    uint32_t key[kMaxE / 32];
+  auto load = [&](int t, uint32_t (&key)[KE]) {
 #pragma unroll
-    for (int i = 0; i < kMaxE / 32; ++i) {
-      if (i * 32 >= E) {
-        key[i] = 0;
-        continue;
-      }
+    for (int i = 0; i < KE; ++i) {
       const int e = lane + 32 * i;
-      const float v = e < E ? __ldg(row + e) : -INFINITY;
+      const float v = t < T && e < E ? __ldcg(p.logits + t * p.ldl + e) : -INFINITY;
       const uint32_t b = __float_as_uint(v + 0.f);  // -0 and 0 are equal
       key[i] = v > -INFINITY ? ((b & 0x80000000u) ? ~b : b | 0x80000000u) : 0u;
     }
-    auto value = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k); };
-    float best = 0.f, sum = 0.f, chosen = 0.f, mine = 0.f;
+  };
+  auto value = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k); };
+  uint32_t key[KE], next[KE];
+  load(warp, next);
+#pragma unroll 1
+  for (int t = warp; t < T; t += kWarps) {
+    uint32_t all[KE];
+#pragma unroll
+    for (int i = 0; i < KE; ++i) all[i] = key[i] = next[i];
+    load(t + kWarps, next);
+    uint32_t mine = 0;  // lane k: the k-th choice
     int my_id = -1;
 #pragma unroll 1
     for (int k = 0; k < top; ++k) {
       uint32_t m = key[0];
 #pragma unroll
-      for (int i = 1; i < kMaxE / 32; ++i)
-        if (i * 32 < E) m = max(m, key[i]);
+      for (int i = 1; i < KE; ++i) m = max(m, key[i]);
       m = __reduce_max_sync(~0u, m);
       if (m == 0) break;
       uint32_t e = 0xFFFFFFFFu;  // the lowest expert with that logit
 #pragma unroll
-      for (int i = kMaxE / 32 - 1; i >= 0; --i)
-        if (i * 32 < E && key[i] == m) e = lane + 32 * i;
+      for (int i = KE - 1; i >= 0; --i)
+        if (key[i] == m) e = lane + 32 * i;
       e = __reduce_min_sync(~0u, e);
-      const float v = value(m);
-      if (k == 0) {
-        best = v;
-#pragma unroll
-        for (int i = 0; i < kMaxE / 32; ++i)
-          if (i * 32 < E && key[i]) sum += expf(value(key[i]) - best);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      }
-      const float w = expf(v - best);
-      chosen += w;
       if (lane == k) {
-        mine = w;
+        mine = m;
         my_id = static_cast<int>(e);
       }
 #pragma unroll
-      for (int i = 0; i < kMaxE / 32; ++i)
-        if (i * 32 < E && e == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
-      if (lane == 0 && w > 0.f) atomicOr(&sh.mask[e][t >> 5], 1u << (t & 31));
+      for (int i = 0; i < KE; ++i)
+        if (e == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
     }
+    const float best = value(__shfl_sync(~0u, mine, 0));
+    const float w = mine ? expf(value(mine) - best) : 0.f;
+    float by = w;
+    if (!p.renorm) {
+      by = 0.f;
+#pragma unroll
+      for (int i = 0; i < KE; ++i)
+        if (all[i]) by += expf(value(all[i]) - best);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) by += __shfl_xor_sync(~0u, by, o);
     if (lane < top) {
-      const float by = p.renorm ? chosen : sum;
-      sh.id[t][lane] = mine > 0.f ? my_id : -1;  // a weight that underflows adds nothing
-      sh.w[t][lane] = mine > 0.f ? mine / by : 0.f;
+      const bool real = w > 0.f;  // a weight that underflows adds nothing
+      sh.id[t][lane] = static_cast<int16_t>(real ? my_id : -1);
+      sh.w[t][lane] = real ? w / by : 0.f;
+      if (real) atomicOr(&sh.mask[my_id][t >> 5], 1u << (t & 31));
     }
   }
+}
+
+// All threads.  Logits are read from L2: the down kernel routes before the kernel it follows
+// has ended, and the logits were complete before that one started anything.
+__device__ void route(const MoeParams& p, Routes& sh) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int E = static_cast<int>(p.E), top = p.top;
+  if (tid < E) sh.mask[tid][0] = sh.mask[tid][1] = 0;
   __syncthreads();
-  // Active experts in ascending order and their rows.
-  const bool mine = tid < E;
-  const int count = mine ? __popc(sh.mask[tid][0]) + __popc(sh.mask[tid][1]) : 0;
+  if (E <= 32) choose<1>(p, sh, warp, lane);
+  else if (E <= 64) choose<2>(p, sh, warp, lane);
+  else if (E <= 128) choose<4>(p, sh, warp, lane);
+  else choose<16>(p, sh, warp, lane);
+  __syncthreads();
+  // Active experts in ascending order and their rows: a thread per expert.
+  const int count = tid < E ? __popc(sh.mask[tid][0]) + __popc(sh.mask[tid][1]) : 0;
   const uint32_t vote = __ballot_sync(~0u, count > 0);
   int rows = count;
 #pragma unroll
@@ -233,39 +232,55 @@ __device__ void route(const MoeParams& p, RouteShared& sh) {
     first += sh.scan[1][w];
   }
   if (count > 0) {
-    sh.expert[act] = tid;
-    sh.off[act] = first;
-    sh.pos[tid] = first;
+    sh.expert[act] = static_cast<int16_t>(tid);
+    sh.off[act] = sh.pos[tid] = static_cast<int16_t>(first);
   }
-  if (tid == kUpThreads - 1) {
+  if (tid == kThreads - 1) {
     sh.active = act + (count > 0);
-    sh.off[sh.active] = first + count;
+    sh.off[sh.active] = static_cast<int16_t>(first + count);
+  }
+  __syncthreads();
+  const int pairs = static_cast<int>(p.T) * top;
+#pragma unroll 1
+  for (int i = tid; i < pairs; i += kThreads) {
+    const int t = i / top, e = sh.id[t][i - t * top];
+    if (e < 0) continue;
+    const uint32_t lo = sh.mask[e][0], bit = (1u << (t & 31)) - 1;
+    const int at = sh.pos[e] + (t < 32 ? __popc(lo & bit) : __popc(lo) + __popc(sh.mask[e][1] & bit));
+    sh.token[at] = static_cast<uint8_t>(t);
+    sh.weight[at] = sh.w[t][i - t * top];
   }
   __syncthreads();
 }
 
 // ------------------------------------------------------------------ up: Z
 template <int NTOK>
-__global__ void __launch_bounds__(kUpThreads, 1)
-    moe_up_kernel(const __grid_constant__ Maps maps, const __grid_constant__ CUtensorMap map_d, const MoeParams p) {
-  using C = Cfg<NTOK>;
+struct UpCfg {
+  static constexpr int kStages = NTOK == 16 ? 6 : 5;
+  static constexpr uint32_t kX = NTOK * BK * 2;
+  static constexpr uint32_t kStage = 2 * W_BYTES + kX;
+  static constexpr uint32_t kTmem = 4 * NTOK;  // (gate, up) twice
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage;
+  static_assert(kSmem + sizeof(Routes) + 512 <= 227 * 1024, "shared memory");
+};
+
+template <int NTOK>
+__global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_constant__ UpMaps maps, const MoeParams p) {
+  using C = UpCfg<NTOK>;
   constexpr int STAGES = C::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ RouteShared rt;
+  __shared__ Routes rt;
   __shared__ Pipe<STAGES> pipe;
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t ring = (raw + 1023u) & ~1023u;
-  const uint32_t x_ring = ring + STAGES * W_BYTES;
-  float* xch = reinterpret_cast<float*>(smem_raw + (ring - raw) + C::kRing);  // [kHalf][64]: x W_u of a tile
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   volatile uint32_t* abort = &pipe.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     pipe.init();
-    tma_prefetch_map(&maps.a);
-    tma_prefetch_map(&maps.a2);
-    tma_prefetch_map(&maps.b);
-    tma_prefetch_map(&map_d);
+    tma_prefetch_map(&maps.wg);
+    tma_prefetch_map(&maps.wu);
+    tma_prefetch_map(&maps.x);
+    tma_prefetch_map(&maps.wd);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&pipe.tmem_base), C::kTmem);
@@ -280,7 +295,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
 
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   const uint32_t kb = static_cast<uint32_t>((p.K + BK - 1) / BK);
-  const uint32_t ntiles = static_cast<uint32_t>((p.I + 63) / 64);
+  const uint32_t ntiles = static_cast<uint32_t>((p.I + 127) / 128);
   const uint32_t units = static_cast<uint32_t>(rt.active) * ntiles * kb;
   const uint32_t ctas = min(units, gridDim.x);
   const bool works = blockIdx.x < ctas;
@@ -294,18 +309,20 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       bool ok = true;
       for (uint32_t u = u0; ok && u < u1;) {
         const uint32_t tile = u / kb, end = min(u1, (tile + 1) * kb);
-        const int32_t e = rt.expert[tile / ntiles], n0 = static_cast<int32_t>(tile % ntiles) * 64;
+        const int32_t e = rt.expert[tile / ntiles], n0 = static_cast<int32_t>(tile % ntiles) * 128;
         for (int32_t k = static_cast<int32_t>(u - tile * kb) * BK; u < end; ++u, k += BK) {
           const uint32_t s = it % STAGES;
           if (!mbar_wait(smem_u32(&pipe.empty[s]), ((it / STAGES) & 1u) ^ 1u, abort, p.status, kDevTimeoutProducer)) {
             ok = false;
             break;
           }
-          const uint32_t fb = smem_u32(&pipe.full[s]), w = ring + s * W_BYTES;
-          mbar_arrive_expect_tx(fb, W_BYTES + C::kX);
-          tma_load_3d(w, &maps.a, fb, n0, k, e);
-          tma_load_3d(w + W_BYTES / 2, &maps.a2, fb, n0, k, e);
-          tma_load_2d(x_ring + s * C::kX, &maps.b, fb, k, 0);
+          const uint32_t fb = smem_u32(&pipe.full[s]), w = ring + s * C::kStage;
+          mbar_arrive_expect_tx(fb, C::kStage);
+          tma_load_3d(w, &maps.wg, fb, n0, k, e);
+          tma_load_3d(w + W_BYTES / 2, &maps.wg, fb, n0 + 64, k, e);
+          tma_load_3d(w + W_BYTES, &maps.wu, fb, n0, k, e);
+          tma_load_3d(w + W_BYTES * 3 / 2, &maps.wu, fb, n0 + 64, k, e);
+          tma_load_2d(w + 2 * W_BYTES, &maps.x, fb, k, 0);
           ++it;
         }
       }
@@ -319,8 +336,8 @@ __global__ void __launch_bounds__(kUpThreads, 1)
           for (uint32_t d = d0; d < d1; ++d) {
             const uint32_t tile = d / per, in = d - tile * per, a = in / dkb;
             const int32_t n0 = static_cast<int32_t>(tile) * 128, k = static_cast<int32_t>(in - a * dkb) * BK;
-            prefetch_l2_3d(&map_d, n0, k, rt.expert[a]);
-            if (n0 + 64 < p.K) prefetch_l2_3d(&map_d, n0 + 64, k, rt.expert[a]);
+            prefetch_l2_3d(&maps.wd, n0, k, rt.expert[a]);
+            if (n0 + 64 < p.K) prefetch_l2_3d(&maps.wd, n0 + 64, k, rt.expert[a]);
           }
         }
       }
@@ -330,7 +347,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      // A = [W_g | W_u]^T tile, 64 columns each (N contiguous: MN-major), B = all tokens' X block.
+      // A = W_g^T, W_u^T tiles (N contiguous: MN-major), B = all tokens' X block.
       constexpr uint32_t idesc = idesc_bf16_f32(128, NTOK, true, false);
       uint32_t it = 0, lt = 0;
       bool ok = true;
@@ -339,6 +356,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         const uint32_t acc = lt & 1u;
         if (!mbar_wait(smem_u32(&pipe.tempty[acc]), ((lt >> 1) & 1u) ^ 1u, abort, p.status, kDevTimeoutMma)) break;
         tc_fence_after();
+        const uint32_t d = tmem_base + acc * 2 * NTOK;
         for (; u < end; ++u, ++it) {
           const uint32_t s = it % STAGES;
           if (!mbar_wait(smem_u32(&pipe.full[s]), (it / STAGES) & 1u, abort, p.status, kDevTimeoutMma)) {
@@ -346,11 +364,14 @@ __global__ void __launch_bounds__(kUpThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t w0 = ring + s * W_BYTES, x0 = x_ring + s * C::kX;
+          const uint32_t w0 = ring + s * C::kStage, x0 = w0 + 2 * W_BYTES;
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_bf16(tmem_base + acc * NTOK, sdesc_sw128(w0 + k * 2048, W_BYTES / 2, 1024),
-                      sdesc_sw128(x0 + k * 32, 16, 1024), idesc, (u > first || k > 0) ? 1u : 0u);
+          for (int k = 0; k < BK / 16; ++k) {
+            const uint64_t bdesc = sdesc_sw128(x0 + k * 32, 16, 1024);
+            const uint32_t add = (u > first || k > 0) ? 1u : 0u;
+            umma_bf16(d, sdesc_sw128(w0 + k * 2048, W_BYTES / 2, 1024), bdesc, idesc, add);
+            umma_bf16(d + NTOK, sdesc_sw128(w0 + W_BYTES + k * 2048, W_BYTES / 2, 1024), bdesc, idesc, add);
+          }
           umma_commit(smem_u32(&pipe.empty[s]));
         }
         if (ok) umma_commit(smem_u32(&pipe.tfull[acc]));
@@ -360,64 +381,56 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       mbar_wait(smem_u32(&pipe.drain), 0, &never, p.status, kDevTimeoutDrain);
     }
   } else if (warp < 6) {
-    // ------------------------------------------------------------ epilogue
+    // ------------------------------------------------------------ epilogue: a thread per column
     const int q = warp & 3, row = q * 32 + lane, etid = threadIdx.x - 64;
     const int64_t ldz = ldz_of(p.I);
-    uint16_t* Z = reinterpret_cast<uint16_t*>(ws + z_at(p.T));
-    float* parts = reinterpret_cast<float*>(ws + kPartsAt);
+    uint16_t* Z = reinterpret_cast<uint16_t*>(ws + (kPartsAt + 2 * kMaxCtas * part_floats(NTOK) * 4));
+    float* parts = reinterpret_cast<float*>(ws + kPartsAt) + row;
     uint32_t lt = 0;
     for (uint32_t u = u0; u < u1; ++lt) {
       const uint32_t tile = u / kb, end = min(u1, (tile + 1) * kb);
       const bool whole = end - u == kb;
       const uint32_t acc = lt & 1u;
-      const int a = static_cast<int>(tile / ntiles), e = rt.expert[a];
-      const int n = static_cast<int>(tile % ntiles) * 64 + (row & 63);
-      const uint32_t masks[2] = {rt.mask[e][0], rt.mask[e][1]};
+      const int a = static_cast<int>(tile / ntiles), z0 = rt.off[a], rows = rt.off[a + 1] - z0;
+      const int64_t n = static_cast<int64_t>(tile % ntiles) * 128 + row;
       // One thread waits (bounded); all 128 take the same decision after the barrier.
       if (etid == 0)
         pipe.seg_ok = mbar_wait(smem_u32(&pipe.tfull[acc]), (lt >> 1) & 1u, abort, p.status, kDevTimeoutEpilogue) ? 1u : 0u;
       epi_bar();
       if (!pipe.seg_ok) break;
       tc_fence_after();
-      // z of tokens [32 h, + kHalf) of the tile from its finished sums v.
-      auto finish = [&](int h, const float (&v)[C::kHalf]) {
-        const uint32_t mask = masks[h];
-        if (row >= 64) {
-#pragma unroll
-          for (int t = 0; t < C::kHalf; ++t)
-            if ((mask >> t) & 1u) xch[t * 64 + row - 64] = v[t];
-        }
-        epi_bar();
-        if (row < 64 && n < p.I) {
-          const int64_t z0 = rt.off[a] + (h ? __popc(masks[0]) : 0);
-#pragma unroll
-          for (int t = 0; t < C::kHalf; ++t)
-            if ((mask >> t) & 1u) {
-              const float z = v[t] / (1.f + expf(-v[t])) * xch[t * 64 + row];
-              Z[(z0 + __popc(mask & ((1u << t) - 1))) * ldz + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
-            }
-        }
-        epi_bar();
+      auto store = [&](int r, float g, float up) {
+        const float z = g / (1.f + expf(-g)) * up;
+        if (n < p.I) Z[(z0 + r) * ldz + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
       };
       // A CTA's part of a tile that began in an earlier CTA is its first, else its last.
-      float* part = parts + (2 * blockIdx.x + (u0 > tile * kb ? 0 : 1)) * part_floats(p.T) + row;
+      float* part = parts + (2 * blockIdx.x + (u0 > tile * kb ? 0 : 1)) * part_floats(NTOK);
+      const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 2 * NTOK;
+      constexpr int B = 8;  // rows at a time
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += B) {
+        float g[B], up[B];
 #pragma unroll
-      for (int h = 0; h < NTOK / C::kHalf; ++h) {
-        float v[C::kHalf];
-        tmem_ld<C::kHalf>(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NTOK + h * 32, v);
-        if (h == NTOK / C::kHalf - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&pipe.tempty[acc]));
+        for (int j = 0; j < B; ++j) {
+          const uint32_t t = rt.token[min(z0 + r0 + j, kMaxPairs - 1)] & (NTOK - 1);  // past the rows: any
+          tmem_ld1(t0 + t, g[j]);
+          tmem_ld1(t0 + NTOK + t, up[j]);
         }
-        if (whole) {
-          finish(h, v);
-        } else {
+        tmem_ld_wait();
 #pragma unroll
-          for (int t = 0; t < C::kHalf; ++t)
-            if ((masks[h] >> t) & 1u) __stcg(part + (h * 32 + t) * 128, v[t]);
+        for (int j = 0; j < B; ++j) {
+          if (r0 + j >= rows) break;
+          if (whole) {
+            store(r0 + j, g[j], up[j]);
+          } else {
+            __stcg(part + (r0 + j) * 256, g[j]);
+            __stcg(part + (r0 + j) * 256 + 128, up[j]);
+          }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&pipe.tempty[acc]));
       if (!whole) {
         // The barrier orders the CTA's stores before the ticket, whose release covers them.  A
         // CTA is the first one of at most one tile that goes on after it: its counter is the tile's.
@@ -431,40 +444,27 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         }
         epi_bar();
         if (pipe.is_last) {
-#pragma unroll
-          for (int h = 0; h < NTOK / C::kHalf; ++h) {
-            float s[C::kHalf];
-#pragma unroll
-            for (int t = 0; t < C::kHalf; ++t) s[t] = 0.f;
+#pragma unroll 1
+          for (int r0 = 0; r0 < rows; r0 += 4) {
+            float g[4] = {0.f, 0.f, 0.f, 0.f}, up[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
             for (uint32_t c = c0; c <= c1; ++c) {
-              const float* src = parts + (2 * c + (c > c0 ? 0 : 1)) * part_floats(p.T) + row;
+              const float* src = parts + (2 * c + (c > c0 ? 0 : 1)) * part_floats(NTOK) + r0 * 256;
 #pragma unroll
-              for (int t = 0; t < C::kHalf; ++t)
-                if ((masks[h] >> t) & 1u) s[t] += __ldcg(src + (h * 32 + t) * 128);
+              for (int j = 0; j < 4; ++j) {
+                const int at = r0 + j < rows ? j : 0;
+                g[j] += __ldcg(src + at * 256);
+                up[j] += __ldcg(src + at * 256 + 128);
+              }
             }
-            finish(h, s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (r0 + j < rows) store(r0 + j, g[j], up[j]);
           }
         }
-        epi_bar();  // is_last is rewritten only after everyone read it
       }
+      epi_bar();  // seg_ok and is_last are rewritten only after everyone read them
       u = end;
-    }
-  } else if (warp == 6 && blockIdx.x == 0) {
-    // ------------------------------------------------------------ the routes, for the down kernel
-    Routes* out = reinterpret_cast<Routes*>(ws + kRoutesAt);
-    if (lane == 0) out->active = rt.active;
-    for (int i = lane; i <= rt.active; i += 32) {
-      if (i < rt.active) out->expert[i] = rt.expert[i];
-      out->off[i] = rt.active ? rt.off[i] : 0;
-    }
-    const int top = p.top, pairs = static_cast<int>(p.T) * top;
-    for (int i = lane; i < pairs; i += 32) {
-      const int t = i / top, e = rt.id[t][i - t * top];
-      if (e < 0) continue;
-      const uint32_t lo = rt.mask[e][0], hi = rt.mask[e][1], bit = (1u << (t & 31)) - 1;
-      const int at = rt.pos[e] + (t < 32 ? __popc(lo & bit) : __popc(lo) + __popc(hi & bit));
-      out->token[at] = t;
-      out->weight[at] = rt.w[t][i - t * top];
     }
   }
 
@@ -478,48 +478,46 @@ __global__ void __launch_bounds__(kUpThreads, 1)
 
 // ------------------------------------------------------------------ down: Y
 template <int NTOK>
-__global__ void __launch_bounds__(kDownThreads, 1)
-    moe_down_kernel(const __grid_constant__ Maps maps, const MoeParams p) {
-  using C = Cfg<NTOK>;
+struct DownCfg {
+  static constexpr int kStages = NTOK == 64 ? 6 : 8;
+  static constexpr uint32_t kZ = NTOK * BK * 2;
+  static constexpr uint32_t kStage = W_BYTES + kZ;
+  static constexpr uint32_t kTmem = NTOK == 16 ? 32 : 2 * NTOK;
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage + NTOK * 128 * 4;
+  static_assert(kSmem + sizeof(Routes) + 512 <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void join_bar() { asm volatile("bar.sync 2, 448;" ::: "memory"); }
+
+template <int NTOK>
+__global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_constant__ DownMaps maps, const MoeParams p) {
+  using C = DownCfg<NTOK>;
   constexpr int STAGES = C::kStages;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ Routes rt;
   __shared__ Pipe<STAGES> pipe;
-  __shared__ int32_t expert[kMaxE], off[kMaxE + 1], token[kMaxPairs];
-  __shared__ float weight[kMaxPairs];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
-  const uint32_t z_ring = ring + STAGES * W_BYTES;
-  float* yacc = reinterpret_cast<float*>(smem_raw + (ring - raw) + C::kRing);  // [T][128]
+  float* yacc = reinterpret_cast<float*>(smem_raw + (ring - raw) + STAGES * C::kStage);  // [T][128]
   volatile uint32_t* abort = &pipe.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* ws = static_cast<uint8_t*>(p.ws);
-  const Routes* routes = reinterpret_cast<const Routes*>(ws + kRoutesAt);
 
   if (threadIdx.x == 0) {
     pipe.init();
-    tma_prefetch_map(&maps.a);
-    tma_prefetch_map(&maps.b);
+    tma_prefetch_map(&maps.wd);
+    tma_prefetch_map(&maps.z);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&pipe.tmem_base), C::kTmem);
     tmem_relinquish();
   }
-  pdl_wait();
-  const int active = __ldcg(&routes->active);
-  for (int i = threadIdx.x; i <= active; i += kDownThreads) {
-    if (i < active) expert[i] = __ldcg(&routes->expert[i]);
-    off[i] = __ldcg(&routes->off[i]);
-  }
-  const int rows_all = __ldcg(&routes->off[active]);
-  for (int i = threadIdx.x; i < rows_all; i += kDownThreads) {
-    token[i] = __ldcg(&routes->token[i]);
-    weight[i] = __ldcg(&routes->weight[i]);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = pipe.tmem_base;
-  const int T = static_cast<int>(p.T);
+  route(p, rt);  // before the wait for the up kernel: see there
+  uint8_t* ws = static_cast<uint8_t*>(p.ws);
+  const int T = static_cast<int>(p.T), active = rt.active;
   const uint32_t kb = static_cast<uint32_t>((p.I + BK - 1) / BK), per = static_cast<uint32_t>(active) * kb;
   const uint32_t units = static_cast<uint32_t>((p.K + 127) / 128) * per;
   const uint32_t ctas = min(units, gridDim.x);
@@ -527,36 +525,41 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   const Split split(units, ctas > 0 ? ctas : 1);
   const uint32_t u0 = works ? split.start(blockIdx.x) : 0, u1 = works ? split.start(blockIdx.x + 1) : 0;
 
-  if (active == 0) {  // no expert at all: Y = 0
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kDownThreads + threadIdx.x; i < p.T * p.K;
-         i += static_cast<int64_t>(gridDim.x) * kDownThreads)
-      p.Y[i / p.K * p.ldy + i % p.K] = 0;
-  }
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      fence_proxy_async_global();  // Z was written by ordinary stores
-      uint32_t it = 0;
-      bool ok = true;
-      for (uint32_t u = u0; ok && u < u1;) {
+      auto load_w = [&](uint32_t it, uint32_t u) {
         const uint32_t tile = u / per, in = u - tile * per, a = in / kb;
-        const uint32_t end = min(u1, tile * per + (a + 1) * kb);
-        const int32_t n0 = static_cast<int32_t>(tile) * 128, e = expert[a], z0 = off[a];
-        const int boxes = (off[a + 1] - z0 + 15) / 16;
-        for (int32_t k = static_cast<int32_t>(in - a * kb) * BK; u < end; ++u, k += BK) {
-          const uint32_t s = it % STAGES;
-          if (!mbar_wait(smem_u32(&pipe.empty[s]), ((it / STAGES) & 1u) ^ 1u, abort, p.status, kDevTimeoutProducer)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = smem_u32(&pipe.full[s]), w = ring + s * W_BYTES;
-          mbar_arrive_expect_tx(fb, W_BYTES + boxes * (16 * BK * 2));
-          tma_load_3d(w, &maps.a, fb, n0, k, e);
-          tma_load_3d(w + W_BYTES / 2, &maps.a, fb, n0 + 64, k, e);
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d(z_ring + s * C::kX + i * (16 * BK * 2), &maps.b, fb, k, z0 + i * 16);
-          ++it;
+        const int32_t n0 = static_cast<int32_t>(tile) * 128, k = static_cast<int32_t>(in - a * kb) * BK, e = rt.expert[a];
+        const uint32_t fb = smem_u32(&pipe.full[it % STAGES]), w = ring + (it % STAGES) * C::kStage;
+        const int boxes = (rt.off[a + 1] - rt.off[a] + 15) / 16;
+        mbar_arrive_expect_tx(fb, W_BYTES + boxes * (16 * BK * 2));
+        tma_load_3d(w, &maps.wd, fb, n0, k, e);
+        tma_load_3d(w + W_BYTES / 2, &maps.wd, fb, n0 + 64, k, e);
+      };
+      auto load_z = [&](uint32_t it, uint32_t u) {
+        const uint32_t tile = u / per, in = u - tile * per, a = in / kb;
+        const int32_t k = static_cast<int32_t>(in - a * kb) * BK, z0 = rt.off[a];
+        const uint32_t fb = smem_u32(&pipe.full[it % STAGES]), z = ring + (it % STAGES) * C::kStage + W_BYTES;
+        const int boxes = (rt.off[a + 1] - z0 + 15) / 16;
+        for (int i = 0; i < boxes; ++i) tma_load_2d(z + i * (16 * BK * 2), &maps.z, fb, k, z0 + i * 16);
+      };
+      // The ring's first weights come while the up kernel ends; its Z after the wait.
+      const uint32_t ahead = min(u1 - u0, static_cast<uint32_t>(STAGES));
+      for (uint32_t i = 0; i < ahead; ++i) load_w(i, u0 + i);
+      pdl_wait();
+      fence_proxy_async_global();  // Z was written by ordinary stores
+      for (uint32_t i = 0; i < ahead; ++i) load_z(i, u0 + i);
+      uint32_t it = ahead;
+      bool ok = true;
+      for (uint32_t u = u0 + ahead; u < u1; ++u, ++it) {
+        if (!mbar_wait(smem_u32(&pipe.empty[it % STAGES]), ((it / STAGES) & 1u) ^ 1u, abort, p.status,
+                       kDevTimeoutProducer)) {
+          ok = false;
+          break;
         }
+        load_w(it, u);
+        load_z(it, u);
       }
       pdl_trigger();
       if (!ok) pipe.drain_loads(it, p.status);
@@ -564,12 +567,13 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
+      pdl_wait();  // so that its bounded waits start when the data can come
       uint32_t it = 0, lt = 0;
       bool ok = true;
       for (uint32_t u = u0; ok && u < u1; ++lt) {
         const uint32_t tile = u / per, in = u - tile * per, a = in / kb;
         const uint32_t end = min(u1, tile * per + (a + 1) * kb), first = u;
-        const uint32_t boxes = (off[a + 1] - off[a] + 15) / 16;
+        const uint32_t boxes = (rt.off[a + 1] - rt.off[a] + 15) / 16;
         const uint32_t idesc = idesc_bf16_f32(128, 16 * boxes, true, false);
         const uint32_t acc = lt & 1u;
         if (!mbar_wait(smem_u32(&pipe.tempty[acc]), ((lt >> 1) & 1u) ^ 1u, abort, p.status, kDevTimeoutMma)) break;
@@ -581,7 +585,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t w0 = ring + s * W_BYTES, z0 = z_ring + s * C::kX;
+          const uint32_t w0 = ring + s * C::kStage, z0 = w0 + W_BYTES;
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k)
             umma_bf16(tmem_base + acc * NTOK, sdesc_sw128(w0 + k * 2048, W_BYTES / 2, 1024),
@@ -595,70 +599,118 @@ __global__ void __launch_bounds__(kDownThreads, 1)
       mbar_wait(smem_u32(&pipe.drain), 0, &never, p.status, kDevTimeoutDrain);
     }
   } else {
-    // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, row = q * 32 + lane, etid = threadIdx.x - 64;
+    pdl_wait();
     float* parts = reinterpret_cast<float*>(ws + kPartsAt);
-    for (int t = 0; t < T; ++t) yacc[t * 128 + row] = 0.f;  // a thread touches its column only
-    uint32_t lt = 0;
-    for (uint32_t u = u0; u < u1; ++lt) {
-      const uint32_t tile = u / per, in = u - tile * per, a = in / kb;
-      const uint32_t tile_end = (tile + 1) * per, end = min(u1, tile * per + (a + 1) * kb);
-      const uint32_t acc = lt & 1u;
-      const int z0 = off[a], rows = off[a + 1] - z0;
-      if (etid == 0)
-        pipe.seg_ok = mbar_wait(smem_u32(&pipe.tfull[acc]), (lt >> 1) & 1u, abort, p.status, kDevTimeoutEpilogue) ? 1u : 0u;
-      epi_bar();
-      if (!pipe.seg_ok) break;
-      tc_fence_after();
+    const int jtid = threadIdx.x - 64;  // of the 448 that join tiles
+    if (active == 0)  // no expert at all: Y = 0
+      for (int64_t i = static_cast<int64_t>(blockIdx.x) * 448 + jtid; i < p.T * p.K; i += static_cast<int64_t>(gridDim.x) * 448)
+        p.Y[i / p.K * p.ldy + i % p.K] = 0;
+    // Adds a tile's parts in CTA order, four columns of one token a thread, and writes them.
+    auto join = [&](uint32_t tile) {
+      const uint32_t c0 = split.worker(tile * per), c1 = split.worker((tile + 1) * per - 1);
 #pragma unroll 1
-      for (int g = 0; g < rows; g += 16) {
-        float v[16];
-        tmem_ld<16>(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NTOK + g, v);
+      for (int i = jtid; i < T * 32; i += 448) {
+        const int t = i >> 5, c4 = (i & 31) * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (uint32_t c = c0; c <= c1; c += 8) {
+          float4 v[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (g + j < rows) {
-            float* y = yacc + token[z0 + g + j] * 128 + row;
-            *y = fmaf(weight[z0 + g + j], v[j], *y);
-          }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&pipe.tempty[acc]));
-      u = end;
-      if (u < tile_end && u < u1) {
-        epi_bar();  // seg_ok is rewritten only after everyone read it
-        continue;
-      }
-      // ---- the column tile is done, here or as far as this CTA goes
-      const int64_t n = static_cast<int64_t>(tile) * 128 + row;
-      const uint32_t c0 = split.worker(tile * per), c1 = split.worker(tile_end - 1);
-      bool write = true;
-      if (c0 != c1) {
-        float* part = parts + (2 * blockIdx.x + (u0 > tile * per ? 0 : 1)) * part_floats(p.T) + row;
-        for (int t = 0; t < T; ++t) __stcg(part + t * 128, yacc[t * 128 + row]);
-        epi_bar();
-        if (etid == 0) {
-          uint32_t* counter = reinterpret_cast<uint32_t*>(ws) + kMaxCtas + c0;
-          const bool last = take_ticket(counter) == c1 - c0;
-          if (last) *counter = 0;
-          pipe.is_last = last;
-        }
-        epi_bar();
-        write = pipe.is_last;
-        if (write) {
-          for (int t = 0; t < T; ++t) yacc[t * 128 + row] = 0.f;
-          for (uint32_t c = c0; c <= c1; ++c) {
-            const float* src = parts + (2 * c + (c > c0 ? 0 : 1)) * part_floats(p.T) + row;
-#pragma unroll 8
-            for (int t = 0; t < T; ++t) yacc[t * 128 + row] += __ldcg(src + t * 128);
+          for (int x = 0; x < 8; ++x)
+            v[x] = c + x <= c1 ? __ldcg(reinterpret_cast<const float4*>(
+                                     parts + (2 * (c + x) + (c + x > c0 ? 0 : 1)) * part_floats(NTOK) + t * 128 + c4))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            s.x += v[x].x;
+            s.y += v[x].y;
+            s.z += v[x].z;
+            s.w += v[x].w;
           }
         }
+        const float y[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t n = static_cast<int64_t>(tile) * 128 + c4 + j;
+          if (n < p.K) p.Y[t * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y[j]));
+        }
       }
-      if (write && n < p.K)
-        for (int t = 0; t < T; ++t)
-          p.Y[t * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(yacc[t * 128 + row]));
-      for (int t = 0; t < T; ++t) yacc[t * 128 + row] = 0.f;
-      epi_bar();
+    };
+    if (warp < 6) {
+      // ---------------------------------------------------------- epilogue: a thread per column
+      const int q = warp & 3, row = q * 32 + lane, etid = threadIdx.x - 64;
+      for (int t = 0; t < T; ++t) yacc[t * 128 + row] = 0.f;  // a thread touches its column only
+      uint32_t lt = 0;
+      for (uint32_t u = u0; u < u1; ++lt) {
+        const uint32_t tile = u / per, in = u - tile * per, a = in / kb;
+        const uint32_t tile_end = (tile + 1) * per, end = min(u1, tile * per + (a + 1) * kb);
+        const uint32_t acc = lt & 1u;
+        const int z0 = rt.off[a], rows = rt.off[a + 1] - z0;
+        if (etid == 0)
+          pipe.seg_ok = mbar_wait(smem_u32(&pipe.tfull[acc]), (lt >> 1) & 1u, abort, p.status, kDevTimeoutEpilogue) ? 1u : 0u;
+        epi_bar();
+        if (!pipe.seg_ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int g = 0; g < rows; g += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NTOK + g, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (g + j < rows) {
+              float* y = yacc + rt.token[z0 + g + j] * 128 + row;
+              *y = fmaf(rt.weight[z0 + g + j], __uint_as_float(v[j]), *y);
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&pipe.tempty[acc]));
+        u = end;
+        if (u == tile_end || u == u1) {
+          // ---- the column tile is done, here or as far as this CTA goes
+          const int64_t n = static_cast<int64_t>(tile) * 128 + row;
+          const uint32_t c0 = split.worker(tile * per), c1 = split.worker(tile_end - 1);
+          if (c0 == c1) {
+            for (int t = 0; t < T; ++t) {
+              if (n < p.K) p.Y[t * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(yacc[t * 128 + row]));
+              yacc[t * 128 + row] = 0.f;
+            }
+          } else {
+            float* part = parts + (2 * blockIdx.x + (u0 > tile * per ? 0 : 1)) * part_floats(NTOK) + row;
+            for (int t = 0; t < T; ++t) {
+              __stcg(part + t * 128, yacc[t * 128 + row]);
+              yacc[t * 128 + row] = 0.f;
+            }
+            // Barrier, ticket and counter as in the up kernel.
+            epi_bar();
+            if (etid == 0) {
+              uint32_t* counter = reinterpret_cast<uint32_t*>(ws) + kMaxCtas + c0;
+              const bool last = take_ticket(counter) == c1 - c0;
+              if (last) *counter = 0;
+              pipe.is_last = last;
+              if (last) pipe.job = static_cast<int32_t>(tile);
+            }
+            epi_bar();
+            if (pipe.is_last) {
+              join_bar();  // the other warps take the job
+              join(tile);
+              join_bar();
+            }
+          }
+        }
+        epi_bar();  // seg_ok and is_last are rewritten only after everyone read them
+      }
+      if (etid == 0) pipe.job = -1;
+      join_bar();
+    } else {
+      for (;;) {
+        join_bar();
+        const int32_t tile = pipe.job;
+        if (tile < 0) break;
+        join(static_cast<uint32_t>(tile));
+        join_bar();
+      }
     }
   }
 
@@ -671,21 +723,16 @@ __global__ void __launch_bounds__(kDownThreads, 1)
 }
 
 template <int NTOK>
-cudaError_t launch_ntok(const MoeParams& p, const Maps& up, const Maps& down, int sms, cudaStream_t s) {
-  using C = Cfg<NTOK>;
-  constexpr uint32_t smem_up = 1024 + C::kRing + C::kHalf * 64 * 4;
-  constexpr uint32_t smem_down = 1024 + C::kRing + NTOK * 128 * 4;
-  static_assert(smem_up + sizeof(RouteShared) + 512 <= 227 * 1024, "shared memory");
-  static_assert(smem_down + (2 * kMaxE + 1 + 2 * kMaxPairs) * 4 + 512 <= 227 * 1024, "shared memory");
+cudaError_t launch_ntok(const MoeParams& p, const UpMaps& up, const DownMaps& down, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> done_up{0}, done_down{0};
-  cudaError_t e = ensure_smem_attr(moe_up_kernel<NTOK>, smem_up, done_up);
+  cudaError_t e = ensure_smem_attr(moe_up_kernel<NTOK>, UpCfg<NTOK>::kSmem, done_up);
   if (e != cudaSuccess) return e;
-  e = ensure_smem_attr(moe_down_kernel<NTOK>, smem_down, done_down);
+  e = ensure_smem_attr(moe_down_kernel<NTOK>, DownCfg<NTOK>::kSmem, done_down);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(sms < kMaxCtas ? sms : kMaxCtas));
-  e = launch_pdl(moe_up_kernel<NTOK>, grid, dim3(kUpThreads), smem_up, s, up, down.a, p);
+  const dim3 grid(static_cast<unsigned>(sms < kMaxCtas ? sms : kMaxCtas)), block(kThreads);
+  e = launch_pdl(moe_up_kernel<NTOK>, grid, block, UpCfg<NTOK>::kSmem, s, up, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(moe_down_kernel<NTOK>, grid, dim3(kDownThreads), smem_down, s, down, p);
+  return launch_pdl(moe_down_kernel<NTOK>, grid, block, DownCfg<NTOK>::kSmem, s, down, p);
 }
 
 }  // namespace
@@ -704,16 +751,17 @@ cudaError_t launch_moe(const MoeParams& p, int sms, cudaStream_t s) {
   auto stride = [&](int64_t given, int64_t rows, int64_t ld) {
     return static_cast<uint64_t>(p.E > 1 ? given : rows * ld);
   };
-  Maps up, down;
+  UpMaps up;
+  DownMaps down;
   const int ntok = ntok_of(p.T);
   const uint8_t* z = static_cast<const uint8_t*>(p.ws) + z_at(p.T);
-  if (!make_bf16_map(&up.a, p.Wg, p.I, p.K, p.ldwg, experts, stride(p.strideWg, p.K, p.ldwg), 64, BK) ||
-      !make_bf16_map(&up.a2, p.Wu, p.I, p.K, p.ldwu, experts, stride(p.strideWu, p.K, p.ldwu), 64, BK) ||
-      !make_bf16_map(&up.b, p.X, p.K, p.T, p.ldx, 1, 0, BK, ntok) ||
-      !make_bf16_map(&down.a, p.Wd, p.K, p.I, p.ldwd, experts, stride(p.strideWd, p.I, p.ldwd), 64, BK) ||
-      !make_bf16_map(&down.b, z, p.I, p.T * p.top, ldz_of(p.I), 1, 0, BK, 16))
+  if (!make_bf16_map(&up.wg, p.Wg, p.I, p.K, p.ldwg, experts, stride(p.strideWg, p.K, p.ldwg), 64, BK) ||
+      !make_bf16_map(&up.wu, p.Wu, p.I, p.K, p.ldwu, experts, stride(p.strideWu, p.K, p.ldwu), 64, BK) ||
+      !make_bf16_map(&up.x, p.X, p.K, p.T, p.ldx, 1, 0, BK, ntok) ||
+      !make_bf16_map(&up.wd, p.Wd, p.K, p.I, p.ldwd, experts, stride(p.strideWd, p.I, p.ldwd), 64, BK) ||
+      !make_bf16_map(&down.z, z, p.I, p.T * p.top, ldz_of(p.I), 1, 0, BK, 16))
     return cudaErrorInvalidValue;
-  down.a2 = down.a;
+  down.wd = up.wd;
   return ntok == 16 ? launch_ntok<16>(p, up, down, sms, s)
                     : ntok == 32 ? launch_ntok<32>(p, up, down, sms, s) : launch_ntok<64>(p, up, down, sms, s);
 }
