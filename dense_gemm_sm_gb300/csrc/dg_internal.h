@@ -184,6 +184,11 @@ bool make_tile_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t esz, co
                    uint64_t inner, uint64_t outer, uint64_t ld, uint64_t batch, uint64_t stride,
                    uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle,
                    uint32_t box_batch);
+// The same with the size of the lines that L2 fetches for it (make_tile_map: 256 bytes).
+bool make_tile_map_l2(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t esz, const void* base,
+                      uint64_t inner, uint64_t outer, uint64_t ld, uint64_t batch, uint64_t stride,
+                      uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle,
+                      uint32_t box_batch, CUtensorMapL2promotion promotion);
 
 // ------------------------------------------------------------------ misc
 // C = beta * C over a (batch, M, N) strided view (K == 0 or alpha == 0).

@@ -925,15 +925,15 @@ std::unordered_map<MapKey, CUtensorMap, MapKeyHash> g_map_cache;
 // as zero (and are not written by stores).  Encoded maps are cached by (address, shape,
 // type, box): repeated calls on the same buffers (the usual inference loop) skip the
 // encoding on the launch path.
-bool make_tile_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t esz, const void* base,
-                   uint64_t inner, uint64_t outer, uint64_t ld, uint64_t batch, uint64_t stride,
-                   uint32_t box_inner, uint32_t box_outer,
-                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B, uint32_t box_batch = 1) {
+bool make_tile_map_l2(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t esz, const void* base,
+                      uint64_t inner, uint64_t outer, uint64_t ld, uint64_t batch, uint64_t stride,
+                      uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle,
+                      uint32_t box_batch, CUtensorMapL2promotion promotion) {
   MapKey key;
   std::memset(&key, 0, sizeof key);
   key.base = base; key.inner = inner; key.outer = outer; key.ld = ld;
   key.batch = batch > 1 ? batch : 1; key.stride = batch > 1 ? stride : 0;
-  key.box_inner = box_inner | (static_cast<uint32_t>(dtype) << 16);
+  key.box_inner = box_inner | (static_cast<uint32_t>(dtype) << 16) | (static_cast<uint32_t>(promotion) << 24);
   key.box_outer = box_outer | (static_cast<uint32_t>(swizzle) << 16) | (box_batch << 20);
   {
     std::lock_guard<std::mutex> lock(g_map_mu);
@@ -951,13 +951,21 @@ bool make_tile_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t esz, co
   cuuint32_t box[3] = {box_inner, box_outer, box_batch};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, dtype, rank3 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
   std::lock_guard<std::mutex> lock(g_map_mu);
   if (g_map_cache.size() >= 4096) g_map_cache.clear();
   g_map_cache.emplace(key, *map);
   return true;
+}
+
+bool make_tile_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t esz, const void* base,
+                   uint64_t inner, uint64_t outer, uint64_t ld, uint64_t batch, uint64_t stride,
+                   uint32_t box_inner, uint32_t box_outer,
+                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B, uint32_t box_batch = 1) {
+  return make_tile_map_l2(map, dtype, esz, base, inner, outer, ld, batch, stride, box_inner, box_outer,
+                          swizzle, box_batch, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,

@@ -10,8 +10,8 @@
 //   * up: (expert, 128 columns of W_g and of W_u, 64 rows of K) units of the active experts;
 //   * down: (128 columns of W_d, expert, 64 rows of I) units.  A column tile sums over experts in
 //     FP32 in shared memory, one addition per expert and token.
-// Both route all tokens in every CTA (a warp per token: about a microsecond, less than another
-// launch), and cut the units evenly over the CTAs, however many experts are active.  Tiles are
+// Both route up to 16 tokens in every CTA, a warp per token (more have a small launch of their own
+// first), and cut the units evenly over the CTAs, however many experts are active.  Tiles are
 // 128 columns, 256 bytes of each weight row: with 64 columns of W_g and 64 of W_u beside them
 // the up kernel streamed 4.9 TB/s where this form's rows of 256 bytes reach 6.
 // Units stream through a ring of TMA stages into tcgen05 with the weights as the 128-row
@@ -39,11 +39,16 @@ constexpr int BK = 64;               // rows of a unit
 constexpr uint32_t W_BYTES = 128 * BK * 2;  // of one matrix
 constexpr int kThreads = 512;        // routing: a warp per token
 constexpr int kWarps = kThreads / 32;
-constexpr int kPrefetch = 10;        // units of W_d that the up kernel asks L2 for, per CTA
+static_assert(kMaxE == kThreads, "a thread per expert");
+constexpr int kPrefetch = 16;        // units of W_d after its ring that a CTA asks L2 for early
+// Small calls: a CTA is given at least this many units, as a join of many parts costs more than
+// a few more units in a row.
+constexpr uint32_t kMinUp = 2, kMinDown = 4;
 
-// Workspace: counters (zero between calls), parts of cut tiles, Z (rows sorted by expert).
-constexpr int64_t kPartsAt = 2048;
-static_assert(2 * kMaxCtas * 4 <= kPartsAt, "counters");
+// Workspace: counters (zero between calls), the tokens' choices (calls with a routing launch),
+// parts of cut tiles, Z (rows sorted by expert).
+constexpr int64_t kChoicesAt = 2048, kPartsAt = kChoicesAt + 8192;
+static_assert(2 * kMaxCtas * 4 <= kChoicesAt, "counters");
 constexpr int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 constexpr int ntok_of(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 constexpr __host__ __device__ int64_t part_floats(int ntok) { return ntok * 256; }
@@ -68,6 +73,9 @@ __device__ __forceinline__ uint32_t take_ticket(uint32_t* a) {
 }
 // Orders this thread's view of ordinary global stores before its TMA loads.
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+// The warps that join cut tiles: all but the producer's and the MMA issuer's.
+constexpr int kJoin = kThreads - 64;
+__device__ __forceinline__ void join_bar() { asm volatile("bar.sync 2, %0;" ::"n"(kJoin) : "memory"); }
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_l2_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
@@ -77,7 +85,7 @@ __device__ __forceinline__ void prefetch_l2_3d(const CUtensorMap* map, int32_t x
 }
 
 struct UpMaps {
-  CUtensorMap wg, wu, x, wd;  // wd: to ask L2 for its head
+  CUtensorMap wg, wu, x;
 };
 struct DownMaps {
   CUtensorMap wd, z;
@@ -133,11 +141,21 @@ struct Routes {
   int32_t active;
 };
 
-// The chosen experts of tokens warp, warp + kWarps, ...; KE * 32 >= E.  A lane holds the logits
-// of experts lane, lane + 32, ... as integers in the order of their values, 0 for an expert that
-// is off (-inf, NaN); the largest is taken `top` times.
-template <int KE>
-__device__ __forceinline__ void choose(const MoeParams& p, Routes& sh, int warp, int lane) {
+// The choices of all tokens in the workspace.
+struct Choices {
+  float w[kMaxT][kMaxTop];
+  int16_t id[kMaxT][kMaxTop];
+};
+static_assert(sizeof(Choices) <= kPartsAt - kChoicesAt, "choices");
+
+// The chosen experts of tokens warp, warp + warps, ..., a warp per token; KE * 32 >= E.  A lane holds the logits of
+// experts lane, lane + 32, ... as integers in the order of their values, 0 for an expert that is
+// off (-inf, NaN).  The `top`-th largest is found bit by bit from the top, by votes, stopping as
+// soon as a threshold leaves exactly `top`: some 17 votes whatever `top` is.  (Taking the
+// largest `top` times took 6.4 us for 48 tokens, 8 of 64 experts, by integer reductions, 8.3 us
+// by shuffles.)
+template <int KE, bool GLOBAL>
+__device__ __forceinline__ void choose(const MoeParams& p, Routes* sh, Choices* out, int warp, int warps, int lane) {
   const int T = static_cast<int>(p.T), E = static_cast<int>(p.E), top = p.top;
   auto load = [&](int t, uint32_t (&key)[KE]) {
 #pragma unroll
@@ -152,64 +170,106 @@ __device__ __forceinline__ void choose(const MoeParams& p, Routes& sh, int warp,
   uint32_t key[KE], next[KE];
   load(warp, next);
 #pragma unroll 1
-  for (int t = warp; t < T; t += kWarps) {
-    uint32_t all[KE];
+  for (int t = warp; t < T; t += warps) {
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < KE; ++i) all[i] = key[i] = next[i];
-    load(t + kWarps, next);
-    uint32_t mine = 0;  // lane k: the k-th choice
-    int my_id = -1;
+    for (int i = 0; i < KE; ++i) {
+      key[i] = next[i];
+      m = max(m, key[i]);
+    }
+    load(t + warps, next);
+    const float best = value(__reduce_max_sync(~0u, m));
+    auto count = [&](uint32_t least) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < KE; ++i) n += __popc(__ballot_sync(~0u, key[i] >= least));
+      return n;
+    };
+    uint32_t bar = 1;  // chosen: key > bar - 1, or some of those equal to bar
+    int left = top, n = count(1);
+    if (n > top) {
+      bar = 0;
 #pragma unroll 1
-    for (int k = 0; k < top; ++k) {
-      uint32_t m = key[0];
-#pragma unroll
-      for (int i = 1; i < KE; ++i) m = max(m, key[i]);
-      m = __reduce_max_sync(~0u, m);
-      if (m == 0) break;
-      uint32_t e = 0xFFFFFFFFu;  // the lowest expert with that logit
-#pragma unroll
-      for (int i = KE - 1; i >= 0; --i)
-        if (key[i] == m) e = lane + 32 * i;
-      e = __reduce_min_sync(~0u, e);
-      if (lane == k) {
-        mine = m;
-        my_id = static_cast<int>(e);
+      for (uint32_t bit = 0x80000000u; bit != 0 && n != top; bit >>= 1) {
+        const int c = count(bar | bit);
+        if (c >= top) {
+          bar |= bit;
+          n = c;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < KE; ++i)
-        if (e == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
     }
-    const float best = value(__shfl_sync(~0u, mine, 0));
-    const float w = mine ? expf(value(mine) - best) : 0.f;
-    float by = w;
-    if (!p.renorm) {
-      by = 0.f;
+    const bool tied = n > top;  // more than `top` from bar on: the lowest experts of those equal to it
+    if (tied) left = top - count(bar + 1);
+    float w[KE], sum = 0.f;
+    int slot = 0;
 #pragma unroll
-      for (int i = 0; i < KE; ++i)
-        if (all[i]) by += expf(value(all[i]) - best);
+    for (int i = 0; i < KE; ++i) {
+      const uint32_t lower = (1u << lane) - 1;
+      bool in = key[i] >= bar && key[i] > 0;
+      if (tied) {
+        const uint32_t equal = __ballot_sync(~0u, key[i] == bar);
+        if (key[i] == bar && __popc(equal & lower) >= left) in = false;
+        left -= min(left, __popc(equal));
+      }
+      const float x = key[i] ? expf(value(key[i]) - best) : 0.f;
+      w[i] = in ? x : 0.f;
+      sum += p.renorm ? w[i] : x;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) by += __shfl_xor_sync(~0u, by, o);
-    if (lane < top) {
-      const bool real = w > 0.f;  // a weight that underflows adds nothing
-      sh.id[t][lane] = static_cast<int16_t>(real ? my_id : -1);
-      sh.w[t][lane] = real ? w / by : 0.f;
-      if (real) atomicOr(&sh.mask[my_id][t >> 5], 1u << (t & 31));
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+#pragma unroll
+    for (int i = 0; i < KE; ++i) {
+      const uint32_t in = __ballot_sync(~0u, w[i] > 0.f);  // a weight that underflows adds nothing
+      if (w[i] > 0.f) {
+        const int at = slot + __popc(in & ((1u << lane) - 1));
+        (GLOBAL ? out->id : sh->id)[t][at] = static_cast<int16_t>(lane + 32 * i);
+        (GLOBAL ? out->w : sh->w)[t][at] = w[i] / sum;
+        if (!GLOBAL) atomicOr(&sh->mask[lane + 32 * i][t >> 5], 1u << (t & 31));
+      }
+      slot += __popc(in);
     }
+    if (lane >= slot && lane < top) (GLOBAL ? out->id : sh->id)[t][lane] = -1;
   }
 }
 
-// All threads.  Logits are read from L2: the down kernel routes before the kernel it follows
-// has ended, and the logits were complete before that one started anything.
-__device__ void route(const MoeParams& p, Routes& sh) {
+template <bool GLOBAL>
+__device__ __forceinline__ void choose_all(const MoeParams& p, Routes* sh, Choices* out, int warp, int warps, int lane) {
+  if (p.E <= 64) choose<2, GLOBAL>(p, sh, out, warp, warps, lane);
+  else if (p.E <= 128) choose<4, GLOBAL>(p, sh, out, warp, warps, lane);
+  else choose<16, GLOBAL>(p, sh, out, warp, warps, lane);
+}
+
+// More than 16 tokens: a launch of its own, a warp per token.  In every CTA of the other two
+// kernels the same took 7 us for 48 or 64 tokens of 64 experts, twice; for up to 16 tokens (one a
+// warp) it takes 2 to 3 us there, which this launch would not beat.
+constexpr int kRouteWarps = 4;
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const MoeParams p) {
+  pdl_wait();
+  pdl_trigger();
+  Choices* out = reinterpret_cast<Choices*>(static_cast<uint8_t*>(p.ws) + kChoicesAt);
+  choose_all<true>(p, nullptr, out, blockIdx.x * kRouteWarps + (threadIdx.x >> 5), gridDim.x * kRouteWarps, threadIdx.x & 31);
+}
+
+// All threads; the masks are zero and that is visible.  Logits and choices are read from L2: the
+// down kernel routes before the up kernel has ended, and they were complete before that one
+// started anything.
+template <int NTOK>
+__device__ __forceinline__ void route(const MoeParams& p, Routes& sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int E = static_cast<int>(p.E), top = p.top;
-  if (tid < E) sh.mask[tid][0] = sh.mask[tid][1] = 0;
-  __syncthreads();
-  if (E <= 32) choose<1>(p, sh, warp, lane);
-  else if (E <= 64) choose<2>(p, sh, warp, lane);
-  else if (E <= 128) choose<4>(p, sh, warp, lane);
-  else choose<16>(p, sh, warp, lane);
+  if constexpr (NTOK == 16) {
+    choose_all<false>(p, &sh, nullptr, warp, kWarps, lane);
+  } else {
+    const Choices* in = reinterpret_cast<const Choices*>(static_cast<const uint8_t*>(p.ws) + kChoicesAt);
+    for (int i = tid; i < static_cast<int>(p.T) * kMaxTop; i += kThreads) {
+      const int t = i / kMaxTop, k = i % kMaxTop;
+      if (k >= top) continue;
+      const int16_t e = __ldcg(&in->id[t][k]);
+      sh.id[t][k] = e;
+      sh.w[t][k] = __ldcg(&in->w[t][k]);
+      if (e >= 0) atomicOr(&sh.mask[e][t >> 5], 1u << (t & 31));
+    }
+  }
   __syncthreads();
   // Active experts in ascending order and their rows: a thread per expert.
   const int count = tid < E ? __popc(sh.mask[tid][0]) + __popc(sh.mask[tid][1]) : 0;
@@ -275,12 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
   volatile uint32_t* abort = &pipe.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  rt.mask[threadIdx.x][0] = rt.mask[threadIdx.x][1] = 0;  // kMaxE == kThreads
   if (threadIdx.x == 0) {
     pipe.init();
     tma_prefetch_map(&maps.wg);
     tma_prefetch_map(&maps.wu);
     tma_prefetch_map(&maps.x);
-    tma_prefetch_map(&maps.wd);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&pipe.tmem_base), C::kTmem);
@@ -291,16 +351,55 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem_base = pipe.tmem_base;
   pdl_wait();
-  route(p, rt);
+  // The down kernel's CTAs take an SM each as this kernel's leave it, route, and fill their rings.
+  pdl_trigger();
+  route<NTOK>(p, rt);
 
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   const uint32_t kb = static_cast<uint32_t>((p.K + BK - 1) / BK);
   const uint32_t ntiles = static_cast<uint32_t>((p.I + 127) / 128);
   const uint32_t units = static_cast<uint32_t>(rt.active) * ntiles * kb;
-  const uint32_t ctas = min(units, gridDim.x);
+  const uint32_t ctas = min((units + kMinUp - 1) / kMinUp, gridDim.x);
   const bool works = blockIdx.x < ctas;
   const Split split(units, ctas > 0 ? ctas : 1);
   const uint32_t u0 = works ? split.start(blockIdx.x) : 0, u1 = works ? split.start(blockIdx.x + 1) : 0;
+
+  const int64_t ldz = ldz_of(p.I);
+  uint16_t* Z = reinterpret_cast<uint16_t*>(ws + (kPartsAt + 2 * kMaxCtas * part_floats(NTOK) * 4));
+  auto activate = [](float g, float up) { return __float2bfloat16_rn(g / (1.f + expf(-g)) * up); };
+  // Adds a tile's parts in CTA order, four columns of one row a thread, and writes their Z.
+  auto join = [&](uint32_t tile) {
+    const uint32_t c0 = split.worker(tile * kb), c1 = split.worker((tile + 1) * kb - 1);
+    const int a = static_cast<int>(tile / ntiles), z0 = rt.off[a], rows = rt.off[a + 1] - z0;
+    const float* parts = reinterpret_cast<const float*>(ws + kPartsAt);
+#pragma unroll 1
+    for (int i = threadIdx.x - 64; i < rows * 32; i += kJoin) {
+      const int r = i >> 5, c4 = (i & 31) * 4;
+      float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+#pragma unroll 1
+      for (uint32_t c = c0; c <= c1; c += 4) {
+        float4 v[4], w[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float* src = parts + (2 * (c + x) + (c + x > c0 ? 0 : 1)) * part_floats(NTOK) + r * 256 + c4;
+          const bool in = c + x <= c1;
+          v[x] = in ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          w[x] = in ? __ldcg(reinterpret_cast<const float4*>(src + 128)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          g.x += v[x].x; g.y += v[x].y; g.z += v[x].z; g.w += v[x].w;
+          u.x += w[x].x; u.y += w[x].y; u.z += w[x].z; u.w += w[x].w;
+        }
+      }
+      const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t n = static_cast<int64_t>(tile % ntiles) * 128 + c4 + j;
+        if (n < p.I) Z[(z0 + r) * ldz + n] = __bfloat16_as_ushort(activate(gs[j], us[j]));
+      }
+    }
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -326,22 +425,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
           ++it;
         }
       }
-      if (ok && rt.active > 0) {
-        // The head of this CTA's range of the down kernel goes to L2 while this kernel ends.
-        const uint32_t dkb = static_cast<uint32_t>((p.I + BK - 1) / BK), per = rt.active * dkb;
-        const uint32_t dunits = static_cast<uint32_t>((p.K + 127) / 128) * per, dctas = min(dunits, gridDim.x);
-        if (blockIdx.x < dctas) {
-          const Split ds(dunits, dctas);
-          const uint32_t d0 = ds.start(blockIdx.x), d1 = min(ds.start(blockIdx.x + 1), d0 + kPrefetch);
-          for (uint32_t d = d0; d < d1; ++d) {
-            const uint32_t tile = d / per, in = d - tile * per, a = in / dkb;
-            const int32_t n0 = static_cast<int32_t>(tile) * 128, k = static_cast<int32_t>(in - a * dkb) * BK;
-            prefetch_l2_3d(&maps.wd, n0, k, rt.expert[a]);
-            if (n0 + 64 < p.K) prefetch_l2_3d(&maps.wd, n0 + 64, k, rt.expert[a]);
-          }
-        }
-      }
-      pdl_trigger();
       if (!ok) pipe.drain_loads(it, p.status);
     }
   } else if (warp == 1) {
@@ -383,8 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
   } else if (warp < 6) {
     // ------------------------------------------------------------ epilogue: a thread per column
     const int q = warp & 3, row = q * 32 + lane, etid = threadIdx.x - 64;
-    const int64_t ldz = ldz_of(p.I);
-    uint16_t* Z = reinterpret_cast<uint16_t*>(ws + (kPartsAt + 2 * kMaxCtas * part_floats(NTOK) * 4));
     float* parts = reinterpret_cast<float*>(ws + kPartsAt) + row;
     uint32_t lt = 0;
     for (uint32_t u = u0; u < u1; ++lt) {
@@ -400,8 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
       if (!pipe.seg_ok) break;
       tc_fence_after();
       auto store = [&](int r, float g, float up) {
-        const float z = g / (1.f + expf(-g)) * up;
-        if (n < p.I) Z[(z0 + r) * ldz + n] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
+        if (n < p.I) Z[(z0 + r) * ldz + n] = __bfloat16_as_ushort(activate(g, up));
       };
       // A CTA's part of a tile that began in an earlier CTA is its first, else its last.
       float* part = parts + (2 * blockIdx.x + (u0 > tile * kb ? 0 : 1)) * part_floats(NTOK);
@@ -444,27 +524,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
         }
         epi_bar();
         if (pipe.is_last) {
-#pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += 4) {
-            float g[4] = {0.f, 0.f, 0.f, 0.f}, up[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-            for (uint32_t c = c0; c <= c1; ++c) {
-              const float* src = parts + (2 * c + (c > c0 ? 0 : 1)) * part_floats(NTOK) + r0 * 256;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int at = r0 + j < rows ? j : 0;
-                g[j] += __ldcg(src + at * 256);
-                up[j] += __ldcg(src + at * 256 + 128);
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (r0 + j < rows) store(r0 + j, g[j], up[j]);
-          }
+          if (etid == 0) pipe.job = static_cast<int32_t>(tile);
+          join_bar();  // the other warps take the job
+          join(tile);
+          join_bar();
         }
       }
       epi_bar();  // seg_ok and is_last are rewritten only after everyone read them
       u = end;
+    }
+    if (etid == 0) pipe.job = -1;
+    join_bar();
+  } else {
+    for (;;) {
+      join_bar();
+      const int32_t tile = pipe.job;
+      if (tile < 0) break;
+      join(static_cast<uint32_t>(tile));
+      join_bar();
     }
   }
 
@@ -487,8 +564,6 @@ struct DownCfg {
   static_assert(kSmem + sizeof(Routes) + 512 <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void join_bar() { asm volatile("bar.sync 2, 448;" ::: "memory"); }
-
 template <int NTOK>
 __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_constant__ DownMaps maps, const MoeParams p) {
   using C = DownCfg<NTOK>;
@@ -502,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
   volatile uint32_t* abort = &pipe.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  rt.mask[threadIdx.x][0] = rt.mask[threadIdx.x][1] = 0;  // kMaxE == kThreads
   if (threadIdx.x == 0) {
     pipe.init();
     tma_prefetch_map(&maps.wd);
@@ -515,12 +591,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = pipe.tmem_base;
-  route(p, rt);  // before the wait for the up kernel: see there
+  route<NTOK>(p, rt);  // before the wait for the up kernel: see there
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   const int T = static_cast<int>(p.T), active = rt.active;
   const uint32_t kb = static_cast<uint32_t>((p.I + BK - 1) / BK), per = static_cast<uint32_t>(active) * kb;
   const uint32_t units = static_cast<uint32_t>((p.K + 127) / 128) * per;
-  const uint32_t ctas = min(units, gridDim.x);
+  const uint32_t ctas = min((units + kMinDown - 1) / kMinDown, gridDim.x);
   const bool works = blockIdx.x < ctas;
   const Split split(units, ctas > 0 ? ctas : 1);
   const uint32_t u0 = works ? split.start(blockIdx.x) : 0, u1 = works ? split.start(blockIdx.x + 1) : 0;
@@ -528,38 +604,61 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      auto load_w = [&](uint32_t it, uint32_t u) {
-        const uint32_t tile = u / per, in = u - tile * per, a = in / kb;
-        const int32_t n0 = static_cast<int32_t>(tile) * 128, k = static_cast<int32_t>(in - a * kb) * BK, e = rt.expert[a];
-        const uint32_t fb = smem_u32(&pipe.full[it % STAGES]), w = ring + (it % STAGES) * C::kStage;
-        const int boxes = (rt.off[a + 1] - rt.off[a] + 15) / 16;
-        mbar_arrive_expect_tx(fb, W_BYTES + boxes * (16 * BK * 2));
-        tma_load_3d(w, &maps.wd, fb, n0, k, e);
-        tma_load_3d(w + W_BYTES / 2, &maps.wd, fb, n0 + 64, k, e);
+      // A place in the row of units; stepping needs no division (with two a unit this thread,
+      // not HBM, set the pace where L2 already had the weights).
+      struct Place {
+        int32_t n0, k, a;
       };
-      auto load_z = [&](uint32_t it, uint32_t u) {
-        const uint32_t tile = u / per, in = u - tile * per, a = in / kb;
-        const int32_t k = static_cast<int32_t>(in - a * kb) * BK, z0 = rt.off[a];
-        const uint32_t fb = smem_u32(&pipe.full[it % STAGES]), z = ring + (it % STAGES) * C::kStage + W_BYTES;
-        const int boxes = (rt.off[a + 1] - z0 + 15) / 16;
-        for (int i = 0; i < boxes; ++i) tma_load_2d(z + i * (16 * BK * 2), &maps.z, fb, k, z0 + i * 16);
+      const int32_t k_end = static_cast<int32_t>(kb) * BK;
+      auto step = [&](Place& x) {
+        x.k += BK;
+        if (x.k < k_end) return;
+        x.k = 0;
+        if (++x.a == active) {
+          x.a = 0;
+          x.n0 += 128;
+        }
       };
+      auto boxes_of = [&](int32_t a) { return (rt.off[a + 1] - rt.off[a] + 15) / 16; };
+      auto load_w = [&](uint32_t s, const Place& x) {
+        const uint32_t fb = smem_u32(&pipe.full[s]), w = ring + s * C::kStage;
+        mbar_arrive_expect_tx(fb, W_BYTES + boxes_of(x.a) * (16 * BK * 2));
+        tma_load_3d(w, &maps.wd, fb, x.n0, x.k, rt.expert[x.a]);
+        tma_load_3d(w + W_BYTES / 2, &maps.wd, fb, x.n0 + 64, x.k, rt.expert[x.a]);
+      };
+      auto load_z = [&](uint32_t s, const Place& x) {
+        const uint32_t fb = smem_u32(&pipe.full[s]), z = ring + s * C::kStage + W_BYTES;
+        const int boxes = boxes_of(x.a);
+        for (int i = 0; i < boxes; ++i) tma_load_2d(z + i * (16 * BK * 2), &maps.z, fb, x.k, rt.off[x.a] + i * 16);
+      };
+      const uint32_t tile0 = per ? u0 / per : 0, a0 = per ? (u0 - tile0 * per) / kb : 0;
+      const Place first = {static_cast<int32_t>(tile0) * 128, static_cast<int32_t>(u0 - tile0 * per - a0 * kb) * BK,
+                           static_cast<int32_t>(a0)};
       // The ring's first weights come while the up kernel ends; its Z after the wait.
       const uint32_t ahead = min(u1 - u0, static_cast<uint32_t>(STAGES));
-      for (uint32_t i = 0; i < ahead; ++i) load_w(i, u0 + i);
+      Place w = first;
+      for (uint32_t i = 0; i < ahead; ++i, step(w)) load_w(i, w);
+      // And L2 is asked for what follows: HBM streams on while the last up CTAs end.
+      const uint32_t asked = min(u1 - u0 - ahead, static_cast<uint32_t>(kPrefetch));
+      Place l2 = w;
+      for (uint32_t i = 0; i < asked; ++i, step(l2)) {
+        prefetch_l2_3d(&maps.wd, l2.n0, l2.k, rt.expert[l2.a]);
+        if (l2.n0 + 64 < p.K) prefetch_l2_3d(&maps.wd, l2.n0 + 64, l2.k, rt.expert[l2.a]);
+      }
       pdl_wait();
       fence_proxy_async_global();  // Z was written by ordinary stores
-      for (uint32_t i = 0; i < ahead; ++i) load_z(i, u0 + i);
+      Place z = first;
+      for (uint32_t i = 0; i < ahead; ++i, step(z)) load_z(i, z);
       uint32_t it = ahead;
       bool ok = true;
-      for (uint32_t u = u0 + ahead; u < u1; ++u, ++it) {
-        if (!mbar_wait(smem_u32(&pipe.empty[it % STAGES]), ((it / STAGES) & 1u) ^ 1u, abort, p.status,
-                       kDevTimeoutProducer)) {
+      for (uint32_t u = u0 + ahead; u < u1; ++u, ++it, step(w)) {
+        const uint32_t s = it % STAGES;
+        if (!mbar_wait(smem_u32(&pipe.empty[s]), ((it / STAGES) & 1u) ^ 1u, abort, p.status, kDevTimeoutProducer)) {
           ok = false;
           break;
         }
-        load_w(it, u);
-        load_z(it, u);
+        load_w(s, w);
+        load_z(s, w);
       }
       pdl_trigger();
       if (!ok) pipe.drain_loads(it, p.status);
@@ -601,27 +700,27 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
   } else {
     pdl_wait();
     float* parts = reinterpret_cast<float*>(ws + kPartsAt);
-    const int jtid = threadIdx.x - 64;  // of the 448 that join tiles
+    const int jtid = threadIdx.x - 64;  // of those that join tiles
     if (active == 0)  // no expert at all: Y = 0
-      for (int64_t i = static_cast<int64_t>(blockIdx.x) * 448 + jtid; i < p.T * p.K; i += static_cast<int64_t>(gridDim.x) * 448)
+      for (int64_t i = static_cast<int64_t>(blockIdx.x) * kJoin + jtid; i < p.T * p.K; i += static_cast<int64_t>(gridDim.x) * kJoin)
         p.Y[i / p.K * p.ldy + i % p.K] = 0;
     // Adds a tile's parts in CTA order, four columns of one token a thread, and writes them.
     auto join = [&](uint32_t tile) {
       const uint32_t c0 = split.worker(tile * per), c1 = split.worker((tile + 1) * per - 1);
 #pragma unroll 1
-      for (int i = jtid; i < T * 32; i += 448) {
+      for (int i = jtid; i < T * 32; i += kJoin) {
         const int t = i >> 5, c4 = (i & 31) * 4;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (uint32_t c = c0; c <= c1; c += 8) {
-          float4 v[8];
+        for (uint32_t c = c0; c <= c1; c += 12) {
+          float4 v[12];
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
+          for (int x = 0; x < 12; ++x)
             v[x] = c + x <= c1 ? __ldcg(reinterpret_cast<const float4*>(
                                      parts + (2 * (c + x) + (c + x > c0 ? 0 : 1)) * part_floats(NTOK) + t * 128 + c4))
                                : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
+          for (int x = 0; x < 12; ++x) {
             s.x += v[x].x;
             s.y += v[x].y;
             s.z += v[x].z;
@@ -730,6 +829,11 @@ cudaError_t launch_ntok(const MoeParams& p, const UpMaps& up, const DownMaps& do
   e = ensure_smem_attr(moe_down_kernel<NTOK>, DownCfg<NTOK>::kSmem, done_down);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(sms < kMaxCtas ? sms : kMaxCtas)), block(kThreads);
+  if (NTOK > 16) {
+    const unsigned ctas = static_cast<unsigned>((p.T + kRouteWarps - 1) / kRouteWarps);
+    e = launch_pdl(moe_route_kernel, dim3(ctas), dim3(32 * kRouteWarps), 0, s, p);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_pdl(moe_up_kernel<NTOK>, grid, block, UpCfg<NTOK>::kSmem, s, up, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(moe_down_kernel<NTOK>, grid, block, DownCfg<NTOK>::kSmem, s, down, p);
@@ -748,20 +852,25 @@ cudaError_t launch_moe(const MoeParams& p, int sms, cudaStream_t s) {
   // Experts are the third dimension; a map of one expert keeps it (its second index is never
   // loaded), so that the kernels have one form.
   const uint64_t experts = p.E > 1 ? p.E : 2;
-  auto stride = [&](int64_t given, int64_t rows, int64_t ld) {
-    return static_cast<uint64_t>(p.E > 1 ? given : rows * ld);
+  auto weights = [&](CUtensorMap* map, const uint16_t* w, int64_t rows, int64_t cols, int64_t ld, int64_t stride) {
+    if (p.E == 1) stride = rows * ld;
+    // Rows that start on 256-byte lines are read in whole ones.  Otherwise L2 is to fetch the
+    // sectors asked for only: with 256-byte fetches the two ends of every row's 256 bytes bring
+    // lines of which little is used before they are gone (rows of 2000 bytes: 868 MB read for 500).
+    const bool lines = reinterpret_cast<uintptr_t>(w) % 256 == 0 && ld % 128 == 0 && stride % 128 == 0;
+    return make_tile_map_l2(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, cols, rows, ld, experts, stride, 64, BK,
+                         CU_TENSOR_MAP_SWIZZLE_128B, 1,
+                         lines ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE);
   };
   UpMaps up;
   DownMaps down;
   const int ntok = ntok_of(p.T);
   const uint8_t* z = static_cast<const uint8_t*>(p.ws) + z_at(p.T);
-  if (!make_bf16_map(&up.wg, p.Wg, p.I, p.K, p.ldwg, experts, stride(p.strideWg, p.K, p.ldwg), 64, BK) ||
-      !make_bf16_map(&up.wu, p.Wu, p.I, p.K, p.ldwu, experts, stride(p.strideWu, p.K, p.ldwu), 64, BK) ||
+  if (!weights(&up.wg, p.Wg, p.K, p.I, p.ldwg, p.strideWg) || !weights(&up.wu, p.Wu, p.K, p.I, p.ldwu, p.strideWu) ||
+      !weights(&down.wd, p.Wd, p.I, p.K, p.ldwd, p.strideWd) ||
       !make_bf16_map(&up.x, p.X, p.K, p.T, p.ldx, 1, 0, BK, ntok) ||
-      !make_bf16_map(&up.wd, p.Wd, p.K, p.I, p.ldwd, experts, stride(p.strideWd, p.I, p.ldwd), 64, BK) ||
       !make_bf16_map(&down.z, z, p.I, p.T * p.top, ldz_of(p.I), 1, 0, BK, 16))
     return cudaErrorInvalidValue;
-  down.wd = up.wd;
   return ntok == 16 ? launch_ntok<16>(p, up, down, sms, s)
                     : ntok == 32 ? launch_ntok<32>(p, up, down, sms, s) : launch_ntok<64>(p, up, down, sms, s);
 }

@@ -203,9 +203,9 @@ dg_status moe_bf16(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top, int3
   if (ldx < K || ldl < E || ldwg < I || ldwu < I || ldwd < K || ldy < K) return DG_ERR_INVALID_ARG;
   if (E > 1 && (strideWg < K * ldwg || strideWu < K * ldwu || strideWd < I * ldwd)) return DG_ERR_INVALID_ARG;
   if (T > 64 || top > 16 || E > 512 || K > INT32_MAX || I > INT32_MAX) return DG_ERR_UNSUPPORTED;
-  {  // units of 64 x 64 (128) weights of the experts that T tokens can reach, counted in 31 bits
-    const int64_t reach = E < T * top ? E : T * top, kb = (K + 63) / 64, ib = (I + 63) / 64;
-    if (kb > INT32_MAX / ib / reach) return DG_ERR_UNSUPPORTED;
+  {  // units of 64 x 128 weights of all experts, counted in 31 bits
+    const int64_t kb = (K + 63) / 64, ib = (I + 63) / 64;
+    if (kb > INT32_MAX / ib / E) return DG_ERR_UNSUPPORTED;
   }
   if (!workspace || workspace_bytes < moe_ws_bytes(T, I, top)) return DG_ERR_INVALID_ARG;
   if (!aligned(X, 16) || !aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(Wd, 16) || ldx % 8 || ldwg % 8 ||

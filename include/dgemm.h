@@ -390,8 +390,7 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
  *   - workspace: see above; dg_moe_workspace_bytes (0 for sizes it does not take).
  *   - Errors: negative sizes, I == 0, top outside 1..E, short strides, null pointers, a
  *     workspace that is too small DG_ERR_INVALID_ARG; T > 64, top > 16, E > 512, K or I over
- *     2^31 - 1 or 2^31 or more blocks of 64 x 64 weights in the experts that T tokens can
- *     choose DG_ERR_UNSUPPORTED; X or a weight not 16-byte aligned, their strides not
+ *     2^31 - 1 or E matrices of 2^31 or more blocks of 64 x 64 DG_ERR_UNSUPPORTED; X or a weight not 16-byte aligned, their strides not
  *     multiples of 8, workspace not 256-byte aligned DG_ERR_MISALIGNED.  T == 0 or K == 0:
  *     nothing.
  */
