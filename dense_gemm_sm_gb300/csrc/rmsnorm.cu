@@ -109,56 +109,56 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p, const
   const R* res = kRes ? static_cast<const R*>(p.R) + r * p.ldr : nullptr;
   R* hout = kRes ? static_cast<R*>(p.H) + r * p.ldh : nullptr;
   YT* y = static_cast<YT*>(p.Y) + r * p.ldy;
-  const int64_t cols = p.cols;
+  const int cols = static_cast<int>(p.cols);
+  // An index of this thread's element j of chunk i.
+  auto at = [&](int i, int j) { return VEC ? (i * tpr + t) * 8 + j : (8 * i + j) * tpr + t; };
   float h[C][8];
-  float w[C][8];
-  // All loads first: h and gain.
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    const int64_t c0 = (static_cast<int64_t>(i) * tpr + t) * 8;
-    if (VEC && c0 + 8 <= cols) {
-      load8(x + c0, h[i]);
-      load8(p.gain + c0, w[i]);
+    if (VEC && at(i, 8) <= cols) {
+      load8(x + at(i, 0), h[i]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t c = VEC ? c0 + j : static_cast<int64_t>(8 * i + j) * tpr + t;
-        h[i][j] = c < cols ? load1(x + c) : 0.f;
-        w[i][j] = c < cols ? load1(p.gain + c) : 0.f;
-      }
+      for (int j = 0; j < 8; ++j) h[i][j] = at(i, j) < cols ? load1(x + at(i, j)) : 0.f;
     }
   }
   if (kRes) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int64_t c0 = (static_cast<int64_t>(i) * tpr + t) * 8;
-      if (VEC && c0 + 8 <= cols) {
-        float v[8];
-        load8(res + c0, v);
+      float v[8];
+      if (VEC && at(i, 8) <= cols) {
+        load8(res + at(i, 0), v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] += v[j];
-        store8(hout + c0, h[i]);
+        store8(hout + at(i, 0), h[i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t c = VEC ? c0 + j : static_cast<int64_t>(8 * i + j) * tpr + t;
-          if (c < cols) {
-            h[i][j] += load1(res + c);
-            store1(hout + c, h[i][j]);
+        for (int j = 0; j < 8; ++j)
+          if (at(i, j) < cols) {
+            h[i][j] += load1(res + at(i, j));
+            store1(hout + at(i, j), h[i][j]);
           }
-        }
       }
     }
   }
+  // The gain multiplies at once: h itself is not needed again.
   float sum = 0.f, top = 0.f;
 #pragma unroll
-  for (int i = 0; i < C; ++i)
+  for (int i = 0; i < C; ++i) {
+    float w[8];
+    if (VEC && at(i, 8) <= cols) {
+      load8(p.gain + at(i, 0), w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = at(i, j) < cols ? load1(p.gain + at(i, j)) : 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       sum = fmaf(h[i][j], h[i][j], sum);
-      h[i][j] *= w[i][j];
+      h[i][j] *= w[j];
       if (kCodes) top = fmaxf(top, fabsf(h[i][j]));
     }
+  }
   row_reduce(sum, top, cta, scratch);
   float f = 1.f / sqrtf(sum / static_cast<float>(cols) + p.eps);
   float inv = 1.f;
@@ -169,17 +169,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p, const
   }
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    const int64_t c0 = (static_cast<int64_t>(i) * tpr + t) * 8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[i][j] = kCodes ? h[i][j] * f * inv : h[i][j] * f;
-    if (VEC && c0 + 8 <= cols) {
-      store8(y + c0, h[i]);
+    if (VEC && at(i, 8) <= cols) {
+      store8(y + at(i, 0), h[i]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t c = VEC ? c0 + j : static_cast<int64_t>(8 * i + j) * tpr + t;
-        if (c < cols) store1(y + c, h[i][j]);
-      }
+      for (int j = 0; j < 8; ++j)
+        if (at(i, j) < cols) store1(y + at(i, j), h[i][j]);
     }
   }
 }
@@ -226,18 +223,23 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormParams p) 
 template <typename XT, typename RT, typename YT>
 cudaError_t launch_typed(const NormParams& p, bool vec, cudaStream_t s) {
   const int64_t chunks = (p.cols + 7) / 8;
-  if (chunks > 4 * 1024)
+  // Chunks a thread: 1 for as long as a CTA holds the row (16384 x 4096 with an FP32 residual:
+  // 107 us, 118 with 2, 124 with 4), except that rows of up to 512 elements then fit a warp with
+  // 2 (16384 x 512: 17.3 us in CTAs of 64 threads, 13.8 so); over 8192 elements 4 (2048 x 16384:
+  // 58 us, 65 with 2).  Unaligned rows over 8192 elements take the two-pass kernel: an element at
+  // a time, more than 8 do not stay in registers.
+  if (chunks > (vec ? 4 : 1) * 1024)
     return launch_pdl(rmsnorm_long_kernel<XT, RT, YT>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, s, p);
-  const int c = chunks > 1024 ? 4 : 1;
+  const int c = !vec ? 1 : chunks > 1024 ? 4 : chunks > 32 && chunks <= 64 ? 2 : 1;
   int tpr = static_cast<int>((chunks + c - 1) / c);
   tpr = (tpr + 31) / 32 * 32;
   const int rows_per_cta = tpr == 32 ? 8 : 1;
   const dim3 grid(static_cast<unsigned>((p.rows + rows_per_cta - 1) / rows_per_cta)), block(tpr * rows_per_cta);
   if (vec)
-    return c == 1 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, true, 1>, grid, block, 0, s, p, tpr)
-                  : launch_pdl(rmsnorm_kernel<XT, RT, YT, true, 4>, grid, block, 0, s, p, tpr);
-  return c == 1 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, false, 1>, grid, block, 0, s, p, tpr)
-                : launch_pdl(rmsnorm_kernel<XT, RT, YT, false, 4>, grid, block, 0, s, p, tpr);
+    return c == 1   ? launch_pdl(rmsnorm_kernel<XT, RT, YT, true, 1>, grid, block, 0, s, p, tpr)
+           : c == 2 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, true, 2>, grid, block, 0, s, p, tpr)
+                    : launch_pdl(rmsnorm_kernel<XT, RT, YT, true, 4>, grid, block, 0, s, p, tpr);
+  return launch_pdl(rmsnorm_kernel<XT, RT, YT, false, 1>, grid, block, 0, s, p, tpr);
 }
 
 template <typename XT, typename RT>
