@@ -208,7 +208,13 @@ struct Shared {
   uint8_t has_head[kWarps], has_tail[kWarps];
   Cut fin[2];                  // items of other CTAs too, for which this CTA came last
   uint32_t last[2];
-  int32_t runs, run_first[kWarps + 1], run_last[kWarps + 1], run_head[kWarps + 1];
+  int32_t runs;
+  struct Run {
+    int8_t first, last, head;  // warps of its tails (first < 0: none) and its head (< 0: none)
+    int8_t slot;               // -1: the item is this CTA's alone, else the CTA's part that this is
+  } run[kWarps + 1];
+  // Where a row of a run's item (and of fin's) goes in O; -1: no such row.
+  int64_t row_at[kWarps + 1][8 * NT], fin_at[2][8 * NT];
   uint32_t abort;
 };
 
@@ -695,14 +701,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   };
   float* cta_parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kCounterBytes) +
                      static_cast<int64_t>(kMaxCtas) * kWarps * C::kPart;
-  auto place = [&](const Cut& cut, int row, int c) {  // output of a row of the item, column c
+  // Element offset in O of a row of the item, -1 past its rows.
+  auto row_of = [&](const Cut& cut, int row) -> int64_t {
     const int head = cut.item / qblocks, rr = (cut.item - head * qblocks) * C::kRows + row;
-    return p.O + static_cast<int64_t>(cut.b) * p.strideO + static_cast<int64_t>(rr / p.group) * p.ldo +
-           (static_cast<int64_t>(head) * p.group + rr % p.group) * D + c;
-  };
-  auto rows_of = [&](const Cut& cut) {
-    const int left = rows_all - cut.item % qblocks * C::kRows;
-    return left < C::kRows ? left : C::kRows;
+    if (rr >= rows_all) return -1;
+    return static_cast<int64_t>(cut.b) * p.strideO + static_cast<int64_t>(rr / p.group) * p.ldo +
+           (static_cast<int64_t>(head) * p.group + rr % p.group) * D;
   };
   if (warp == 0) {
     // Bit w: warp w has a tail, a head.  A run ends at a head, or (the last) after the last
@@ -716,46 +720,57 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const uint32_t own = tails & ~(before ? (1u << (31 - __clz(before))) - 1 : 0u);
     const uint32_t run_tails = own & (upto >> 1);
     if (is_head) {
-      const int run = __popc(before);
-      sh.run_first[run] = run_tails ? __ffs(run_tails) - 1 : -1;
-      sh.run_last[run] = 31 - __clz(run_tails);
-      sh.run_head[run] = lane;
+      auto& run = sh.run[__popc(before)];
+      run.first = static_cast<int8_t>(__ffs(run_tails) - 1);
+      run.last = static_cast<int8_t>(31 - __clz(run_tails));
+      run.head = static_cast<int8_t>(lane);
     }
     if (lane == kWarps) {  // what is left after the last head
-      const int run = __popc(heads);
-      sh.run_first[run] = own ? __ffs(own) - 1 : -1;
-      sh.run_last[run] = 31 - __clz(own);
-      sh.run_head[run] = -1;
-      sh.runs = run + (own ? 1 : 0);
+      auto& run = sh.run[__popc(heads)];
+      run.first = static_cast<int8_t>(__ffs(own) - 1);
+      run.last = static_cast<int8_t>(31 - __clz(own));
+      run.head = -1;
+      sh.runs = __popc(heads) + (own ? 1 : 0);
     }
   }
   __syncthreads();
-  const int outs_max = (rows_all < C::kRows ? rows_all : C::kRows) * (D / 4);
+  // What an output needs of its run and row is worked out once: with the divisions in every
+  // output the join of a batch of ragged sequences took 8 us of its 48.
 #pragma unroll 1
-  for (int i = tid; i < sh.runs * outs_max; i += kThreads) {
-    const int run = i / outs_max, at = i - run * outs_max, row = at / (D / 4), c = at % (D / 4) * 4;
-    const int ft = sh.run_first[run], lt = sh.run_last[run], eh = sh.run_head[run];
-    const Cut cut = ft >= 0 ? sh.tail[ft] : sh.head[eh];
-    if (row >= rows_of(cut)) continue;
+  for (int i = tid; i < sh.runs * C::kRows; i += kThreads) {
+    auto& run = sh.run[i / C::kRows];
+    const Cut& cut = run.first >= 0 ? sh.tail[run.first] : sh.head[run.head];
+    sh.row_at[i / C::kRows][i % C::kRows] = row_of(cut, i % C::kRows);
+    // Slot 0: the item began in an earlier CTA.
+    if (i % C::kRows == 0)
+      run.slot = cut.first >= cta_r0 && cut.first + cut.units <= cta_r1 ? -1 : (cut.first >= cta_r0 ? 1 : 0);
+  }
+  __syncthreads();
+  // An output of four columns a thread.
+  constexpr int kOuts = C::kRows * (D / 4);
+#pragma unroll 1
+  for (int i = tid; i < sh.runs * kOuts; i += kThreads) {
+    const int at = i % kOuts, row = at / (D / 4), c = at % (D / 4) * 4;
+    const int64_t to = sh.row_at[i / kOuts][row];
+    if (to < 0) continue;
+    const auto run = sh.run[i / kOuts];
     Sum s;
-    if (ft >= 0)
+    if (run.first >= 0)
 #pragma unroll 1
-      for (int v = ft; v <= lt; ++v)
+      for (int v = run.first; v <= run.last; ++v)
         if (sh.has_tail[v]) {
           const float* q = tail_part(v);
           s.add(q[C::kRows * D + row], q[C::kRows * D + C::kRows + row],
                 *reinterpret_cast<const float4*>(q + row * D + c));
         }
-    if (eh >= 0) {
-      const float* q = head_part(eh);
-      // Either memory; stores of this CTA's own warps, ordered by its barrier.
+    if (run.head >= 0) {  // either memory; stores of this CTA's own warps, ordered by its barrier
+      const float* q = head_part(run.head);
       s.add(q[C::kRows * D + row], q[C::kRows * D + C::kRows + row], *reinterpret_cast<const float4*>(q + row * D + c));
     }
-    if (cut.first >= cta_r0 && cut.first + cut.units <= cta_r1) {
-      *reinterpret_cast<uint2*>(place(cut, row, c)) = s.value();
+    if (run.slot < 0) {
+      *reinterpret_cast<uint2*>(p.O + to + c) = s.value();
     } else {
-      // Slot 0: the item began in an earlier CTA.
-      float* out = cta_parts + (2 * static_cast<int64_t>(blockIdx.x) + (cut.first >= cta_r0 ? 1 : 0)) * C::kPart;
+      float* out = cta_parts + (2 * static_cast<int64_t>(blockIdx.x) + run.slot) * C::kPart;
       __stcg(reinterpret_cast<float4*>(out + row * D + c), s.v);
       if (c == 0) {
         __stcg(out + C::kRows * D + row, s.m);
@@ -766,45 +781,51 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   __syncthreads();  // before the tickets: their release covers the CTA's stores
   // Only the first and the last run can be of an item of other CTAs too.
   if (tid == 0 || (tid == 32 && sh.runs > 1)) {
-    const int run = tid == 0 ? 0 : sh.runs - 1;
-    if (sh.runs > 0) {
-      const Cut cut = sh.run_first[run] >= 0 ? sh.tail[sh.run_first[run]] : sh.head[sh.run_head[run]];
-      if (cut.first < cta_r0 || cut.first + cut.units > cta_r1) {
-        // A CTA is the first one of at most one item that goes on after it: its counter is that
-        // item's.
-        const uint32_t k0 = split.worker(cut.first) / kWarps, k1 = split.worker(cut.first + cut.units - 1) / kWarps;
-        uint32_t* counter = static_cast<uint32_t*>(p.ws) + k0;
-        if (take_ticket(counter) == k1 - k0) {
-          *counter = 0;  // every contributor has its ticket: ready for the next call
-          const int slot = cut.first >= cta_r0 ? 1 : 0;
-          sh.fin[slot] = cut;
-          sh.last[slot] = 1;
-        }
+    const auto run = sh.run[tid == 0 ? 0 : sh.runs - 1];
+    if (sh.runs > 0 && run.slot >= 0) {
+      const Cut cut = run.first >= 0 ? sh.tail[run.first] : sh.head[run.head];
+      // A CTA is the first one of at most one item that goes on after it: that item's counter is
+      // the first CTA's.
+      const uint32_t k0 = split.worker(cut.first) / kWarps, k1 = split.worker(cut.first + cut.units - 1) / kWarps;
+      uint32_t* counter = static_cast<uint32_t*>(p.ws) + k0;
+      if (take_ticket(counter) == k1 - k0) {
+        *counter = 0;  // every contributor has its ticket: ready for the next call
+        sh.fin[run.slot] = cut;
+        sh.last[run.slot] = 1;
       }
     }
   }
   __syncthreads();
+  if (!sh.last[0] && !sh.last[1]) return;
 
+  constexpr int kBatch = 8;  // parts asked for together
   // ---- items cut between CTAs whose last part was this CTA's: every thread takes an output of
   // four columns, groups of threads the CTAs in turn
+#pragma unroll 1
+  for (int i = tid; i < 2 * C::kRows; i += kThreads)
+    if (sh.last[i / C::kRows]) sh.fin_at[i / C::kRows][i % C::kRows] = row_of(sh.fin[i / C::kRows], i % C::kRows);
+  __syncthreads();
 #pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
     if (!sh.last[slot]) continue;
     const Cut cut = sh.fin[slot];
     const uint32_t k0 = split.worker(cut.first) / kWarps, k1 = split.worker(cut.first + cut.units - 1) / kWarps;
-    const int outs = rows_of(cut) * (D / 4);
-    const int groups = outs < kThreads ? kThreads / outs : 1;
+    // Many parts: groups of threads take them in turn, and join through shared memory.
+    constexpr int kGroups = kOuts < C::kThreads ? C::kThreads / kOuts : 1;
+    const int groups = k1 - k0 + 1 > kBatch ? kGroups : 1;
     float* mid = reinterpret_cast<float*>(smem);  // [thread][6]
 #pragma unroll 1
-    for (int i = tid; i < groups * outs; i += kThreads) {
-      const int grp = i / outs, at = i - grp * outs, row = at / (D / 4), c = at % (D / 4) * 4;
+    for (int i = tid; i < groups * kOuts; i += kThreads) {
+      const int grp = i / kOuts, at = i % kOuts, row = at / (D / 4), c = at % (D / 4) * 4;
+      const int64_t to = sh.fin_at[slot][row];
+      if (to < 0) continue;
       Sum s;
 #pragma unroll 1
-      for (uint32_t k = k0 + grp; k <= k1; k += 4 * groups) {
-        float mk[4], lk[4];
-        float4 v[4];
+      for (uint32_t k = k0 + grp; k <= k1; k += kBatch * groups) {
+        float mk[kBatch], lk[kBatch];
+        float4 v[kBatch];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < kBatch; ++x) {
           const uint32_t kk = k + x * groups;
           const float* q = cta_parts + (2 * static_cast<int64_t>(kk) + (kk == k0 ? 1 : 0)) * C::kPart;
           const bool in = kk <= k1;
@@ -813,10 +834,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           v[x] = in ? __ldcg(reinterpret_cast<const float4*>(q + row * D + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s.add(mk[x], lk[x], v[x]);
+        for (int x = 0; x < kBatch; ++x) s.add(mk[x], lk[x], v[x]);
       }
       if (groups == 1) {
-        *reinterpret_cast<uint2*>(place(cut, row, c)) = s.value();
+        *reinterpret_cast<uint2*>(p.O + to + c) = s.value();
       } else {
         float* d = mid + tid * 6;
         d[0] = s.m;
@@ -829,13 +850,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     }
     if (groups > 1) {  // uniform over the CTA
       __syncthreads();
-      if (tid < outs) {
+      const int64_t to = tid < kOuts ? sh.fin_at[slot][tid / (D / 4)] : -1;
+      if (to >= 0) {
         Sum s;
         for (int x = 0; x < groups; ++x) {
-          const float* d = mid + (x * outs + tid) * 6;
+          const float* d = mid + (x * kOuts + tid) * 6;
           s.add(d[0], d[1], make_float4(d[2], d[3], d[4], d[5]));
         }
-        *reinterpret_cast<uint2*>(place(cut, tid / (D / 4), tid % (D / 4) * 4)) = s.value();
+        *reinterpret_cast<uint2*>(p.O + to + tid % (D / 4) * 4) = s.value();
       }
       __syncthreads();
     }
