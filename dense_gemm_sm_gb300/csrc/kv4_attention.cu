@@ -15,8 +15,10 @@
 //     one 32-bit register at a time); the 128 is taken out in FP32 afterwards, with the row's
 //     scale and zero:
 //       q . K_j = ks_j (q . (128 + kc_j)) + (kz_j - 128 ks_j) sum(q),
-//       O = sum_j P_j (128 + vc_j) + sum_j (p_j vz_j - 128 P_j),   P_j = bf16(p_j vs_j),
-//     where the last sum takes the rounded P_j, so the offsets cancel to FP32 rounding.
+//       O = sum_j P_j (128 + vc_j) - 136 sum_j P_j + sum_j p_j (vz_j + 8 vs_j),
+//     P_j = bf16(p_j vs_j).  The middle sum takes the rounded P_j: what the rounding of P
+//     multiplies is vc_j - 8, V's deviation from the middle of its range and not from its
+//     minimum (64 ragged sequences of normal rows: 0.0011 of O in the mean square, 0.0031 without).
 //   * the order of d in the first product and of keys in the second is free: K rows are read
 //     as they lie (a lane 16 bytes, two key rows), V's codes lie in the cache in fragment order.
 //   * P goes from the first product's output layout to the second's operand layout by
@@ -584,7 +586,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           // ---- P, and O += V^T P^T record by record
 #pragma unroll
           for (int r = 0; r < kRecs; ++r) {
-            const float s0 = lo_of(vp[r][0]), z0 = hi_of(vp[r][0]), s1 = lo_of(vp[r][1]), z1 = hi_of(vp[r][1]);
+            const float s0 = lo_of(vp[r][0]), s1 = lo_of(vp[r][1]);
+            const float z0 = fmaf(8.f, s0, hi_of(vp[r][0])), z1 = fmaf(8.f, s1, hi_of(vp[r][1]));
             uint32_t b0[NT], b1[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -629,7 +632,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], x);
             z[nt][e] += __shfl_xor_sync(~0u, z[nt][e], x);
           }
-          z[nt][e] = fmaf(-128.f, ps[nt][e], z[nt][e]);
+          z[nt][e] = fmaf(-136.f, ps[nt][e], z[nt][e]);
         }
       const bool ends = seg.u + n == seg.units;
       if (seg.u == 0 && ends) {
