@@ -46,21 +46,21 @@ SM_MAX_MHZ_NOMINAL = 2070.0      # only if MEASURED_PEAKS.json gives no maximum 
 # kernel's sources (kernel file, planner, headers) matches the one it was taken with.
 COMMON_SOURCES = ["api.cu", "dg_internal.h", "ptx.cuh", "tile_sched.h"]
 MEASURED_TRAFFIC = {
-    "sgemm_4096": {"bytes_per_launch": 388_868_608, "source_hash": "e90c5c171ec77a81"},
-    "sgemm_ragged": {"bytes_per_launch": 24_665_344, "source_hash": "e90c5c171ec77a81"},
-    "sgemm_256": {"bytes_per_launch": 554_240, "source_hash": "e90c5c171ec77a81"},
-    "ffn_bf16": {"bytes_per_launch": 150_730_752, "source_hash": "b49d157f5b547065"},
-    "ffn_gate_up": {"bytes_per_launch": 232_507_904, "source_hash": "b49d157f5b547065"},
-    "bf16_4096": {"bytes_per_launch": 131_843_328, "source_hash": "b49d157f5b547065"},
-    "qk_batched": {"bytes_per_launch": 1_078_787_584, "source_hash": "b49d157f5b547065"},
-    "decode_m1": {"bytes_per_launch": 104_879_616, "source_hash": "fcbaba222da94a3d"},
-    "decode_m4": {"bytes_per_launch": 105_319_424, "source_hash": "fcbaba222da94a3d"},
-    "decode_m16": {"bytes_per_launch": 105_675_520, "source_hash": "fcbaba222da94a3d"},
-    "decode_chain_m1": {"bytes_per_launch": 408_517_376, "source_hash": "2e8a06e855c12dd8"},
-    "attn_batched": {"bytes_per_launch": 116_075_008, "source_hash": "5c5fab7452fd54ff"},
-    "attn_causal_8k": {"bytes_per_launch": 6_360_064, "source_hash": "5c5fab7452fd54ff"},
-    "fp8_ffn": {"bytes_per_launch": 57_798_912, "source_hash": "2d2f1dc164bf18bc"},
-    "fp8_quant_gemm": {"bytes_per_launch": 23_177_472, "source_hash": "2d2f1dc164bf18bc", "quantiser_bytes_per_launch": 12_605_696},
+    "sgemm_4096": {"bytes_per_launch": 387_794_176, "source_hash": "29f25ed0a70b3557"},
+    "sgemm_ragged": {"bytes_per_launch": 24_566_784, "source_hash": "29f25ed0a70b3557"},
+    "sgemm_256": {"bytes_per_launch": 556_032, "source_hash": "29f25ed0a70b3557"},
+    "ffn_bf16": {"bytes_per_launch": 150_347_776, "source_hash": "46dfd6cccd1c4aa8"},
+    "ffn_gate_up": {"bytes_per_launch": 231_915_520, "source_hash": "46dfd6cccd1c4aa8"},
+    "bf16_4096": {"bytes_per_launch": 132_624_640, "source_hash": "46dfd6cccd1c4aa8"},
+    "qk_batched": {"bytes_per_launch": 1_078_796_032, "source_hash": "46dfd6cccd1c4aa8"},
+    "decode_m1": {"bytes_per_launch": 105_387_264, "source_hash": "0d3c1259779f0708"},
+    "decode_m4": {"bytes_per_launch": 105_303_552, "source_hash": "0d3c1259779f0708"},
+    "decode_m16": {"bytes_per_launch": 105_544_960, "source_hash": "0d3c1259779f0708"},
+    "decode_chain_m1": {"bytes_per_launch": 408_453_120, "source_hash": "0ead40f20b14b938"},
+    "attn_batched": {"bytes_per_launch": 115_548_160, "source_hash": "bb8ee1524c1d4b27"},
+    "attn_causal_8k": {"bytes_per_launch": 6_360_064, "source_hash": "bb8ee1524c1d4b27"},
+    "fp8_ffn": {"bytes_per_launch": 57_750_528, "source_hash": "bc41f0c1514dad40"},
+    "fp8_quant_gemm": {"bytes_per_launch": 23_177_728, "source_hash": "bc41f0c1514dad40", "quantiser_bytes_per_launch": 12_605_696},
 }
 
 
