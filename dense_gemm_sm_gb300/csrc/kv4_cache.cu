@@ -8,12 +8,14 @@
 // and codes 0.
 //
 // HBM-bound: 4 d bytes of K and V on one side, d + 8 on the other, per (token, head).  A warp
-// takes one token and a run of its heads, four at a time with their loads together: lanes 0-15
+// takes one token and a run of its heads, several at a time with their loads together: lanes 0-15
 // the key's row, lanes 16-31 the value's, d / 16 elements a lane (16-byte accesses at d = 128).
-// What a token needs once (its slot's page) is found once, and quotients come from a reciprocal,
-// with the division itself only where its rounding could decide: a warp per (token, head) with
-// 64-bit indices and true divisions issued 450 instructions for each and took 25 us for 8192
-// tokens of 8 heads, which are 6 us of HBM traffic.
+// Writing is bound by its instructions, so they are few: what a token needs once (its slot's
+// page) is found once; minimum and maximum are reduced together as one BF16 pair (maximum,
+// -minimum); quotients come from a reciprocal, correctly rounded by one step with their exact
+// remainder; codes are put together by FP32 multiply-adds.  8192 tokens of 8 heads written and
+// read back: 51 us with a warp per (token, head), 64-bit indices and the compiler's divisions
+// (450 instructions for each), 32 us with a reciprocal whose halves were set right afterwards.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -48,6 +50,26 @@ __device__ __forceinline__ uint8_t* record_of(const Kv4Params& p, int64_t slot, 
   return p.data + (page * p.heads * (p.page_size / kKv4Tokens) + (in >> 4)) * kv4_record_bytes(D);
 }
 
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// a / b rounded to nearest, for y = 1 / b rounded to nearest: the quotient's approximation a y
+// corrected by its remainder, which is exact (P. Markstein, "Computation of elementary functions
+// on the IBM RISC System/6000 processor", 1990: right unless all bits of b's significand are set;
+// no intermediate result may underflow).
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+  const float q = a * y;
+  return fmaf(fmaf(-q, b, a), y, q);
+}
+
 // H: heads of a token in flight; a warp's run of heads is a multiple of it.
 template <int D, bool VEC, int H>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Params p, const int heads_per_warp) {
@@ -70,6 +92,10 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Params p,
     const uint16_t* row = (is_v ? p.V + token * p.ldv : p.K + token * p.ldk) + l * N;
     int u;
     uint8_t* rec0 = record_of<D>(p, slot, &u);
+    int piece[N / 4];
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j)
+      piece[j] = is_v ? 8 * D + v_piece<D>(u, l * (N / 4) + j) : u * (D / 2) + (l * (N / 4) + j) * 2;
     for (int h = h0; h < h1; h += H) {
       uint32_t w[H][N / 2];
 #pragma unroll
@@ -90,71 +116,52 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Params p,
       }
 #pragma unroll
       for (int x = 0; x < H; ++x) {
-        float v[N];
+        uint32_t hi2 = w[x][0], lo2 = w[x][0];
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-          v[2 * j] = __uint_as_float(w[x][j] << 16);
-          v[2 * j + 1] = __uint_as_float(w[x][j] & 0xFFFF0000u);
+        for (int j = 1; j < N / 2; ++j) {
+          hi2 = max2(hi2, w[x][j]);
+          lo2 = min2(lo2, w[x][j]);
         }
-        float lo = v[0], hi = v[0];
+        // (maximum, -minimum) of the lane's elements, then of the row.
+        uint32_t ext = max2(__byte_perm(hi2, lo2, 0x5410) ^ 0x80000000u, __byte_perm(hi2, lo2, 0x7632) ^ 0x80000000u);
 #pragma unroll
-        for (int j = 1; j < N; ++j) {
-          lo = fminf(lo, v[j]);
-          hi = fmaxf(hi, v[j]);
-        }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+        for (int o = 8; o > 0; o >>= 1) ext = max2(ext, __shfl_xor_sync(0xffffffffu, ext, o));
+        const float hi = __uint_as_float(ext << 16), lo = __uint_as_float((ext & 0xFFFF0000u) ^ 0x80000000u);
+        const float range = __fsub_rn(hi, lo);
+        const bool plain = range >= 1e-30f;  // nothing below underflows
+        const __nv_bfloat16 sb =
+            __float2bfloat16_rn(plain ? quotient(range, 15.f, 1.f / 15.f) : __fdiv_rn(range, 15.f));
         const float scale = __bfloat162float(sb);
-        // round(difference / scale), halves to even: n from the product by the reciprocal is the
-        // quotient's nearest integer or, next to a half, its neighbour.  The remainder d - n scale
-        // is exact, so t = 2 |remainder| - scale tells: positive, n is the wrong neighbour; zero,
-        // a half, where n has to be even.  (A quotient that is no half is never rounded to one:
-        // it differs by more than half an FP32 step, as d and scale have 24 and 8 bits.)  Halves
-        // are common, differences of BF16 values over a BF16 scale.
-        const float inv = __frcp_rn(scale);
-        constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-        float n[N], rem[N], worst = -1.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float d = __fsub_rn(v[j], lo);
-          n[j] = fmaf(d, inv, kRound) - kRound;
-          rem[j] = fmaf(-n[j], scale, d);
-          worst = fmaxf(worst, fmaf(2.f, fabsf(rem[j]), -scale));
-        }
-        uint32_t codes = 0;
-        if (!(scale >= 7.5e-37f)) {  // the reciprocal could overflow: the division itself
+        uint32_t codes;
+        if (plain) {
+          // A quotient is at most 15 (1 + 2^-8): rounded, at most 15.
+          const float inv = __frcp_rn(scale);
+          constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+          float n[N];
 #pragma unroll
           for (int j = 0; j < N; ++j) {
-            const float q = scale > 0.f ? rintf(__fdiv_rn(__fsub_rn(v[j], lo), scale)) : 0.f;
+            const float v = __uint_as_float(j & 1 ? w[x][j / 2] & 0xFFFF0000u : w[x][j / 2] << 16);
+            n[j] = (quotient(__fsub_rn(v, lo), scale, inv) + kRound) - kRound;
+          }
+#pragma unroll
+          for (int j = 0; j < N; j += 4) n[j] = fmaf(fmaf(n[j + 3], 16.f, n[j + 2]), 256.f, fmaf(n[j + 1], 16.f, n[j]));
+          // Four codes make an integer below 2^16: the low half of 2^23 + it.
+          codes = __float_as_uint(n[0] + 8388608.f) & 0xFFFFu;
+          if (N == 8) codes = __byte_perm(codes, __float_as_uint(n[N - 4] + 8388608.f), 0x5410);
+        } else {
+          codes = 0;
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float v = __uint_as_float(j & 1 ? w[x][j / 2] & 0xFFFF0000u : w[x][j / 2] << 16);
+            const float q = scale > 0.f ? rintf(__fdiv_rn(__fsub_rn(v, lo), scale)) : 0.f;
             codes |= static_cast<uint32_t>(fminf(fmaxf(q, 0.f), 15.f)) << (4 * j);
           }
-        } else {
-          if (worst >= 0.f) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-              const float t = fmaf(2.f, fabsf(rem[j]), -scale);
-              const bool odd = __float_as_uint(n[j] + kRound) & 1u;
-              if (t > 0.f || (t == 0.f && odd)) n[j] += rem[j] > 0.f ? 1.f : -1.f;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < N; ++j)
-            codes |= (__float_as_uint(fminf(n[j], 15.f) + kRound) & 15u) << (4 * j);
         }
+        // Pieces of two bytes (four columns): a K row's lie together, V's in its own order.
         uint8_t* rec = rec0 + (h + x) * stride;
-        if (!is_v) {
-          if (N == 8) *reinterpret_cast<uint32_t*>(rec + u * (D / 2) + l * 4) = codes;
-          else *reinterpret_cast<uint16_t*>(rec + u * (D / 2) + l * 2) = static_cast<uint16_t>(codes);
-        } else {
 #pragma unroll
-          for (int j = 0; j < N / 4; ++j)
-            *reinterpret_cast<uint16_t*>(rec + 8 * D + v_piece<D>(u, l * (N / 4) + j)) =
-                static_cast<uint16_t>(codes >> (16 * j));
-        }
+        for (int j = 0; j < N / 4; ++j)
+          *reinterpret_cast<uint16_t*>(rec + piece[j]) = static_cast<uint16_t>(codes >> (16 * j));
         if (l == 0)
           *reinterpret_cast<uint32_t*>(rec + 16 * D + (is_v ? 64 : 0) + u * 4) =
               static_cast<uint32_t>(__bfloat16_as_ushort(sb)) | (__float_as_uint(lo) & 0xFFFF0000u);
@@ -181,6 +188,10 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4Params p,
     int u = 0;
     const uint8_t* rec0 = have ? record_of<D>(p, slot, &u) : p.data;
     uint16_t* row = (is_v ? p.V + token * p.ldv : p.K + token * p.ldk) + l * N;
+    int piece[N / 4];
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j)
+      piece[j] = is_v ? 8 * D + v_piece<D>(u, l * (N / 4) + j) : u * (D / 2) + (l * (N / 4) + j) * 2;
     for (int h = h0; h < h1; h += H) {
       uint32_t codes[H], prm[H];
 #pragma unroll
@@ -188,16 +199,9 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4Params p,
         codes[x] = prm[x] = 0;  // the value 0
         if (!have) continue;
         const uint8_t* rec = rec0 + (h + x) * stride;
-        if (!is_v) {
-          if (N == 8) codes[x] = *reinterpret_cast<const uint32_t*>(rec + u * (D / 2) + l * 4);
-          else codes[x] = *reinterpret_cast<const uint16_t*>(rec + u * (D / 2) + l * 2);
-        } else {
 #pragma unroll
-          for (int j = 0; j < N / 4; ++j)
-            codes[x] |= static_cast<uint32_t>(
-                            *reinterpret_cast<const uint16_t*>(rec + 8 * D + v_piece<D>(u, l * (N / 4) + j)))
-                        << (16 * j);
-        }
+        for (int j = 0; j < N / 4; ++j)
+          codes[x] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(rec + piece[j])) << (16 * j);
         prm[x] = *reinterpret_cast<const uint32_t*>(rec + 16 * D + (is_v ? 64 : 0) + u * 4);
       }
 #pragma unroll
@@ -233,14 +237,14 @@ struct Shape {
   dim3 grid;
   int heads_per_warp, in_flight;
 };
-Shape shape_of(const Kv4Params& p, int sms) {
+Shape shape_of(const Kv4Params& p, int sms, int most) {
   const int64_t slots = static_cast<int64_t>(sms) * 64;  // resident warps
   int64_t runs = slots / (p.tokens < slots ? p.tokens : slots);
   if (runs > p.heads) runs = p.heads;
   Shape s;
   s.heads_per_warp = static_cast<int>((p.heads + runs - 1) / runs);
-  s.in_flight = p.heads % 4 == 0 && s.heads_per_warp >= 4 ? 4 : 1;
-  if (s.in_flight == 4) s.heads_per_warp = (s.heads_per_warp + 3) / 4 * 4;
+  s.in_flight = p.heads % most == 0 && s.heads_per_warp >= most ? most : p.heads % 4 == 0 && s.heads_per_warp >= 4 ? 4 : 1;
+  s.heads_per_warp = (s.heads_per_warp + s.in_flight - 1) / s.in_flight * s.in_flight;
   const int64_t need = (p.tokens + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<int64_t>(sms) * 8;
   s.grid = dim3(static_cast<unsigned>(need < cap ? need : cap),
                 static_cast<unsigned>((p.heads + s.heads_per_warp - 1) / s.heads_per_warp));
@@ -249,22 +253,25 @@ Shape shape_of(const Kv4Params& p, int sms) {
 
 }  // namespace
 
-#define DG_KV4_LAUNCH(KERNEL, D, VEC)                                                              \
-  (f.in_flight == 4 ? launch_pdl(KERNEL<D, VEC, 4>, f.grid, b, 0, s, p, f.heads_per_warp)        \
-                    : launch_pdl(KERNEL<D, VEC, 1>, f.grid, b, 0, s, p, f.heads_per_warp))
+#define DG_KV4_LAUNCH(KERNEL, D, VEC, MOST)                                                           \
+  (f.in_flight == MOST ? launch_pdl(KERNEL<D, VEC, MOST>, f.grid, b, 0, s, p, f.heads_per_warp)     \
+   : f.in_flight == 4  ? launch_pdl(KERNEL<D, VEC, 4>, f.grid, b, 0, s, p, f.heads_per_warp)        \
+                       : launch_pdl(KERNEL<D, VEC, 1>, f.grid, b, 0, s, p, f.heads_per_warp))
 
 cudaError_t launch_kv4_append(const Kv4Params& p, int d, bool vec, int sms, cudaStream_t s) {
-  const Shape f = shape_of(p, sms);
+  const Shape f = shape_of(p, sms, 4);
   const dim3 b(kThreads);
-  if (d == 128) return vec ? DG_KV4_LAUNCH(kv4_append_kernel, 128, true) : DG_KV4_LAUNCH(kv4_append_kernel, 128, false);
-  return vec ? DG_KV4_LAUNCH(kv4_append_kernel, 64, true) : DG_KV4_LAUNCH(kv4_append_kernel, 64, false);
+  if (d == 128)
+    return vec ? DG_KV4_LAUNCH(kv4_append_kernel, 128, true, 4) : DG_KV4_LAUNCH(kv4_append_kernel, 128, false, 4);
+  return vec ? DG_KV4_LAUNCH(kv4_append_kernel, 64, true, 4) : DG_KV4_LAUNCH(kv4_append_kernel, 64, false, 4);
 }
 
 cudaError_t launch_kv4_gather(const Kv4Params& p, int d, bool vec, int sms, cudaStream_t s) {
-  const Shape f = shape_of(p, sms);
+  const Shape f = shape_of(p, sms, 8);
   const dim3 b(kThreads);
-  if (d == 128) return vec ? DG_KV4_LAUNCH(kv4_gather_kernel, 128, true) : DG_KV4_LAUNCH(kv4_gather_kernel, 128, false);
-  return vec ? DG_KV4_LAUNCH(kv4_gather_kernel, 64, true) : DG_KV4_LAUNCH(kv4_gather_kernel, 64, false);
+  if (d == 128)
+    return vec ? DG_KV4_LAUNCH(kv4_gather_kernel, 128, true, 8) : DG_KV4_LAUNCH(kv4_gather_kernel, 128, false, 8);
+  return vec ? DG_KV4_LAUNCH(kv4_gather_kernel, 64, true, 8) : DG_KV4_LAUNCH(kv4_gather_kernel, 64, false, 8);
 }
 #undef DG_KV4_LAUNCH
 

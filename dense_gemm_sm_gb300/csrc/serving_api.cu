@@ -60,7 +60,7 @@ dg_status check_cache(const dg_kv4_cache* c) {
   if (!c || c->pages < 0 || c->page_size <= 0 || c->heads <= 0 || c->d <= 0) return DG_ERR_INVALID_ARG;
   if (c->page_size % kKv4Tokens != 0) return DG_ERR_INVALID_ARG;
   if (c->d != 64 && c->d != 128) return DG_ERR_UNSUPPORTED;
-  if (c->page_size > 4096 || c->heads > 65536 || c->pages > INT32_MAX) return DG_ERR_UNSUPPORTED;
+  if (c->page_size > 4096 || c->heads > 4096 || c->pages > INT32_MAX) return DG_ERR_UNSUPPORTED;
   if (c->pages > 0 && !c->data) return DG_ERR_INVALID_ARG;
   if (!aligned(c->data, 16)) return DG_ERR_MISALIGNED;
   return DG_OK;

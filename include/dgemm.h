@@ -313,8 +313,8 @@ dg_status rmsnorm_residual_e4m3(int64_t rows, int64_t cols, const void* X, int64
  *     16 words, 16 words    K's and V's scale (low half) and zero (high half)
  * so that one copy brings a whole record, and V's codes lie as the tensor-core operand wants
  * them.  Token t of a page is slot page * page_size + t.  What unused slots hold is never
- * interpreted.  page_size is a multiple of 16, at most 4096; d is 64 or 128; data
- * 16-byte aligned.
+ * interpreted.  page_size is a multiple of 16, at most 4096; heads at most 4096; d
+ * is 64 or 128; data 16-byte aligned.
  */
 typedef struct {
   uint8_t* data;
@@ -331,7 +331,7 @@ int64_t dg_kv4_block_bytes(int32_t page_size, int32_t d);
  * cache is passed over and reported (DG_ERR_BAD_INDEX from dg_device_status).  Slots of one
  * call are distinct.
  * Errors: null pointers, short strides, a page size that is not a positive multiple of 16
- * DG_ERR_INVALID_ARG; another d or a larger page DG_ERR_UNSUPPORTED; data not 16-byte, slots not 8-byte or K
+ * DG_ERR_INVALID_ARG; another d, a larger page or more heads DG_ERR_UNSUPPORTED; data not 16-byte, slots not 8-byte or K
  * or V not 2-byte aligned DG_ERR_MISALIGNED.  tokens == 0: nothing.
  */
 dg_status kv4_append(const dg_kv4_cache* cache, int64_t tokens, const uint16_t* K, int64_t ldk,

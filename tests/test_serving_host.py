@@ -39,7 +39,7 @@ def cache(data=P, pages=8, page_size=32, heads=2, d=128):
 
 @pytest.mark.parametrize("c,status", [
     (dict(pages=-1), INV), (dict(page_size=0), INV), (dict(page_size=24), INV), (dict(heads=0), INV), (dict(d=0), INV),
-    (dict(data=None), INV), (dict(d=96), UNS), (dict(page_size=65552), UNS), (dict(pages=2 ** 31), UNS), (dict(data=P + 8), MIS)])
+    (dict(data=None), INV), (dict(d=96), UNS), (dict(page_size=4112), UNS), (dict(heads=4097), UNS), (dict(pages=2 ** 31), UNS), (dict(data=P + 8), MIS)])
 def test_cache_refuses(c, status):
     c = cache(**c)
     assert dg.kv4_append(c, 4, P, 256, P, 256, P, stream=0, check=False) == status
