@@ -379,9 +379,9 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
  * A mixture-of-experts layer for few tokens (T <= 64), from the router's logits on:
  *     p = softmax(logits[t]) over the E experts, the `top` largest logits chosen (ties: the
  *     lowest expert), w = p, or p over the sum of the chosen p when renorm is non-zero,
- *     Z = bf16(SiLU(X[t] Wg[e]) * (X[t] Wu[e])),   Y[t] = bf16(sum over chosen e of w_e (Z Wd[e]))
- * with FP32 sums and the activation on the unrounded sums (Z's rounding makes it an operand;
- * gemm_bf16_gate_up_silu's two further roundings are not made).  A logit of -inf switches an
+ *     z = SiLU(X[t] Wg[e]) * (X[t] Wu[e]),   Y[t] = bf16(sum over chosen e of w_e (z Wd[e]))
+ * with FP32 sums and the activation on the unrounded sums; z enters the second product with 16
+ * significant bits, as two BF16 operands (gemm_bf16_gate_up_silu's roundings are not made).  A logit of -inf switches an
  * expert off: it is never computed, and a row of nothing else gives Y = 0.  NaN logits rank
  * as -inf.  +inf logits are not supported (unspecified weights).
  *   - X: T x K BF16.  logits: T x E FP32, row stride ldl (gemm_bf16 with DG_OUT_F32 makes

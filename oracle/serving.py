@@ -180,6 +180,7 @@ def moe(x, logits, wg, wu, wd, top, renorm):
             dz = 1.1 * dg * np.abs(u) + (np.abs(silu) + 1.1 * dg) * du + 8 * F32 * np.abs(z)
             awd = np.abs(wd[e]).astype(np.float64)
             y[t] += w * (z @ wd[e].astype(np.float64))
-            bound[t] += w * ((np.abs(z) * BF16 + dz * (1 + BF16)) @ awd) + \
+            # z enters as two BF16 numbers: the second's rounding is what is left.
+            bound[t] += w * ((np.abs(z) * BF16 ** 2 + dz * (1 + BF16)) @ awd) + \
                 w * (sum_err(I) + (len(chosen) + 32) * F32) * (np.abs(z) @ awd)
     return y, bound + BF16 * np.abs(y) + BF16 * bound
