@@ -62,7 +62,12 @@ struct Cfg {
   static constexpr int kStages = NT == 1 && D == 128 ? 3 : 4;
   static constexpr int kRing = kWarps * kStages * kUnitBytes;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kPart = kRows * (D + 2);                 // floats of a part: outputs, maxima, sums
+  // A part: rows of outputs, then the rows' maxima and their sums of weights.  Rows of 128 are
+  // padded: a warp's 16-byte stores would otherwise all start in two banks (one 8192-token
+  // sequence 12.4 us, 11.3 so; rows of 64 measured no better padded).
+  static constexpr int kPitch = D == 128 ? D + 4 : D;
+  static constexpr int kTop = kRows * kPitch, kSum = kTop + kRows;
+  static constexpr int kPart = kSum + kRows;
   static constexpr int kQ = NT == 4 ? NT * (D / 16) * 32 * 8 : 0;  // a warp's Q fragments (registers otherwise)
   static constexpr int kSmem = kRing + kWarps * kQ;
   static_assert(kWarps * kPart * 4 <= kRing, "the warps' last parts take the ring's place");
@@ -208,15 +213,14 @@ struct Shared {
   Walk start[kWarps];
   Cut head[kWarps], tail[kWarps];
   uint8_t has_head[kWarps], has_tail[kWarps];
-  Cut fin[2];                  // items of other CTAs too, for which this CTA came last
-  uint32_t last[2];
+  int32_t last[2];             // runs of items of other CTAs too, for which this CTA came last; -1: none
   int32_t runs;
   struct Run {
     int8_t first, last, head;  // warps of its tails (first < 0: none) and its head (< 0: none)
     int8_t slot;               // -1: the item is this CTA's alone, else the CTA's part that this is
   } run[kWarps + 1];
-  // Where a row of a run's item (and of fin's) goes in O; -1: no such row.
-  int64_t row_at[kWarps + 1][8 * NT], fin_at[2][8 * NT];
+  // Where a row of a run's item goes in O; -1: no such row.
+  int64_t row_at[kWarps + 1][8 * NT];
   uint32_t abort;
 };
 
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       mbar_init(smem_u32(&sh.empty[warp * 4 + s]), 1);
     }
   if (tid == 0) sh.abort = 0;
-  if (tid < 2) sh.last[tid] = 0;
+  if (tid < 2) sh.last[tid] = -1;
   if (tid < kWarps) sh.has_head[tid] = sh.has_tail[tid] = 0;
   fence_barrier_init();
   __syncthreads();
@@ -668,14 +672,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int row = nt * 8 + 2 * t + e;
-            float4* dst = reinterpret_cast<float4*>(part + row * D + g * (D / 8));
+            float4* dst = reinterpret_cast<float4*>(part + row * C::kPitch + g * (D / 8));
 #pragma unroll
             for (int i = 0; i < MT / 2; ++i)
               dst[i] = make_float4(o[nt][2 * i][e] + z[nt][e], o[nt][2 * i][2 + e] + z[nt][e],
                                    o[nt][2 * i + 1][e] + z[nt][e], o[nt][2 * i + 1][2 + e] + z[nt][e]);
             if (g == 0) {
-              part[C::kRows * D + row] = m[nt][e];
-              part[C::kRows * D + C::kRows + row] = l[nt][e];
+              part[C::kTop + row] = m[nt][e];
+              part[C::kSum + row] = l[nt][e];
             }
           }
         if (lane == 0) {
@@ -749,35 +753,54 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       run.slot = cut.first >= cta_r0 && cut.first + cut.units <= cta_r1 ? -1 : (cut.first >= cta_r0 ? 1 : 0);
   }
   __syncthreads();
-  // An output of four columns a thread.
-  constexpr int kOuts = C::kRows * (D / 4);
+  // An output of four columns a thread, four of them at a time: the heads among their parts (in
+  // L2) are asked for together.
+  constexpr int kOuts = C::kRows * (D / 4), kTogether = 4;
 #pragma unroll 1
-  for (int i = tid; i < sh.runs * kOuts; i += kThreads) {
-    const int at = i % kOuts, row = at / (D / 4), c = at % (D / 4) * 4;
-    const int64_t to = sh.row_at[i / kOuts][row];
-    if (to < 0) continue;
-    const auto run = sh.run[i / kOuts];
-    Sum s;
-    if (run.first >= 0)
-#pragma unroll 1
-      for (int v = run.first; v <= run.last; ++v)
-        if (sh.has_tail[v]) {
-          const float* q = tail_part(v);
-          s.add(q[C::kRows * D + row], q[C::kRows * D + C::kRows + row],
-                *reinterpret_cast<const float4*>(q + row * D + c));
-        }
-    if (run.head >= 0) {  // either memory; stores of this CTA's own warps, ordered by its barrier
-      const float* q = head_part(run.head);
-      s.add(q[C::kRows * D + row], q[C::kRows * D + C::kRows + row], *reinterpret_cast<const float4*>(q + row * D + c));
+  for (int i0 = tid; i0 < sh.runs * kOuts; i0 += kTogether * kThreads) {
+    float hm[kTogether], hl[kTogether];
+    float4 hv[kTogether];
+#pragma unroll
+    for (int x = 0; x < kTogether; ++x) {
+      const int i = i0 + x * kThreads, at = i % kOuts, row = at / (D / 4), c = at % (D / 4) * 4;
+      const int eh = i < sh.runs * kOuts ? sh.run[i / kOuts].head : -1;
+      hm[x] = -INFINITY;
+      hl[x] = 0.f;
+      hv[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (eh >= 0) {  // either memory; stores of this CTA's own warps, ordered by its barrier
+        const float* q = head_part(eh);
+        hm[x] = q[C::kTop + row];
+        hl[x] = q[C::kSum + row];
+        hv[x] = *reinterpret_cast<const float4*>(q + row * C::kPitch + c);
+      }
     }
-    if (run.slot < 0) {
-      *reinterpret_cast<uint2*>(p.O + to + c) = s.value();
-    } else {
-      float* out = cta_parts + (2 * static_cast<int64_t>(blockIdx.x) + run.slot) * C::kPart;
-      __stcg(reinterpret_cast<float4*>(out + row * D + c), s.v);
-      if (c == 0) {
-        __stcg(out + C::kRows * D + row, s.m);
-        __stcg(out + C::kRows * D + C::kRows + row, s.l);
+#pragma unroll
+    for (int x = 0; x < kTogether; ++x) {
+      const int i = i0 + x * kThreads, at = i % kOuts, row = at / (D / 4), c = at % (D / 4) * 4;
+      if (i >= sh.runs * kOuts) break;
+      const int64_t to = sh.row_at[i / kOuts][row];
+      if (to < 0) continue;
+      const auto run = sh.run[i / kOuts];
+      Sum s;
+      if (run.first >= 0)
+#pragma unroll 2
+        for (int v = run.first; v <= run.last; ++v) {
+          const float* q = tail_part(v);
+          const bool have = sh.has_tail[v];  // warps without a unit have none: no weight
+          const float4 f = *reinterpret_cast<const float4*>(q + row * C::kPitch + c);
+          s.add(have ? q[C::kTop + row] : -INFINITY, have ? q[C::kSum + row] : 0.f,
+                have ? f : make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+      s.add(hm[x], hl[x], hv[x]);
+      if (run.slot < 0) {
+        *reinterpret_cast<uint2*>(p.O + to + c) = s.value();
+      } else {
+        float* out = cta_parts + (2 * static_cast<int64_t>(blockIdx.x) + run.slot) * C::kPart;
+        __stcg(reinterpret_cast<float4*>(out + row * C::kPitch + c), s.v);
+        if (c == 0) {
+          __stcg(out + C::kTop + row, s.m);
+          __stcg(out + C::kSum + row, s.l);
+        }
       }
     }
   }
@@ -793,25 +816,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       uint32_t* counter = static_cast<uint32_t*>(p.ws) + k0;
       if (take_ticket(counter) == k1 - k0) {
         *counter = 0;  // every contributor has its ticket: ready for the next call
-        sh.fin[run.slot] = cut;
-        sh.last[run.slot] = 1;
+        sh.last[run.slot] = tid == 0 ? 0 : sh.runs - 1;
       }
     }
   }
   __syncthreads();
-  if (!sh.last[0] && !sh.last[1]) return;
+  if (sh.last[0] < 0 && sh.last[1] < 0) return;
 
   constexpr int kBatch = 8;  // parts asked for together
   // ---- items cut between CTAs whose last part was this CTA's: every thread takes an output of
   // four columns, groups of threads the CTAs in turn
 #pragma unroll 1
-  for (int i = tid; i < 2 * C::kRows; i += kThreads)
-    if (sh.last[i / C::kRows]) sh.fin_at[i / C::kRows][i % C::kRows] = row_of(sh.fin[i / C::kRows], i % C::kRows);
-  __syncthreads();
-#pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
-    if (!sh.last[slot]) continue;
-    const Cut cut = sh.fin[slot];
+    const int last = sh.last[slot];
+    if (last < 0) continue;
+    const Cut cut = sh.run[last].first >= 0 ? sh.tail[sh.run[last].first] : sh.head[sh.run[last].head];
     const uint32_t k0 = split.worker(cut.first) / kWarps, k1 = split.worker(cut.first + cut.units - 1) / kWarps;
     // Many parts: groups of threads take them in turn, and join through shared memory.
     constexpr int kGroups = kOuts < C::kThreads ? C::kThreads / kOuts : 1;
@@ -820,7 +839,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll 1
     for (int i = tid; i < groups * kOuts; i += kThreads) {
       const int grp = i / kOuts, at = i % kOuts, row = at / (D / 4), c = at % (D / 4) * 4;
-      const int64_t to = sh.fin_at[slot][row];
+      const int64_t to = sh.row_at[last][row];
       if (to < 0) continue;
       Sum s;
 #pragma unroll 1
@@ -832,9 +851,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           const uint32_t kk = k + x * groups;
           const float* q = cta_parts + (2 * static_cast<int64_t>(kk) + (kk == k0 ? 1 : 0)) * C::kPart;
           const bool in = kk <= k1;
-          mk[x] = in ? __ldcg(q + C::kRows * D + row) : -INFINITY;
-          lk[x] = in ? __ldcg(q + C::kRows * D + C::kRows + row) : 0.f;
-          v[x] = in ? __ldcg(reinterpret_cast<const float4*>(q + row * D + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          mk[x] = in ? __ldcg(q + C::kTop + row) : -INFINITY;
+          lk[x] = in ? __ldcg(q + C::kSum + row) : 0.f;
+          v[x] = in ? __ldcg(reinterpret_cast<const float4*>(q + row * C::kPitch + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) s.add(mk[x], lk[x], v[x]);
@@ -853,7 +872,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     }
     if (groups > 1) {  // uniform over the CTA
       __syncthreads();
-      const int64_t to = tid < kOuts ? sh.fin_at[slot][tid / (D / 4)] : -1;
+      const int64_t to = tid < kOuts ? sh.row_at[last][tid / (D / 4)] : -1;
       if (to >= 0) {
         Sum s;
         for (int x = 0; x < groups; ++x) {
