@@ -23,10 +23,10 @@
 //     as they lie (a lane 16 bytes, two key rows), V's codes lie in the cache in fragment order.
 //   * P goes from the first product's output layout to the second's operand layout by
 //     movmatrix, in registers.
-// Work: units of 64 (32) keys of all (sequence, cache head, query block) items, in one row, cut
-// evenly over the warps of one CTA per SM whatever the lengths: a warp walks its units with its
-// own ring of bulk copies (one per 16-token record, so pages of any multiple of 16 do) and
-// writes the items that lie whole in its share.  An item cut between warps of a CTA is joined
+// Work: units of 32 keys of all (sequence, cache head, query block) items, in one row, cut evenly
+// over the CTAs (one per SM) and each CTA's share over its warps, whatever the lengths: a warp
+// walks its units with its own ring of bulk copies (one per 16-token record, so pages of any
+// multiple of 16 do) and writes the items that lie whole in its share.  An item cut between warps of a CTA is joined
 // once, at the CTA's end, through shared memory; one cut between CTAs by the last of them to
 // arrive, in CTA order (so results do not depend on arrival).
 #include <cuda_bf16.h>
@@ -45,6 +45,11 @@ namespace {
 constexpr int kMaxCtas = 160;   // CTAs that the workspace has room for
 // A CTA is given at least this many units, so that small calls use fewer CTAs and joins.
 constexpr int kMinUnits = 4;
+// Items of up to this many units are one CTA's, which mostly saves the join of two (8 cache heads
+// of 128, 8 queries each; us with 0, 16, 32, 64 here: 16 x 512 keys 12.2, 9.1, 9.1, 9.1;
+// 100 x 1024 32.5, 32.6, 30.4, 30.3; 8 x 1024 of four queries 31.8, 31.8, 20.3, 20.3;
+// 1 x 1024 8.9, 8.9, 10.2, 10.2; 1 x 2048 9.8, 9.8, 9.8, 13.4).
+constexpr int kWhole = 32;
 // The reference that weights are taken against (2^(score - reference)) follows the running
 // maximum only when that has outgrown it by this much: weights stay below 2^8, which FP32 sums
 // and BF16's exponent carry as well as weights below 1, and most steps scale nothing.
@@ -262,15 +267,23 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   const int rows_all = static_cast<int>(p.Lq) * p.group;
   const uint32_t batch = static_cast<uint32_t>(p.batch);
 
-  // ---- every warp adds up the units for itself; a lane takes a run of sequences
+  // ---- every warp adds up the units for itself; a lane takes a run of sequences, and keeps the
+  // units of the first few
+  constexpr int kKept = 4;
   const uint32_t per = (batch + 31) / 32, b_lo = lane * per, b_hi = min(b_lo + per, batch);
-  uint32_t mine = 0;
-#pragma unroll 1
-  for (uint32_t b = b_lo; b < b_hi; ++b) {
+  auto units_of = [&](uint32_t b) {
     const int32_t n = p.lens[b];
     if (blockIdx.x == 0 && (n < 0 || n > cap)) atomicCAS(p.index_word, 0u, kDevBadIndex);
-    mine += static_cast<uint32_t>(min(max(n, 0), cap) + kUnit - 1) / kUnit;
+    return static_cast<uint32_t>(min(max(n, 0), cap) + kUnit - 1) / kUnit;
+  };
+  uint32_t kept[kKept], mine = 0;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    kept[i] = b_lo + i < b_hi ? units_of(b_lo + i) : 0;
+    mine += kept[i];
   }
+#pragma unroll 1
+  for (uint32_t b = b_lo + kKept; b < b_hi; ++b) mine += units_of(b);
   mine *= ips;
   uint32_t incl = mine;
 #pragma unroll
@@ -291,11 +304,61 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   }
   const uint32_t ctas = min((total + kMinUnits - 1) / kMinUnits, gridDim.x);
   if (blockIdx.x >= ctas) return;  // whole CTAs
-  const Split split(total, ctas * kWarps);
+  const Split split(total, ctas);
+
+  // Where unit r < total lies (all lanes): the lane whose sequences hold it finds the sequence and
+  // what lies before it there.
+  auto locate = [&](uint32_t r) {
+    const int owner = __ffs(__ballot_sync(~0u, r < incl)) - 1;
+    uint32_t at = incl - mine, b0 = b_lo, units = 0;
+    if (lane == owner) {
+#pragma unroll
+      for (int i = 0; i < kKept; ++i)
+        if (units == 0) {
+          const uint32_t n = kept[i] * ips;
+          if (r < at + n) {
+            units = kept[i];
+          } else {
+            at += n;
+            ++b0;
+          }
+        }
+#pragma unroll 1
+      while (units == 0) {
+        const uint32_t here = static_cast<uint32_t>(len_of(b0) + kUnit - 1) / kUnit;
+        if (r < at + here * ips) {
+          units = here;
+        } else {
+          at += here * ips;
+          ++b0;
+        }
+      }
+    }
+    Walk w;
+    w.r = r;
+    w.b = __shfl_sync(~0u, b0, owner);
+    w.units = __shfl_sync(~0u, units, owner);
+    const uint32_t off = r - __shfl_sync(~0u, at, owner);
+    w.item = off / static_cast<uint32_t>(w.units);
+    w.u = off - w.item * w.units;
+    return w;
+  };
+  // The CTAs' shares: even, but a border inside an item of up to kWhole units moves to the item's
+  // nearer end.  (Borders inside longer items stay, so the CTAs of such an item are the even
+  // cut's.)
+  auto border = [&](uint32_t c) {
+    const uint32_t r = split.start(c);
+    if (c == 0 || c == ctas) return r;
+    const Walk w = locate(r);
+    return w.units > kWhole ? r : 2 * w.u < w.units ? r - w.u : r - w.u + w.units;
+  };
+  const uint32_t cta_r0 = border(blockIdx.x), cta_r1 = border(blockIdx.x + 1);
   // The units of this warp, and of the warp that a lane of the copying warp works for.
   const bool copies = warp == kWarps;
-  const uint32_t me = blockIdx.x * kWarps + (copies ? min(lane, kWarps - 1) : warp);
-  const uint32_t r0 = split.start(me), r1 = split.start(me + 1);
+  const uint32_t me = blockIdx.x * kWarps + warp;
+  const Split share(cta_r1 - cta_r0, kWarps);
+  const uint32_t w0 = copies ? min(lane, kWarps - 1) : warp;
+  const uint32_t r0 = cta_r0 + share.start(w0), r1 = cta_r0 + share.start(w0 + 1);
 
   auto move_to = [&](Walk& w, uint32_t r) {  // r < total
     int32_t d = static_cast<int32_t>(r - w.r);
@@ -318,23 +381,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 
   Walk seg;
   if (!copies && r0 < r1) {
-    // The lane whose sequences hold unit r0 finds the sequence and what lies before it there.
-    const int owner = __ffs(__ballot_sync(~0u, r0 < incl)) - 1;
-    uint32_t at = incl - mine, b0 = b_lo;
-    if (lane == owner)
-#pragma unroll 1
-      for (;; ++b0) {
-        const uint32_t n = static_cast<uint32_t>((len_of(b0) + kUnit - 1) / kUnit) * ips;
-        if (r0 < at + n) break;
-        at += n;
-      }
-    seg.r = r0;
-    seg.b = __shfl_sync(~0u, b0, owner);
-    const uint32_t off = r0 - __shfl_sync(~0u, at, owner);
+    seg = locate(r0);
     seg.len = len_of(seg.b);
-    seg.units = (seg.len + kUnit - 1) / kUnit;
-    seg.item = off / static_cast<uint32_t>(seg.units);
-    seg.u = off - seg.item * seg.units;
     if (lane == 0) sh.start[warp] = seg;
   }
   __syncthreads();
@@ -699,7 +747,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 
   // ---- join: the parts in the order of their units are head 0, tail 0, head 1, tail 1, ...; a
   // tail and what follows it, up to the next head, are one item: a run.
-  const uint32_t cta_r0 = split.start(blockIdx.x * kWarps), cta_r1 = split.start((blockIdx.x + 1) * kWarps);
   auto tail_part = [&](int w) { return reinterpret_cast<const float*>(smem + w * C::kStages * C::kUnitBytes); };
   auto head_part = [&](int w) {
     return sh.has_head[w] == 2 ? tail_part(w)
@@ -812,7 +859,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const Cut cut = run.first >= 0 ? sh.tail[run.first] : sh.head[run.head];
       // A CTA is the first one of at most one item that goes on after it: that item's counter is
       // the first CTA's.
-      const uint32_t k0 = split.worker(cut.first) / kWarps, k1 = split.worker(cut.first + cut.units - 1) / kWarps;
+      const uint32_t k0 = split.worker(cut.first), k1 = split.worker(cut.first + cut.units - 1);
       uint32_t* counter = static_cast<uint32_t*>(p.ws) + k0;
       if (take_ticket(counter) == k1 - k0) {
         *counter = 0;  // every contributor has its ticket: ready for the next call
@@ -831,7 +878,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const int last = sh.last[slot];
     if (last < 0) continue;
     const Cut cut = sh.run[last].first >= 0 ? sh.tail[sh.run[last].first] : sh.head[sh.run[last].head];
-    const uint32_t k0 = split.worker(cut.first) / kWarps, k1 = split.worker(cut.first + cut.units - 1) / kWarps;
+    const uint32_t k0 = split.worker(cut.first), k1 = split.worker(cut.first + cut.units - 1);
     // Many parts: groups of threads take them in turn, and join through shared memory.
     constexpr int kGroups = kOuts < C::kThreads ? C::kThreads / kOuts : 1;
     const int groups = k1 - k0 + 1 > kBatch ? kGroups : 1;
