@@ -10,7 +10,7 @@
 // With at most 64 tokens every weight of a chosen expert is used a few times: reading each
 // once from HBM bounds the layer.  Two kernels, one CTA per SM each, the second launched
 // programmatically behind the first:
-//   * up: (expert, 128 columns of W_g and of W_u, 64 rows of K) units of the active experts;
+//   * up: (128 columns of W_g and of W_u, expert, 64 rows of K) units of the active experts;
 //   * down: (128 columns of W_d, expert, 64 rows of I) units.  A column tile sums over experts in
 //     FP32 in shared memory, one addition per expert and token.
 // Both route up to 16 tokens in every CTA, a warp per token (more have a small launch of their own
@@ -67,6 +67,30 @@ struct Split {
     const uint32_t long_units = rem * (q + 1);
     return x < long_units ? x / (q + 1) : rem + (x - long_units) / q;
   }
+};
+
+// A kernel's units, and a CTA's share of them.  CTAs work in groups of neighbours, each on its own
+// one of a group's neighbouring column tiles: the rows' lines that two tiles have in common are
+// then asked for by both at nearly the same time and come from HBM once.  The
+// groups cut the row of (column group, expert, block of rows) units evenly; CTAs whose place in
+// the last group is past the last column have a row that ends before it.
+struct Share {
+  uint32_t group, place, u0 = 0, u1 = 0;
+  Split split;
+  // `tiles` column tiles of `per` units each.
+  __device__ __forceinline__ Share(uint32_t tiles, uint32_t per, uint32_t g, uint32_t least)
+      : group(g), place(blockIdx.x % g), split(0, 1) {
+    const uint32_t units = (tiles + g - 1) / g * per;
+    const uint32_t workers = min((units + least - 1) / least, gridDim.x / g), me = blockIdx.x / g;
+    if (workers == 0) return;
+    split = Split(units, workers);
+    if (me >= workers) return;
+    const uint32_t mine = place < tiles ? ((tiles - place - 1) / g + 1) * per : 0;
+    u0 = min(split.start(me), mine);
+    u1 = min(split.start(me + 1), mine);
+  }
+  __device__ __forceinline__ uint32_t cta(uint32_t worker) const { return worker * group + place; }
+  __device__ __forceinline__ uint32_t column(uint32_t t) const { return (t * group + place) * 128; }  // first, of group t
 };
 
 __device__ __forceinline__ uint32_t take_ticket(uint32_t* a) {
@@ -359,13 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
   route<NTOK>(p, rt);
 
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
-  const uint32_t kb = static_cast<uint32_t>((p.K + BK - 1) / BK);
-  const uint32_t ntiles = static_cast<uint32_t>((p.I + 127) / 128);
-  const uint32_t units = static_cast<uint32_t>(rt.active) * ntiles * kb;
-  const uint32_t ctas = min((units + kMinUp - 1) / kMinUp, gridDim.x);
-  const bool works = blockIdx.x < ctas;
-  const Split split(units, ctas > 0 ? ctas : 1);
-  const uint32_t u0 = works ? split.start(blockIdx.x) : 0, u1 = works ? split.start(blockIdx.x + 1) : 0;
+  const uint32_t kb = static_cast<uint32_t>((p.K + BK - 1) / BK), active = static_cast<uint32_t>(rt.active);
+  const Share share(static_cast<uint32_t>((p.I + 127) / 128), active * kb, p.up_group, kMinUp);
+  const uint32_t u0 = share.u0, u1 = share.u1;
 
   const int64_t ldz = ldz_of(p.I);
   uint16_t* Z = reinterpret_cast<uint16_t*>(ws + (kPartsAt + 2 * kMaxCtas * part_floats(NTOK) * 4));
@@ -378,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
   };
   // Adds a tile's parts in CTA order, four columns of one row a thread, and writes their Z.
   auto join = [&](uint32_t tile) {
-    const uint32_t c0 = split.worker(tile * kb), c1 = split.worker((tile + 1) * kb - 1);
-    const int a = static_cast<int>(tile / ntiles), z0 = rt.off[a], rows = rt.off[a + 1] - z0;
+    const uint32_t c0 = share.split.worker(tile * kb), c1 = share.split.worker((tile + 1) * kb - 1);
+    const int a = static_cast<int>(tile % active), z0 = rt.off[a], rows = rt.off[a + 1] - z0;
     const float* parts = reinterpret_cast<const float*>(ws + kPartsAt);
 #pragma unroll 1
     for (int i = threadIdx.x - 64; i < rows * 32; i += kJoin) {
@@ -390,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
         float4 v[4], w[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const float* src = parts + (2 * (c + x) + (c + x > c0 ? 0 : 1)) * part_floats(NTOK) + r * 256 + c4;
+          const float* src = parts + (2 * share.cta(c + x) + (c + x > c0 ? 0 : 1)) * part_floats(NTOK) + r * 256 + c4;
           const bool in = c + x <= c1;
           v[x] = in ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
           w[x] = in ? __ldcg(reinterpret_cast<const float4*>(src + 128)) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -404,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
       const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t n = static_cast<int64_t>(tile % ntiles) * 128 + c4 + j;
+        const int64_t n = static_cast<int64_t>(share.column(tile / active)) + c4 + j;
         if (n < p.I) put_z(z0 + r, n, gs[j], us[j]);
       }
     }
@@ -417,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
       bool ok = true;
       for (uint32_t u = u0; ok && u < u1;) {
         const uint32_t tile = u / kb, end = min(u1, (tile + 1) * kb);
-        const int32_t e = rt.expert[tile / ntiles], n0 = static_cast<int32_t>(tile % ntiles) * 128;
+        const int32_t e = rt.expert[tile % active], n0 = static_cast<int32_t>(share.column(tile / active));
         for (int32_t k = static_cast<int32_t>(u - tile * kb) * BK; u < end; ++u, k += BK) {
           const uint32_t s = it % STAGES;
           if (!mbar_wait(smem_u32(&pipe.empty[s]), ((it / STAGES) & 1u) ^ 1u, abort, p.status, kDevTimeoutProducer)) {
@@ -481,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
       const uint32_t tile = u / kb, end = min(u1, (tile + 1) * kb);
       const bool whole = end - u == kb;
       const uint32_t acc = lt & 1u;
-      const int a = static_cast<int>(tile / ntiles), z0 = rt.off[a], rows = rt.off[a + 1] - z0;
-      const int64_t n = static_cast<int64_t>(tile % ntiles) * 128 + row;
+      const int a = static_cast<int>(tile % active), z0 = rt.off[a], rows = rt.off[a + 1] - z0;
+      const int64_t n = static_cast<int64_t>(share.column(tile / active)) + row;
       // One thread waits (bounded); all 128 take the same decision after the barrier.
       if (etid == 0)
         pipe.seg_ok = mbar_wait(smem_u32(&pipe.tfull[acc]), (lt >> 1) & 1u, abort, p.status, kDevTimeoutEpilogue) ? 1u : 0u;
@@ -523,10 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
       if (!whole) {
         // The barrier orders the CTA's stores before the ticket, whose release covers them.  A
         // CTA is the first one of at most one tile that goes on after it: its counter is the tile's.
-        const uint32_t c0 = split.worker(tile * kb), c1 = split.worker((tile + 1) * kb - 1);
+        const uint32_t c0 = share.split.worker(tile * kb), c1 = share.split.worker((tile + 1) * kb - 1);
         epi_bar();
         if (etid == 0) {
-          uint32_t* counter = reinterpret_cast<uint32_t*>(ws) + c0;
+          uint32_t* counter = reinterpret_cast<uint32_t*>(ws) + share.cta(c0);
           const bool last = take_ticket(counter) == c1 - c0;
           if (last) *counter = 0;
           pipe.is_last = last;
@@ -609,11 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   const int T = static_cast<int>(p.T), active = rt.active;
   const uint32_t kb = static_cast<uint32_t>((p.I + BK - 1) / BK), per = static_cast<uint32_t>(active) * kb;
-  const uint32_t units = static_cast<uint32_t>((p.K + 127) / 128) * per;
-  const uint32_t ctas = min((units + kMinDown - 1) / kMinDown, gridDim.x);
-  const bool works = blockIdx.x < ctas;
-  const Split split(units, ctas > 0 ? ctas : 1);
-  const uint32_t u0 = works ? split.start(blockIdx.x) : 0, u1 = works ? split.start(blockIdx.x + 1) : 0;
+  const Share share(static_cast<uint32_t>((p.K + 127) / 128), per, p.down_group, kMinDown);
+  const uint32_t u0 = share.u0, u1 = share.u1;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -630,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
         x.k = 0;
         if (++x.a == active) {
           x.a = 0;
-          x.n0 += 128;
+          x.n0 += 128 * static_cast<int32_t>(p.down_group);
         }
       };
       constexpr uint32_t kRow = BK * 2;  // bytes of a row of Z in a stage
@@ -654,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
         }
       };
       const uint32_t tile0 = per ? u0 / per : 0, a0 = per ? (u0 - tile0 * per) / kb : 0;
-      const Place first = {static_cast<int32_t>(tile0) * 128, static_cast<int32_t>(u0 - tile0 * per - a0 * kb) * BK,
+      const Place first = {static_cast<int32_t>(share.column(tile0)), static_cast<int32_t>(u0 - tile0 * per - a0 * kb) * BK,
                            static_cast<int32_t>(a0)};
       // The ring's first weights come while the up kernel ends; its Z after the wait.
       const uint32_t ahead = min(u1 - u0, static_cast<uint32_t>(STAGES));
@@ -727,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
         p.Y[i / p.K * p.ldy + i % p.K] = 0;
     // Adds a tile's parts in CTA order, four columns of one token a thread, and writes them.
     auto join = [&](uint32_t tile) {
-      const uint32_t c0 = split.worker(tile * per), c1 = split.worker((tile + 1) * per - 1);
+      const uint32_t c0 = share.split.worker(tile * per), c1 = share.split.worker((tile + 1) * per - 1);
 #pragma unroll 1
       for (int i = jtid; i < T * 32; i += kJoin) {
         const int t = i >> 5, c4 = (i & 31) * 4;
@@ -738,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
 #pragma unroll
           for (int x = 0; x < 12; ++x)
             v[x] = c + x <= c1 ? __ldcg(reinterpret_cast<const float4*>(
-                                     parts + (2 * (c + x) + (c + x > c0 ? 0 : 1)) * part_floats(NTOK) + t * 128 + c4))
+                                     parts + (2 * share.cta(c + x) + (c + x > c0 ? 0 : 1)) * part_floats(NTOK) + t * 128 + c4))
                                : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int x = 0; x < 12; ++x) {
@@ -751,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
         const float y[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int64_t n = static_cast<int64_t>(tile) * 128 + c4 + j;
+          const int64_t n = static_cast<int64_t>(share.column(tile)) + c4 + j;
           if (n < p.K) p.Y[t * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y[j]));
         }
       }
@@ -802,8 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
         u = end;
         if (u == tile_end || u == u1) {
           // ---- the column tile is done, here or as far as this CTA goes
-          const int64_t n = static_cast<int64_t>(tile) * 128 + row;
-          const uint32_t c0 = split.worker(tile * per), c1 = split.worker(tile_end - 1);
+          const int64_t n = static_cast<int64_t>(share.column(tile)) + row;
+          const uint32_t c0 = share.split.worker(tile * per), c1 = share.split.worker(tile_end - 1);
           if (c0 == c1) {
             for (int t = 0; t < T; ++t) {
               if (n < p.K) p.Y[t * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(yacc[t * 128 + row]));
@@ -818,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
             // Barrier, ticket and counter as in the up kernel.
             epi_bar();
             if (etid == 0) {
-              uint32_t* counter = reinterpret_cast<uint32_t*>(ws) + kMaxCtas + c0;
+              uint32_t* counter = reinterpret_cast<uint32_t*>(ws) + kMaxCtas + share.cta(c0);
               const bool last = take_ticket(counter) == c1 - c0;
               if (last) *counter = 0;
               pipe.is_last = last;
@@ -882,16 +899,34 @@ int64_t moe_ws_bytes(int64_t T, int64_t I, int64_t top) {
 bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
                    uint64_t batch, uint64_t stride, uint32_t box_inner, uint32_t box_outer);
 
-cudaError_t launch_moe(const MoeParams& p, int sms, cudaStream_t s) {
+// CTAs of a group: one where rows start on the 128-byte lines that HBM is read in, so that column
+// tiles share none; otherwise 8, or what a row has tiles for (48 tokens, 61 active experts of
+// 2048 x 1000, 1160 and 700, us: single CTAs 152, 191, 113, pairs 149, 177, 109, fours 145, 179,
+// 108, eights 144, 174, 108; 718 MB came from HBM for the first one's 500 MB of W_g and W_u when
+// neighbouring tiles were read far apart in time, which took 172).
+uint32_t group_of(int64_t cols, int sms, bool lines) {
+  const int64_t tiles = (cols + 127) / 128;
+  uint32_t g = lines ? 1 : 8;
+  while (g > tiles || g > static_cast<uint32_t>(sms)) g /= 2;
+  return g > 0 ? g : 1;
+}
+
+cudaError_t launch_moe(const MoeParams& call, int sms, cudaStream_t s) {
+  MoeParams p = call;
+  auto aligned = [&](const uint16_t* w, int64_t ld, int64_t stride, int64_t bytes) {
+    return reinterpret_cast<uintptr_t>(w) % bytes == 0 && ld * 2 % bytes == 0 && (p.E == 1 || stride * 2 % bytes == 0);
+  };
+  p.up_group = group_of(p.I, sms, aligned(p.Wg, p.ldwg, p.strideWg, 128) && aligned(p.Wu, p.ldwu, p.strideWu, 128));
+  p.down_group = group_of(p.K, sms, aligned(p.Wd, p.ldwd, p.strideWd, 128));
   // Experts are the third dimension; a map of one expert keeps it (its second index is never
   // loaded), so that the kernels have one form.
   const uint64_t experts = p.E > 1 ? p.E : 2;
   auto weights = [&](CUtensorMap* map, const uint16_t* w, int64_t rows, int64_t cols, int64_t ld, int64_t stride) {
+    const bool lines = aligned(w, ld, stride, 256);
     if (p.E == 1) stride = rows * ld;
     // Rows that start on 256-byte lines are read in whole ones.  Otherwise L2 is to fetch the
     // sectors asked for only: with 256-byte fetches the two ends of every row's 256 bytes bring
     // lines of which little is used before they are gone (rows of 2000 bytes: 868 MB read for 500).
-    const bool lines = reinterpret_cast<uintptr_t>(w) % 256 == 0 && ld % 128 == 0 && stride % 128 == 0;
     return make_tile_map_l2(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, cols, rows, ld, experts, stride, 64, BK,
                          CU_TENSOR_MAP_SWIZZLE_128B, 1,
                          lines ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE);
