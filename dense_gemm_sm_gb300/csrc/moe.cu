@@ -205,7 +205,8 @@ __device__ __forceinline__ void choose(const MoeParams& p, Routes* sh, Choices* 
       m = max(m, key[i]);
     }
     load(t + warps, next);
-    const float best = value(__reduce_max_sync(~0u, m));
+    const uint32_t high = __reduce_max_sync(~0u, m), low = __reduce_min_sync(~0u, m);
+    const float best = value(high);
     auto count = [&](uint32_t least) {
       int n = 0;
 #pragma unroll
@@ -215,9 +216,13 @@ __device__ __forceinline__ void choose(const MoeParams& p, Routes* sh, Choices* 
     uint32_t bar = 1;  // chosen: key > bar - 1, or some of those equal to bar
     int left = top, n = count(1);
     if (n > top) {
-      bar = 0;
+      // 32 numbers, which is more than `top`, reach the least of the lanes' largest: what that
+      // and the largest of all begin with is known.
+      uint32_t bit = high != low ? 0x80000000u >> __clz(high ^ low) : 0;
+      bar = high & ~(2 * bit - (bit != 0));
+      n = count(bar);
 #pragma unroll 1
-      for (uint32_t bit = 0x80000000u; bit != 0 && n != top; bit >>= 1) {
+      for (; bit != 0 && n != top; bit >>= 1) {
         const int c = count(bar | bit);
         if (c >= top) {
           bar |= bit;
@@ -244,13 +249,14 @@ __device__ __forceinline__ void choose(const MoeParams& p, Routes* sh, Choices* 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    const float scale = 1.f / sum;  // one division in the code; the weights are within 2^-23
 #pragma unroll
     for (int i = 0; i < KE; ++i) {
       const uint32_t in = __ballot_sync(~0u, w[i] > 0.f);  // a weight that underflows adds nothing
       if (w[i] > 0.f) {
         const int at = slot + __popc(in & ((1u << lane) - 1));
         (GLOBAL ? out->id : sh->id)[t][at] = static_cast<int16_t>(lane + 32 * i);
-        (GLOBAL ? out->w : sh->w)[t][at] = w[i] / sum;
+        (GLOBAL ? out->w : sh->w)[t][at] = w[i] * scale;
         if (!GLOBAL) atomicOr(&sh->mask[lane + 32 * i][t >> 5], 1u << (t & 31));
       }
       slot += __popc(in);
@@ -313,10 +319,10 @@ __device__ __forceinline__ void route(const MoeParams& p, Routes& sh) {
   }
   __syncthreads();
   int act = __popc(vote & ((1u << lane) - 1)), first = rows - count;
-#pragma unroll 1
-  for (int w = 0; w < warp; ++w) {
-    act += sh.scan[0][w];
-    first += sh.scan[1][w];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {  // (to its own warp only, one load waits for another: 0.7 us)
+    act += w < warp ? sh.scan[0][w] : 0;
+    first += w < warp ? sh.scan[1][w] : 0;
   }
   if (count > 0) {
     sh.expert[act] = static_cast<int16_t>(tid);
