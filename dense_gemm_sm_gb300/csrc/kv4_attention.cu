@@ -28,7 +28,7 @@
 // walks its units with its own ring of bulk copies (one per 16-token record, so pages of any
 // multiple of 16 do) and writes the items that lie whole in its share.  An item cut between warps of a CTA is joined
 // once, at the CTA's end, through shared memory; one cut between CTAs by the last of them to
-// arrive, in CTA order (so results do not depend on arrival).
+// arrive, in CTA order (so results do not depend on arrival), of very many CTAs in two steps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -54,7 +54,11 @@ constexpr int kWhole = 32;
 // maximum only when that has outgrown it by this much: weights stay below 2^8, which FP32 sums
 // and BF16's exponent carry as well as weights below 1, and most steps scale nothing.
 constexpr float kSlack = 8.f;
-constexpr int64_t kCounterBytes = 1024;  // one ticket counter per CTA, then the parts
+// An item of very many CTAs is joined in two steps, this many neighbours first.
+constexpr uint32_t kTeam = 12;
+constexpr int kTeams = 2 * ((kMaxCtas + kTeam - 1) / kTeam);  // places of their sums and counters
+constexpr int64_t kCounterBytes = 1024;  // ticket counters of the CTAs and the teams, then the parts
+static_assert((kMaxCtas + kTeams) * 4 <= kCounterBytes, "counters");
 
 template <int D, int NT>
 struct Cfg {
@@ -193,16 +197,23 @@ struct Cut {
 struct Sum {
   float m = -INFINITY, l = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  __device__ __forceinline__ void add(float mk, float lk, const float4& x) {
-    const float top = fmaxf(m, mk);
+  // Adds N parts against their common maximum: their weights do not wait for one another.
+  template <int N>
+  __device__ __forceinline__ void add(const float (&mk)[N], const float (&lk)[N], const float4 (&x)[N]) {
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, mk[i]);
     if (!(top > -INFINITY)) return;  // nothing seen yet
-    const float a = ex2(m - top), b = ex2(mk - top);
+    const float a = ex2(m - top);
     m = top;
-    l = l * a + lk * b;
-    v.x = v.x * a + x.x * b;
-    v.y = v.y * a + x.y * b;
-    v.z = v.z * a + x.z * b;
-    v.w = v.w * a + x.w * b;
+    l *= a;
+    v = make_float4(v.x * a, v.y * a, v.z * a, v.w * a);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float b = ex2(mk[i] - top);
+      l = fmaf(lk[i], b, l);
+      v = make_float4(fmaf(x[i].x, b, v.x), fmaf(x[i].y, b, v.y), fmaf(x[i].z, b, v.z), fmaf(x[i].w, b, v.w));
+    }
   }
   __device__ __forceinline__ uint2 value() const {
     const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -220,6 +231,7 @@ struct Shared {
   uint8_t has_head[kWarps], has_tail[kWarps];
   int32_t last[2];             // runs of items of other CTAs too, for which this CTA came last; -1: none
   int32_t runs;
+  bool ends[2];                // the step of its join is the item's last
   struct Run {
     int8_t first, last, head;  // warps of its tails (first < 0: none) and its head (< 0: none)
     int8_t slot;               // -1: the item is this CTA's alone, else the CTA's part that this is
@@ -829,16 +841,26 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (to < 0) continue;
       const auto run = sh.run[i / kOuts];
       Sum s;
-      if (run.first >= 0)
-#pragma unroll 2
-        for (int v = run.first; v <= run.last; ++v) {
-          const float* q = tail_part(v);
-          const bool have = sh.has_tail[v];  // warps without a unit have none: no weight
-          const float4 f = *reinterpret_cast<const float4*>(q + row * C::kPitch + c);
-          s.add(have ? q[C::kTop + row] : -INFINITY, have ? q[C::kSum + row] : 0.f,
-                have ? f : make_float4(0.f, 0.f, 0.f, 0.f));
+      s.m = hm[x];
+      s.l = hl[x];
+      s.v = hv[x];
+      constexpr int kTails = 4;
+#pragma unroll 1
+      for (int v = run.first >= 0 ? run.first : kWarps; v <= run.last; v += kTails) {
+        float mk[kTails], lk[kTails];
+        float4 f[kTails];
+#pragma unroll
+        for (int y = 0; y < kTails; ++y) {
+          const int w = min(v + y, static_cast<int>(run.last));
+          const float* q = tail_part(w);
+          const bool have = v + y <= run.last && sh.has_tail[w];  // warps without a unit have none: no weight
+          const float4 z = *reinterpret_cast<const float4*>(q + row * C::kPitch + c);
+          mk[y] = have ? q[C::kTop + row] : -INFINITY;
+          lk[y] = have ? q[C::kSum + row] : 0.f;
+          f[y] = have ? z : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-      s.add(hm[x], hl[x], hv[x]);
+        s.add(mk, lk, f);
+      }
       if (run.slot < 0) {
         *reinterpret_cast<uint2*>(p.O + to + c) = s.value();
       } else {
@@ -853,83 +875,152 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   }
   __syncthreads();  // before the tickets: their release covers the CTA's stores
   // Only the first and the last run can be of an item of other CTAs too.
-  if (tid == 0 || (tid == 32 && sh.runs > 1)) {
-    const auto run = sh.run[tid == 0 ? 0 : sh.runs - 1];
-    if (sh.runs > 0 && run.slot >= 0) {
-      const Cut cut = run.first >= 0 ? sh.tail[run.first] : sh.head[run.head];
-      // A CTA is the first one of at most one item that goes on after it: that item's counter is
-      // the first CTA's.
-      const uint32_t k0 = split.worker(cut.first), k1 = split.worker(cut.first + cut.units - 1);
-      uint32_t* counter = static_cast<uint32_t*>(p.ws) + k0;
-      if (take_ticket(counter) == k1 - k0) {
-        *counter = 0;  // every contributor has its ticket: ready for the next call
-        sh.last[run.slot] = tid == 0 ? 0 : sh.runs - 1;
-      }
-    }
-  }
-  __syncthreads();
-  if (sh.last[0] < 0 && sh.last[1] < 0) return;
-
-  constexpr int kBatch = 8;  // parts asked for together
-  // ---- items cut between CTAs whose last part was this CTA's: every thread takes an output of
-  // four columns, groups of threads the CTAs in turn
+  constexpr int kAtOnce = NT == 1 ? 1 : 4, kBatch = NT == 1 ? 8 : 4;
+  // An item whose parts would take the threads more turns than this is joined in two steps (one
+  // sequence of 32768, 16 queries of one head: 20.9 us, in one step of 38 turns 47.8; 4 items of
+  // 16768 keys, 32 queries, 10 turns: 35.4 and 57.6; 7 queries, 2 turns: 11.0 and 9.9).
+  constexpr int kTurns = 4;
+  uint32_t* counters = static_cast<uint32_t*>(p.ws);
+  // The parts of a step of an item's join are places lo .. hi - 1 from base on, the item's first
+  // in the odd half of its place, all others in the even ones.
+  struct Step {
+    uint32_t base, lo, hi, first;
+    uint32_t counter, sum;  // the step's counter; the part that its sum is, unless it is the last
+    bool ends;
+  };
+  auto cut_of = [&](int r) { return sh.run[r].first >= 0 ? sh.tail[sh.run[r].first] : sh.head[sh.run[r].head]; };
+  auto outs_of = [&](const Cut& cut) {  // of the rows that the item has
+    return min(C::kRows, rows_all - cut.item % qblocks * C::kRows) * (D / 4);
+  };
+  // Step `pass` of the join of a run's item.
+  auto step_of = [&](int r, int pass) {
+    const Cut cut = cut_of(r);
+    const uint32_t k0 = split.worker(cut.first), k1 = split.worker(cut.first + cut.units - 1), team = k0 / kTeam;
+    const uint32_t at = (blockIdx.x - k0) / kTeam, from = k0 + at * kTeam;
+    if (pass > 0) return Step{2 * kMaxCtas, team, team + (k1 - k0) / kTeam + 1, team, k0, 0, true};
+    if (k1 - k0 < kTurns * kBatch * max(kThreads / outs_of(cut), 1)) return Step{0, k0, k1 + 1, k0, k0, 0, true};
+    const uint32_t place = 2 * (team + at) + (at == 0);
+    return Step{0, from, min(from + kTeam, k1 + 1), k0, kMaxCtas + place, 2 * kMaxCtas + place, false};
+  };
 #pragma unroll 1
-  for (int slot = 0; slot < 2; ++slot) {
-    const int last = sh.last[slot];
-    if (last < 0) continue;
-    const Cut cut = sh.run[last].first >= 0 ? sh.tail[sh.run[last].first] : sh.head[sh.run[last].head];
-    const uint32_t k0 = split.worker(cut.first), k1 = split.worker(cut.first + cut.units - 1);
-    // Many parts: groups of threads take them in turn, and join through shared memory.
-    constexpr int kGroups = kOuts < C::kThreads ? C::kThreads / kOuts : 1;
-    const int groups = k1 - k0 + 1 > kBatch ? kGroups : 1;
-    float* mid = reinterpret_cast<float*>(smem);  // [thread][6]
-#pragma unroll 1
-    for (int i = tid; i < groups * kOuts; i += kThreads) {
-      const int grp = i / kOuts, at = i % kOuts, row = at / (D / 4), c = at % (D / 4) * 4;
-      const int64_t to = sh.row_at[last][row];
-      if (to < 0) continue;
-      Sum s;
-#pragma unroll 1
-      for (uint32_t k = k0 + grp; k <= k1; k += kBatch * groups) {
-        float mk[kBatch], lk[kBatch];
-        float4 v[kBatch];
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-          const uint32_t kk = k + x * groups;
-          const float* q = cta_parts + (2 * static_cast<int64_t>(kk) + (kk == k0 ? 1 : 0)) * C::kPart;
-          const bool in = kk <= k1;
-          mk[x] = in ? __ldcg(q + C::kTop + row) : -INFINITY;
-          lk[x] = in ? __ldcg(q + C::kSum + row) : 0.f;
-          v[x] = in ? __ldcg(reinterpret_cast<const float4*>(q + row * C::kPitch + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int pass = 0; pass < 2; ++pass) {
+    // A CTA is the first one of at most one item that goes on after it: that item's counter is
+    // the first CTA's.  (The barrier before orders the CTA's stores; the ticket's release covers
+    // them.)
+    if (tid == 0 || tid == 32) {
+      const int side = tid == 0 ? 0 : 1, r = pass > 0 ? sh.last[side] : side == 0 ? 0 : sh.runs - 1;
+      int last = -1;
+      if (pass > 0 ? r >= 0 && !sh.ends[side] : r >= side && r < sh.runs && sh.run[r].slot >= 0) {
+        const Step step = step_of(r, pass);
+        if (take_ticket(counters + step.counter) == step.hi - step.lo - 1) {
+          counters[step.counter] = 0;  // every contributor has its ticket: ready for the next call
+          last = r;
+          sh.ends[side] = step.ends;
         }
+      }
+      sh.last[side] = last;
+    }
+    __syncthreads();
+    if (sh.last[0] < 0 && sh.last[1] < 0) return;
+
+    // ---- the steps whose last part was this CTA's.  The outputs of both are one row of outputs
+    // of four columns; a thread takes kAtOnce of them, and asks for kBatch parts of each
+    // together.  Many parts of few outputs: groups of threads take the parts in turn, and join
+    // through shared memory.
+    Step step[2];
+    uint32_t most = 0;
+    int outs[2];
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) s.add(mk[x], lk[x], v[x]);
+    for (int side = 0; side < 2; ++side) {
+      const int last = sh.last[side];
+      outs[side] = 0;
+      step[side] = Step{0, 0, 0, 0, 0, 0, true};
+      if (last < 0) continue;
+      step[side] = step_of(last, pass);
+      outs[side] = outs_of(cut_of(last));
+      most = max(most, step[side].hi - step[side].lo);
+    }
+    const int n = outs[0] + outs[1];
+    const int groups = most > kBatch && 2 * n <= kThreads ? kThreads / n : 1;
+    float* mid = reinterpret_cast<float*>(smem);  // [thread][6]
+    auto emit = [&](const Sum& s, bool second, int at) {
+      const int row = at / (D / 4), c = at % (D / 4) * 4;
+      if (second ? step[1].ends : step[0].ends) {
+        *reinterpret_cast<uint2*>(p.O + sh.row_at[sh.last[second]][row] + c) = s.value();
+        return;
+      }
+      float* out = cta_parts + static_cast<int64_t>(second ? step[1].sum : step[0].sum) * C::kPart;
+      __stcg(reinterpret_cast<float4*>(out + row * C::kPitch + c), s.v);
+      if (c == 0) {
+        __stcg(out + C::kTop + row, s.m);
+        __stcg(out + C::kSum + row, s.l);
+      }
+    };
+#pragma unroll 1
+    for (int i0 = tid; i0 < groups * n; i0 += kAtOnce * kThreads) {
+      Sum s[kAtOnce];
+      int at[kAtOnce], row[kAtOnce];
+      bool second[kAtOnce];
+      uint32_t k[kAtOnce];
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int i = i0 + x * kThreads, grp = groups > 1 ? i / n : 0, o = i - grp * n;
+        second[x] = o >= outs[0];
+        at[x] = i < groups * n ? o - (second[x] ? outs[0] : 0) : -1;
+        row[x] = at[x] >= 0 ? at[x] / (D / 4) : 0;
+        k[x] = (second[x] ? step[1].lo : step[0].lo) + grp;
+      }
+#pragma unroll 1
+      for (uint32_t done = 0; done < most; done += kBatch * groups) {
+        float mk[kAtOnce][kBatch], lk[kAtOnce][kBatch];
+        float4 v[kAtOnce][kBatch];
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x)
+#pragma unroll
+          for (int y = 0; y < kBatch; ++y) {
+            const uint32_t kk = k[x] + done + y * groups;
+            const Step& st = second[x] ? step[1] : step[0];
+            const float* q = cta_parts + static_cast<int64_t>(st.base + 2 * kk + (kk == st.first)) * C::kPart;
+            const bool in = at[x] >= 0 && kk < st.hi;
+            mk[x][y] = in ? __ldcg(q + C::kTop + row[x]) : -INFINITY;
+            lk[x][y] = in ? __ldcg(q + C::kSum + row[x]) : 0.f;
+            v[x][y] = in ? __ldcg(reinterpret_cast<const float4*>(q + row[x] * C::kPitch + at[x] % (D / 4) * 4))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) s[x].add(mk[x], lk[x], v[x]);
       }
       if (groups == 1) {
-        *reinterpret_cast<uint2*>(p.O + to + c) = s.value();
-      } else {
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x)
+          if (at[x] >= 0) emit(s[x], second[x], at[x]);
+      } else {  // (one turn)
         float* d = mid + tid * 6;
-        d[0] = s.m;
-        d[1] = s.l;
-        d[2] = s.v.x;
-        d[3] = s.v.y;
-        d[4] = s.v.z;
-        d[5] = s.v.w;
+        d[0] = s[0].m;
+        d[1] = s[0].l;
+        d[2] = s[0].v.x;
+        d[3] = s[0].v.y;
+        d[4] = s[0].v.z;
+        d[5] = s[0].v.w;
       }
     }
     if (groups > 1) {  // uniform over the CTA
       __syncthreads();
-      const int64_t to = tid < kOuts ? sh.row_at[last][tid / (D / 4)] : -1;
-      if (to >= 0) {
+      if (tid < n) {
         Sum s;
+#pragma unroll 4
         for (int x = 0; x < groups; ++x) {
-          const float* d = mid + (x * kOuts + tid) * 6;
-          s.add(d[0], d[1], make_float4(d[2], d[3], d[4], d[5]));
+          const float* d = mid + (x * n + tid) * 6;
+          const float mk[1] = {d[0]}, lk[1] = {d[1]};
+          const float4 v[1] = {make_float4(d[2], d[3], d[4], d[5])};
+          s.add(mk, lk, v);
         }
-        *reinterpret_cast<uint2*>(p.O + to + tid % (D / 4) * 4) = s.value();
+        const bool second = tid >= outs[0];
+        emit(s, second, tid - (second ? outs[0] : 0));
       }
-      __syncthreads();
     }
+    if (step[0].ends && step[1].ends) return;
+    __syncthreads();
   }
 }
 
@@ -953,7 +1044,7 @@ int tiles_of(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 template <int D, int NT>
 constexpr int64_t ws_bytes() {
   using C = Cfg<D, NT>;
-  return kCounterBytes + static_cast<int64_t>(kMaxCtas) * (C::kWarps + 2) * C::kPart * 4;
+  return kCounterBytes + (static_cast<int64_t>(kMaxCtas) * (C::kWarps + 2) + kTeams) * C::kPart * 4;
 }
 
 }  // namespace

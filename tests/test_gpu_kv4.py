@@ -195,6 +195,16 @@ def test_attention_batches(torch, lens):
     check(torch, lens, 1, 8, 2, 128, 64, seed=len(lens))
 
 
+@pytest.mark.parametrize("lens,lq,hq,d", [([6000], 1, 16, 128), ([9000, 0, 4000], 2, 16, 64), ([20000], 1, 8, 64),
+                                          ([3000, 2600, 2700], 1, 32, 128), ([40, 4100, 4200, 70], 1, 16, 128)])
+def test_attention_of_long_sequences_and_one_cache_head(torch, lens, lq, hq, d):
+    # So many CTAs share a sequence that their sums are joined in two steps; twice with one workspace.
+    ws = torch.zeros(dg.dg_attention_kv4_workspace_bytes(len(lens), lq, hq, 1, d), dtype=torch.uint8, device="cuda")
+    for seed in (1, 2):
+        check(torch, lens, lq, hq, 1, d, 64, seed=seed, ws=ws)
+    assert not ws[:1024].any()
+
+
 def test_attention_strides(torch):
     check(torch, [130, 40], 2, 4, 2, 128, 16, pad=72, batch_pad=16)
 
