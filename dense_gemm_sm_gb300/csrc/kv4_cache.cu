@@ -28,7 +28,9 @@
 namespace dg {
 namespace {
 
-constexpr int kThreads = 256;
+// Small CTAs, so that what does not fill the last wave is little: 8192 tokens of 8 heads written and
+// read back take 23.3 us, with 256 threads 26.1 (64: 23.1, but 2000 tokens 12.4 and not 10.6).
+constexpr int kThreads = 128;
 
 // Byte offset, in its record, of the two-byte piece of V codes that holds columns
 // [4 m, 4 m + 4) of token u (0..15).
@@ -245,7 +247,7 @@ Shape shape_of(const Kv4Params& p, int sms, int most) {
   s.heads_per_warp = static_cast<int>((p.heads + runs - 1) / runs);
   s.in_flight = p.heads % most == 0 && s.heads_per_warp >= most ? most : p.heads % 4 == 0 && s.heads_per_warp >= 4 ? 4 : 1;
   s.heads_per_warp = (s.heads_per_warp + s.in_flight - 1) / s.in_flight * s.in_flight;
-  const int64_t need = (p.tokens + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<int64_t>(sms) * 8;
+  const int64_t need = (p.tokens + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<int64_t>(sms) * 16;
   s.grid = dim3(static_cast<unsigned>(need < cap ? need : cap),
                 static_cast<unsigned>((p.heads + s.heads_per_warp - 1) / s.heads_per_warp));
   return s;
