@@ -24,6 +24,7 @@ namespace {
 
 struct None {};
 
+
 __device__ __forceinline__ float bits_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bits_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -48,6 +49,55 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+// The same from any address: the 16-byte words that hold them, and a shift that is one of the
+// whole row, so no lane goes its own way.
+__device__ __forceinline__ void load8_any(const uint16_t* p, float (&v)[8]) {
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / 2;
+  const uint4* g = reinterpret_cast<const uint4*>(p - shift);
+  const uint4 a = g[0];
+  uint32_t w[7] = {a.x, a.y, a.z, a.w, 0, 0, 0};
+  if (shift != 0) {
+    const uint4 b = g[1];
+    if (shift & 4) {
+      w[0] = a.z; w[1] = a.w; w[2] = b.x; w[3] = b.y; w[4] = b.z; w[5] = b.w;
+    } else {
+      w[4] = b.x; w[5] = b.y; w[6] = b.z;
+    }
+    if (shift & 2) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (shift & 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __byte_perm(w[i], w[i + 1], 0x5432);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bits_lo(w[i]);
+    v[2 * i + 1] = bits_hi(w[i]);
+  }
+}
+__device__ __forceinline__ void load8_any(const float* p, float (&v)[8]) {
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / 4;
+  const float4* g = reinterpret_cast<const float4*>(p - shift);
+  const float4 a = g[0], b = g[1];
+  float w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0.f, 0.f, 0.f, 0.f};
+  if (shift != 0) {
+    const float4 c = g[2];
+    w[8] = c.x; w[9] = c.y; w[10] = c.z; w[11] = c.w;
+    if (shift & 2) {
+#pragma unroll
+      for (int i = 0; i < 10; ++i) w[i] = w[i + 2];
+    }
+    if (shift & 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = w[i + 1];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = w[i];
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
@@ -91,10 +141,17 @@ __device__ __forceinline__ void row_reduce(float& sum, float& top, bool cta, flo
 }
 
 // One row per 32 threads (8 rows a CTA) or per CTA of tpr threads, C chunks of 8 elements a
-// thread.  VEC: chunk i of thread t is elements [8 (i tpr + t), + 8); otherwise a thread takes
-// elements t, t + tpr, ... one by one, so that a warp's accesses stay contiguous.
-template <typename XT, typename RT, typename YT, bool VEC, int C>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p, const int tpr) {
+// thread.
+//   kAligned: chunk i of thread t is elements [8 (i tpr + t), + 8);
+//   kShifted: rows begin anywhere, but those of H as far from an aligned address as those of Y:
+//     chunks are the aligned ones of Y, what is read comes from any address; chunks within 8
+//     elements of the row's ends go one element at a time, so that nothing outside is read;
+//   kSingle: a thread takes elements t, t + tpr, ... one by one, so that a warp's accesses stay
+//     contiguous.
+enum Mode { kSingle, kAligned, kShifted };
+// (Two CTAs an SM cost the shifted form a few spills: 8192 x 4096, FP32 residual, codes, 99 -> 84 us.)
+template <typename XT, typename RT, typename YT, Mode M, int C>
+__global__ void __launch_bounds__(1024, M == kShifted && C == 1 ? 2 : 0) rmsnorm_kernel(const NormParams p, const int tpr) {
   constexpr bool kRes = !std::is_same<RT, None>::value;
   constexpr bool kCodes = std::is_same<YT, uint8_t>::value;
   using R = typename std::conditional<kRes, RT, float>::type;
@@ -110,31 +167,40 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p, const
   R* hout = kRes ? static_cast<R*>(p.H) + r * p.ldh : nullptr;
   YT* y = static_cast<YT*>(p.Y) + r * p.ldy;
   const int cols = static_cast<int>(p.cols);
+  const int skip = M == kShifted ? static_cast<int>(reinterpret_cast<uintptr_t>(y) / sizeof(YT) & 7) : 0;
   // An index of this thread's element j of chunk i.
-  auto at = [&](int i, int j) { return VEC ? (i * tpr + t) * 8 + j : (8 * i + j) * tpr + t; };
+  auto at = [&](int i, int j) { return M == kSingle ? (8 * i + j) * tpr + t : (i * tpr + t) * 8 + j - skip; };
+  auto inside = [&](int i, int j) { return (M != kShifted || at(i, j) >= 0) && at(i, j) < cols; };
+  auto whole = [&](int i) {
+    return M == kAligned ? at(i, 8) <= cols : M == kShifted && at(i, 0) >= 8 && at(i, 16) <= cols;
+  };
+  auto load = [&](const auto* from, float (&v)[8]) {
+    if constexpr (M == kShifted) load8_any(from, v);
+    else load8(from, v);
+  };
   float h[C][8];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    if (VEC && at(i, 8) <= cols) {
-      load8(x + at(i, 0), h[i]);
+    if (whole(i)) {
+      load(x + at(i, 0), h[i]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = at(i, j) < cols ? load1(x + at(i, j)) : 0.f;
+      for (int j = 0; j < 8; ++j) h[i][j] = inside(i, j) ? load1(x + at(i, j)) : 0.f;
     }
   }
   if (kRes) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float v[8];
-      if (VEC && at(i, 8) <= cols) {
-        load8(res + at(i, 0), v);
+      if (whole(i)) {
+        load(res + at(i, 0), v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] += v[j];
         store8(hout + at(i, 0), h[i]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (at(i, j) < cols) {
+          if (inside(i, j)) {
             h[i][j] += load1(res + at(i, j));
             store1(hout + at(i, j), h[i][j]);
           }
@@ -146,11 +212,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p, const
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     float w[8];
-    if (VEC && at(i, 8) <= cols) {
-      load8(p.gain + at(i, 0), w);
+    if (whole(i)) {
+      load(p.gain + at(i, 0), w);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = at(i, j) < cols ? load1(p.gain + at(i, j)) : 0.f;
+      for (int j = 0; j < 8; ++j) w[j] = inside(i, j) ? load1(p.gain + at(i, j)) : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -171,12 +237,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p, const
   for (int i = 0; i < C; ++i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[i][j] = kCodes ? h[i][j] * f * inv : h[i][j] * f;
-    if (VEC && at(i, 8) <= cols) {
+    if (whole(i)) {
       store8(y + at(i, 0), h[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (at(i, j) < cols) store1(y + at(i, j), h[i][j]);
+        if (inside(i, j)) store1(y + at(i, j), h[i][j]);
     }
   }
 }
@@ -221,36 +287,47 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormParams p) 
 }
 
 template <typename XT, typename RT, typename YT>
-cudaError_t launch_typed(const NormParams& p, bool vec, cudaStream_t s) {
-  const int64_t chunks = (p.cols + 7) / 8;
+cudaError_t launch_typed(const NormParams& p, Mode m, cudaStream_t s) {
+  // Shifted chunks pay from 128 elements a row (16384 rows of 100, 200, 1000 BF16: 9.3, 10.3, 29 us,
+  // one at a time 8.7, 14.7, 69).  FP32 elements fill a warp's accesses one at a time too: few
+  // short rows are faster so (1000 x 777: 3.3 us and 3.5; with a residual and codes 4.8 and 6.4;
+  // 16384 x 777: 26 and 19.5; 1000 x 2777: 7.6 and 5.6).
+  constexpr bool kWide = std::is_same<XT, float>::value || std::is_same<RT, float>::value;
+  const int64_t least = kWide && p.rows * p.cols < (int64_t{1} << 22) ? 1024 : 128;
+  if (m == kShifted && p.cols < least) m = kSingle;
+  const int64_t chunks = (p.cols + (m == kShifted ? 14 : 7)) / 8;
   // Chunks a thread: 1 for as long as a CTA holds the row (16384 x 4096 with an FP32 residual:
   // 107 us, 118 with 2, 124 with 4), except that rows of up to 512 elements then fit a warp with
   // 2 (16384 x 512: 17.3 us in CTAs of 64 threads, 13.8 so); over 8192 elements 4 (2048 x 16384:
-  // 58 us, 65 with 2).  Unaligned rows over 8192 elements take the two-pass kernel: an element at
-  // a time, more than 8 do not stay in registers.
-  if (chunks > (vec ? 4 : 1) * 1024)
+  // 58 us, 65 with 2), shifted 2 (4096 x 8190: 82 us, one element at a time 191).  Longer rows,
+  // and those over 8192 elements that go one at a time, take the two-pass kernel: they do not stay
+  // in registers (2048 x 16384 shifted, 4 chunks: 116 us, in two passes 80).
+  if (chunks > (m == kSingle ? 1 : m == kShifted ? 2 : 4) * 1024)
     return launch_pdl(rmsnorm_long_kernel<XT, RT, YT>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, s, p);
-  const int c = !vec ? 1 : chunks > 1024 ? 4 : chunks > 32 && chunks <= 64 ? 2 : 1;
+  const int c = chunks > 1024 ? (m == kShifted ? 2 : 4) : m == kAligned && chunks > 32 && chunks <= 64 ? 2 : 1;
   int tpr = static_cast<int>((chunks + c - 1) / c);
   tpr = (tpr + 31) / 32 * 32;
   const int rows_per_cta = tpr == 32 ? 8 : 1;
   const dim3 grid(static_cast<unsigned>((p.rows + rows_per_cta - 1) / rows_per_cta)), block(tpr * rows_per_cta);
-  if (vec)
-    return c == 1   ? launch_pdl(rmsnorm_kernel<XT, RT, YT, true, 1>, grid, block, 0, s, p, tpr)
-           : c == 2 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, true, 2>, grid, block, 0, s, p, tpr)
-                    : launch_pdl(rmsnorm_kernel<XT, RT, YT, true, 4>, grid, block, 0, s, p, tpr);
-  return launch_pdl(rmsnorm_kernel<XT, RT, YT, false, 1>, grid, block, 0, s, p, tpr);
+  if (m == kAligned)
+    return c == 1   ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 1>, grid, block, 0, s, p, tpr)
+           : c == 2 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 2>, grid, block, 0, s, p, tpr)
+                    : launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 4>, grid, block, 0, s, p, tpr);
+  if (m == kShifted)
+    return c == 1 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kShifted, 1>, grid, block, 0, s, p, tpr)
+                  : launch_pdl(rmsnorm_kernel<XT, RT, YT, kShifted, 2>, grid, block, 0, s, p, tpr);
+  return launch_pdl(rmsnorm_kernel<XT, RT, YT, kSingle, 1>, grid, block, 0, s, p, tpr);
 }
 
 template <typename XT, typename RT>
-cudaError_t launch_out(const NormParams& p, bool vec, cudaStream_t s) {
-  return p.scales ? launch_typed<XT, RT, uint8_t>(p, vec, s) : launch_typed<XT, RT, uint16_t>(p, vec, s);
+cudaError_t launch_out(const NormParams& p, Mode m, cudaStream_t s) {
+  return p.scales ? launch_typed<XT, RT, uint8_t>(p, m, s) : launch_typed<XT, RT, uint16_t>(p, m, s);
 }
 
 template <typename XT>
-cudaError_t launch_res(const NormParams& p, bool r_f32, bool vec, cudaStream_t s) {
-  if (!p.R) return launch_out<XT, None>(p, vec, s);
-  return r_f32 ? launch_out<XT, float>(p, vec, s) : launch_out<XT, uint16_t>(p, vec, s);
+cudaError_t launch_res(const NormParams& p, bool r_f32, Mode m, cudaStream_t s) {
+  if (!p.R) return launch_out<XT, None>(p, m, s);
+  return r_f32 ? launch_out<XT, float>(p, m, s) : launch_out<XT, uint16_t>(p, m, s);
 }
 
 }  // namespace
@@ -258,7 +335,12 @@ cudaError_t launch_res(const NormParams& p, bool r_f32, bool vec, cudaStream_t s
 cudaError_t launch_rmsnorm(const NormParams& p, bool x_f32, bool r_f32, bool vec, int sms,
                            cudaStream_t s) {
   (void)sms;
-  return x_f32 ? launch_res<float>(p, r_f32, vec, s) : launch_res<uint16_t>(p, r_f32, vec, s);
+  // Where rows of H and of Y are equally far from an aligned address.
+  const uint64_t y = reinterpret_cast<uintptr_t>(p.Y) / (p.scales ? 1 : 2), h = reinterpret_cast<uintptr_t>(p.H) / (r_f32 ? 4 : 2);
+  const uint64_t period = r_f32 ? 4 : 8;  // elements of 16 bytes of H
+  const bool together = !p.R || ((h - y) % period == 0 && (p.rows == 1 || static_cast<uint64_t>(p.ldh - p.ldy) % period == 0));
+  const Mode m = vec ? kAligned : together ? kShifted : kSingle;
+  return x_f32 ? launch_res<float>(p, r_f32, m, s) : launch_res<uint16_t>(p, r_f32, m, s);
 }
 
 }  // namespace dg

@@ -117,6 +117,53 @@ def test_types_strides_and_alignment(torch, xt, rt, e4m3, ld_off):
     run(torch, 37, 1000, t[xt], t[rt], ld_off[0], ld_off[1], e4m3, ldy=1005 if ld_off[1] == 3 else 1000)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("xt,rt", [("bf16", "none"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32"), ("f32", "none"), ("f32", "f32")])
+@pytest.mark.parametrize("cols,ld", [(128, 133), (143, 143), (600, 605), (1031, 1033), (4096, 4101), (8179, 8179), (9001, 9010), (16500, 16501)])
+def test_rows_that_begin_anywhere(torch, cols, ld, xt, rt, e4m3):
+    # Each operand a different distance from an aligned address, H and Y the same.
+    t = {"bf16": torch.bfloat16, "f32": torch.float32, "none": None}
+    xt, rt = t[xt], t[rt]
+    rows = 5
+    for k in range(8):
+        _, X = make(torch, (rows, cols), ld + 2 * k, xt, k, offset=k)
+        _, R = make(torch, (rows, cols), ld + k, rt, 20 + k, offset=(5 * k + 3) % 8) if rt is not None else (None, None)
+        _, gain = make(torch, (1, cols), cols, torch.bfloat16, 40 + k, offset=(3 * k + 1) % 8)
+        H0, H = make(torch, (rows, cols), ld, rt, 60 + k, offset=7 - k) if rt is not None else (None, None)
+        keep = None if H0 is None else H0.clone()
+        Y0 = torch.full((rows * ld + 16,), 0xA5 if e4m3 else 7.0, dtype=torch.uint8 if e4m3 else torch.bfloat16, device="cuda")
+        Y = Y0[7 - k:7 - k + rows * ld].view(rows, ld)[:, :cols]
+        s = torch.full((rows,), -1.0, device="cuda")
+        T = {torch.float32: dg.DG_OUT_F32, torch.bfloat16: dg.DG_OUT_BF16, None: dg.DG_OUT_BF16}
+        args = (rows, cols, X, ld + 2 * k, T[xt], R, ld + k if R is not None else 0, T[rt], H, ld if R is not None else 0, gain, EPS)
+        if e4m3:
+            dg.rmsnorm_residual_e4m3(*args, Y, ld, s)
+        else:
+            dg.rmsnorm_residual_bf16(*args, Y, ld)
+        sync(torch)
+        h, y = ref.rmsnorm(host(X), None if R is None else host(R), host(gain)[0], EPS)
+        if e4m3:
+            check_codes(torch, y, Y.contiguous(), s, cols)
+            if H is not None:
+                check(torch, h, np.zeros_like(y), H, torch.zeros_like(X), rt, cols)
+        else:
+            check(torch, h, y, H, Y, rt, cols)
+        for buf, old, off in ((Y0, None, 7 - k), (H0, keep, 7 - k)):  # nothing around the rows is written
+            if buf is None:
+                continue
+            mask = torch.ones_like(buf, dtype=torch.bool)
+            mask[off:off + rows * ld].view(rows, ld)[:, :cols] = False
+            got = buf[mask]
+            same = (got == (0xA5 if e4m3 else 7.0)) if old is None else (got == old[mask]) | (got.isnan() & old[mask].isnan())
+            assert bool(same.all())
+
+
+@pytest.mark.parametrize("cols,ld", [(777, 777), (4099, 4100)])
+@pytest.mark.parametrize("rt", ["bf16", "f32"])
+def test_in_place_residual_of_rows_that_begin_anywhere(torch, cols, ld, rt):
+    run(torch, 6, cols, torch.bfloat16, torch.bfloat16 if rt == "bf16" else torch.float32, ld, 0, False, inplace=True, ldy=ld)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 8, 9, 4097])
 @pytest.mark.parametrize("cols", [96, 520])
 def test_rows(torch, rows, cols):
