@@ -119,10 +119,11 @@ __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = static_cast<
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint8_t* p, float v) { *p = static_cast<uint8_t>(pack_e4m3(v, 0.f)); }
 
-// Sum and maximum over the threads of one row: a warp, or the whole CTA.
-__device__ __forceinline__ void row_reduce(float& sum, float& top, bool cta, float2* scratch) {
+// Sum and maximum over the threads of one row: `lanes` of a warp, or the whole CTA.
+__device__ __forceinline__ void row_reduce(float& sum, float& top, int lanes, bool cta, float2* scratch) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
+    if (o >= lanes) continue;
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
@@ -140,8 +141,9 @@ __device__ __forceinline__ void row_reduce(float& sum, float& top, bool cta, flo
   }
 }
 
-// One row per 32 threads (8 rows a CTA) or per CTA of tpr threads, C chunks of 8 elements a
-// thread.
+// One row per CTA of tpr threads, per warp (8 rows a CTA) or, PART, per tpr = 8 or 16 lanes, C
+// chunks of 8 elements a thread (200000 rows of 128: 19 us, 48 in warps half of which idle; 64 wide
+// with a residual and codes 16 and 74).
 //   kAligned: chunk i of thread t is elements [8 (i tpr + t), + 8);
 //   kShifted: rows begin anywhere, but those of H as far from an aligned address as those of Y:
 //     chunks are the aligned ones of Y, what is read comes from any address; chunks within 8
@@ -150,7 +152,7 @@ __device__ __forceinline__ void row_reduce(float& sum, float& top, bool cta, flo
 //     contiguous.
 enum Mode { kSingle, kAligned, kShifted };
 // (Two CTAs an SM cost the shifted form a few spills: 8192 x 4096, FP32 residual, codes, 99 -> 84 us.)
-template <typename XT, typename RT, typename YT, Mode M, int C>
+template <typename XT, typename RT, typename YT, Mode M, int C, bool PART = false>
 __global__ void __launch_bounds__(1024, M == kShifted && C == 1 ? 2 : 0) rmsnorm_kernel(const NormParams p, const int tpr) {
   constexpr bool kRes = !std::is_same<RT, None>::value;
   constexpr bool kCodes = std::is_same<YT, uint8_t>::value;
@@ -158,15 +160,18 @@ __global__ void __launch_bounds__(1024, M == kShifted && C == 1 ? 2 : 0) rmsnorm
   __shared__ float2 scratch[32];
   pdl_trigger();
   pdl_wait();  // launched with programmatic serialisation: X may come from the previous kernel
-  const bool cta = tpr > 32;
-  const int t = cta ? threadIdx.x : (threadIdx.x & 31);
-  const int64_t r = cta ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (r >= p.rows) return;  // whole warps: a CTA of several rows has no barrier
+  const bool cta = !PART && tpr > 32;
+  const int t = cta ? threadIdx.x : (threadIdx.x & (PART ? tpr - 1 : 31)), shift = PART && tpr == 8 ? 3 : PART ? 4 : 5;
+  const int64_t r = cta ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * (blockDim.x >> shift) + (threadIdx.x >> shift);
+  // A CTA of several rows has no barrier, so whole warps can go; part of one past the last row
+  // stays for the others' sums.
+  const bool live = r < p.rows;
+  if (!PART && !live) return;
   const XT* x = static_cast<const XT*>(p.X) + r * p.ldx;
   const R* res = kRes ? static_cast<const R*>(p.R) + r * p.ldr : nullptr;
   R* hout = kRes ? static_cast<R*>(p.H) + r * p.ldh : nullptr;
   YT* y = static_cast<YT*>(p.Y) + r * p.ldy;
-  const int cols = static_cast<int>(p.cols);
+  const int cols = !PART || live ? static_cast<int>(p.cols) : 0;
   const int skip = M == kShifted ? static_cast<int>(reinterpret_cast<uintptr_t>(y) / sizeof(YT) & 7) : 0;
   // An index of this thread's element j of chunk i.
   auto at = [&](int i, int j) { return M == kSingle ? (8 * i + j) * tpr + t : (i * tpr + t) * 8 + j - skip; };
@@ -225,13 +230,13 @@ __global__ void __launch_bounds__(1024, M == kShifted && C == 1 ? 2 : 0) rmsnorm
       if (kCodes) top = fmaxf(top, fabsf(h[i][j]));
     }
   }
-  row_reduce(sum, top, cta, scratch);
-  float f = 1.f / sqrtf(sum / static_cast<float>(cols) + p.eps);
+  row_reduce(sum, top, PART ? tpr : 32, cta, scratch);
+  float f = 1.f / sqrtf(sum / static_cast<float>(static_cast<int>(p.cols)) + p.eps);
   float inv = 1.f;
   if (kCodes) {
     const float amax = top * f;
     inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 0.f;
-    if (t == 0) p.scales[r] = __fdiv_rn(amax, 448.f);
+    if (t == 0 && (!PART || live)) p.scales[r] = __fdiv_rn(amax, 448.f);
   }
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormParams p) 
     sum = fmaf(h, h, sum);
     if (kCodes) top = fmaxf(top, fabsf(h * load1(p.gain + c)));
   }
-  row_reduce(sum, top, true, scratch);
+  row_reduce(sum, top, 32, true, scratch);
   const float f = 1.f / sqrtf(sum / static_cast<float>(p.cols) + p.eps);
   float inv = 1.f;
   if (kCodes) {
@@ -306,9 +311,12 @@ cudaError_t launch_typed(const NormParams& p, Mode m, cudaStream_t s) {
     return launch_pdl(rmsnorm_long_kernel<XT, RT, YT>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, s, p);
   const int c = chunks > 1024 ? (m == kShifted ? 2 : 4) : m == kAligned && chunks > 32 && chunks <= 64 ? 2 : 1;
   int tpr = static_cast<int>((chunks + c - 1) / c);
-  tpr = (tpr + 31) / 32 * 32;
-  const int rows_per_cta = tpr == 32 ? 8 : 1;
+  tpr = tpr <= 8 ? 8 : tpr <= 16 ? 16 : (tpr + 31) / 32 * 32;
+  const int rows_per_cta = tpr <= 32 ? 256 / tpr : 1;
   const dim3 grid(static_cast<unsigned>((p.rows + rows_per_cta - 1) / rows_per_cta)), block(tpr * rows_per_cta);
+  if (tpr < 32)  // (the shifted form begins with longer rows)
+    return m == kAligned ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 1, true>, grid, block, 0, s, p, tpr)
+                         : launch_pdl(rmsnorm_kernel<XT, RT, YT, kSingle, 1, true>, grid, block, 0, s, p, tpr);
   if (m == kAligned)
     return c == 1   ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 1>, grid, block, 0, s, p, tpr)
            : c == 2 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 2>, grid, block, 0, s, p, tpr)

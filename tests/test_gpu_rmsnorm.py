@@ -164,6 +164,14 @@ def test_in_place_residual_of_rows_that_begin_anywhere(torch, cols, ld, rt):
     run(torch, 6, cols, torch.bfloat16, torch.bfloat16 if rt == "bf16" else torch.float32, ld, 0, False, inplace=True, ldy=ld)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", [1, 3, 4, 15, 17, 31, 33, 70])
+@pytest.mark.parametrize("cols,ld", [(1, 1), (5, 9), (40, 40), (64, 64), (65, 65), (120, 128), (127, 127), (128, 136)])
+def test_short_rows(torch, rows, cols, ld, e4m3):
+    run(torch, rows, cols, torch.bfloat16, torch.float32, ld, 0, e4m3)
+    run(torch, rows, cols, torch.float32, torch.bfloat16, ld, 0, e4m3, inplace=True, ldy=ld)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 8, 9, 4097])
 @pytest.mark.parametrize("cols", [96, 520])
 def test_rows(torch, rows, cols):
