@@ -303,13 +303,17 @@ cudaError_t launch_typed(const NormParams& p, Mode m, cudaStream_t s) {
   const int64_t chunks = (p.cols + (m == kShifted ? 14 : 7)) / 8;
   // Chunks a thread: 1 for as long as a CTA holds the row (16384 x 4096 with an FP32 residual:
   // 107 us, 118 with 2, 124 with 4), except that rows of up to 512 elements then fit a warp with
-  // 2 (16384 x 512: 17.3 us in CTAs of 64 threads, 13.8 so); over 8192 elements 4 (2048 x 16384:
-  // 58 us, 65 with 2), shifted 2 (4096 x 8190: 82 us, one element at a time 191).  Longer rows,
+  // 2 (16384 x 512: 17.3 us in CTAs of 64 threads, 13.8 so); over 8192 elements 3 or 4
+  // (2048 x 16384: 58 us with 4, 65 with 2): what leaves more CTAs of 64 registers a thread to an SM,
+  // and 3 where both leave the same (4096 x 12288, residual, codes: 84 us with 3, 99 with 4; 4096 x
+  // 10240 81 and 72); shifted 2 (4096 x 8190: 82 us, one element at a time 191).  Longer rows,
   // and those over 8192 elements that go one at a time, take the two-pass kernel: they do not stay
   // in registers (2048 x 16384 shifted, 4 chunks: 116 us, in two passes 80).
   if (chunks > (m == kSingle ? 1 : m == kShifted ? 2 : 4) * 1024)
     return launch_pdl(rmsnorm_long_kernel<XT, RT, YT>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, s, p);
-  const int c = chunks > 1024 ? (m == kShifted ? 2 : 4) : m == kAligned && chunks > 32 && chunks <= 64 ? 2 : 1;
+  auto threads = [&](int64_t each) { return ((chunks + each - 1) / each + 31) / 32 * 32; };
+  const bool three = threads(3) <= 1024 && 1024 / threads(3) == 1024 / threads(4);
+  const int c = chunks > 1024 ? (m == kShifted ? 2 : three ? 3 : 4) : m == kAligned && chunks > 32 && chunks <= 64 ? 2 : 1;
   int tpr = static_cast<int>((chunks + c - 1) / c);
   tpr = tpr <= 8 ? 8 : tpr <= 16 ? 16 : (tpr + 31) / 32 * 32;
   const int rows_per_cta = tpr <= 32 ? 256 / tpr : 1;
@@ -320,6 +324,7 @@ cudaError_t launch_typed(const NormParams& p, Mode m, cudaStream_t s) {
   if (m == kAligned)
     return c == 1   ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 1>, grid, block, 0, s, p, tpr)
            : c == 2 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 2>, grid, block, 0, s, p, tpr)
+           : c == 3 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 3>, grid, block, 0, s, p, tpr)
                     : launch_pdl(rmsnorm_kernel<XT, RT, YT, kAligned, 4>, grid, block, 0, s, p, tpr);
   if (m == kShifted)
     return c == 1 ? launch_pdl(rmsnorm_kernel<XT, RT, YT, kShifted, 1>, grid, block, 0, s, p, tpr)

@@ -172,6 +172,13 @@ def test_short_rows(torch, rows, cols, ld, e4m3):
     run(torch, rows, cols, torch.float32, torch.bfloat16, ld, 0, e4m3, inplace=True, ldy=ld)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("cols", [8208, 10240, 12288, 12296, 20000, 24576, 24584])
+def test_long_rows(torch, cols, e4m3):
+    run(torch, 3, cols, torch.bfloat16, torch.bfloat16, cols, 0, e4m3)
+    run(torch, 2, cols, torch.float32, None, cols + 8, 0, e4m3)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 8, 9, 4097])
 @pytest.mark.parametrize("cols", [96, 520])
 def test_rows(torch, rows, cols):
