@@ -92,6 +92,13 @@ def test_sizes(torch, K, I, T):
     check(torch, T, K, I, 5, 3)
 
 
+# Rows off 128-byte lines: CTAs in groups on neighbouring column tiles, the last group's tiles fewer.
+@pytest.mark.parametrize("K,I", [(1288, 1160), (1160, 2056), (2600, 520), (520, 2600), (264, 1032)])
+@pytest.mark.parametrize("T", [1, 24, 64])
+def test_rows_off_lines(torch, K, I, T):
+    check(torch, T, K, I, 6, 2)
+
+
 @pytest.mark.parametrize("E,top", [(1, 1), (2, 1), (2, 2), (8, 8), (16, 16), (33, 4), (64, 8), (128, 1), (512, 3)])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_experts(torch, E, top, renorm):
