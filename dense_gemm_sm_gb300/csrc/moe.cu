@@ -45,8 +45,10 @@ constexpr int kWarps = kThreads / 32;
 static_assert(kMaxE == kThreads, "a thread per expert");
 constexpr int kPrefetch = 16;        // units of W_d after its ring that a CTA asks L2 for early
 // Small calls: a CTA is given at least this many units, as a join of many parts costs more than
-// a few more units in a row.
-constexpr uint32_t kMinUp = 2, kMinDown = 4;
+// a few more units in a row (up 2, 4 or 8, us: one token, 4 of 32 experts of 1024 x 512 16.1, 15.8,
+// 17.1; 6 tokens, 2 of 8 of 904 x 74 22.1, 18.2, 20.2; down 3, 4 or 8: 16.7, 15.8, 16.7 and 20.0, 18.2,
+// 19.0).
+constexpr uint32_t kMinUp = 4, kMinDown = 4;
 
 // Workspace: counters (zero between calls), the tokens' choices (calls with a routing launch),
 // parts of cut tiles, Z (rows sorted by expert, then the same rows' remainders).
