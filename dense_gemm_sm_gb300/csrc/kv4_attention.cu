@@ -80,7 +80,7 @@ struct Cfg {
   static constexpr int kQ = NT == 4 ? NT * (D / 16) * 32 * 8 : 0;  // a warp's Q fragments (registers otherwise)
   static constexpr int kSmem = kRing + kWarps * kQ;
   static_assert(kWarps * kPart * 4 <= kRing, "the warps' last parts take the ring's place");
-  static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
+  static_assert(kSmem + 4096 <= 227 * 1024, "shared memory, with the static part");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -238,6 +238,7 @@ struct Shared {
   } run[kWarps + 1];
   // Where a row of a run's item goes in O; -1: no such row.
   int64_t row_at[kWarps + 1][8 * NT];
+  uint32_t issued[kWarps];     // stages of a ring that were filled, over the whole call
   uint32_t abort;
 };
 
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     }
   if (tid == 0) sh.abort = 0;
   if (tid < 2) sh.last[tid] = -1;
-  if (tid < kWarps) sh.has_head[tid] = sh.has_tail[tid] = 0;
+  if (tid < kWarps) sh.has_head[tid] = sh.has_tail[tid] = 0, sh.issued[tid] = 0;
   fence_barrier_init();
   __syncthreads();
   pdl_trigger();
@@ -425,6 +426,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       uint32_t put = 0;  // slot, and its phase in bit 8
       uint32_t fresh = C::kStages;  // slots never used
       uint64_t since = 0;
+      uint32_t issued = 0;
 #pragma unroll 1
       for (;;) {
         const uint32_t s = put & 255u;
@@ -459,10 +461,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           bulk_load(to + s * C::kUnitBytes + i * C::kRec, src, p.one_copy ? nrec * C::kRec : C::kRec, bar);
         }
         put = s + 1 == C::kStages ? (put & 256u) ^ 256u : put + 1;
+        ++issued;
         if (at.r + 1 >= r1) break;
         move_to(at, at.r + 1);
         look_up();
       }
+      sh.issued[lane] = issued;
     }
   } else if (r0 < r1) {
     uint32_t got = 0;  // stage in use: the slot, and its phase in bit 8
@@ -529,10 +533,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
       }
 
+      bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         const uint32_t slot = got & 255u;
-        mbar_wait(smem_u32(&sh.full[warp * 4 + slot]), got >> 8, &sh.abort, p.status, kDevTimeoutMma);
+        ok = __all_sync(~0u, mbar_wait(smem_u32(&sh.full[warp * 4 + slot]), got >> 8, &sh.abort, p.status, kDevTimeoutMma));
+        if (!ok) break;
         const uint32_t have = sh.mask[warp * 4 + slot];
         {
           const uint32_t st = ring + slot * C::kUnitBytes;
@@ -682,9 +688,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
         }
         __syncwarp();  // all lanes have read the stage
-        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[warp * 4 + slot]));
+        if (lane == 0 && p.fault != 1) mbar_arrive(smem_u32(&sh.empty[warp * 4 + slot]));
         got = slot + 1 == C::kStages ? (got & 256u) ^ 256u : got + 1;
       }
+      if (!ok) break;  // given up: nothing of this piece is kept
 
       // ---- the segment's sums; a whole item is written, a part kept for the join
 #pragma unroll
@@ -756,6 +763,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     }
   }
   __syncthreads();
+  if (sh.abort) {
+    // Some wait of this CTA ran out: its results are void, no ticket is taken.  What it copies still
+    // lands in its own rings before it ends.
+    if (lane == 0 && !copies) {
+      const uint32_t issued = sh.issued[warp];
+      uint32_t never = 0;
+      for (uint32_t i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+        mbar_wait(smem_u32(&sh.full[warp * 4 + i % C::kStages]), i / C::kStages & 1u, &never, p.status, kDevTimeoutDrain);
+    }
+    return;
+  }
 
   // ---- join: the parts in the order of their units are head 0, tail 0, head 1, tail 1, ...; a
   // tail and what follows it, up to the next head, are one item: a run.
@@ -1034,6 +1052,7 @@ cudaError_t launch_variant(const Kv4AttnParams& p, int sms, cudaStream_t s) {
   const int rows = static_cast<int>(p.Lq) * p.group;
   Kv4AttnParams q = p;
   q.one_copy = p.page_size % C::kUnit == 0;
+  q.fault = g_fault_injection;
   return launch_pdl(kern, dim3(static_cast<unsigned>(sms < kMaxCtas ? sms : kMaxCtas)), dim3(C::kThreads), C::kSmem,
                     s, q, (rows + C::kRows - 1) / C::kRows);
 }

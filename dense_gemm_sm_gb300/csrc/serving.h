@@ -58,6 +58,7 @@ struct Kv4AttnParams {
   int32_t page_size, heads;         // heads: of the cache
   uint32_t page_magic;              // n / (page_size / 16) = n * magic >> 32 for n < 2^24; 0: one record a page
   int32_t one_copy;                 // set at launch: pages hold whole units
+  int32_t fault;                    // set at launch: 1: stages are not released (test hook)
   int64_t batch, Lq;
   int32_t group;                    // query heads per cache head
   float c_log2;                     // scale * log2(e)
