@@ -126,7 +126,8 @@ struct Pipe {
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem_base, abort, is_last, seg_ok;
-  int32_t job;  // down: the column tile to join, -1 for none left
+  uint32_t issued;  // stages that the producer filled, written when it ends
+  int32_t job;  // the tile to join, -1 for none left
   __device__ void init() {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -140,12 +141,13 @@ struct Pipe {
     abort = 0;
     is_last = 0;
     seg_ok = 0;
+    issued = 0;
     fence_barrier_init();
   }
-  // After a producer gave up: its copies in flight end before the CTA does.
-  __device__ void drain_loads(uint32_t it, uint32_t* status) {
+  // After any role gave up: the copies in flight end before the CTA does.
+  __device__ void drain_loads(uint32_t* status) {
     uint32_t never = 0;
-    for (uint32_t j = it > STAGES ? it - STAGES : 0u; j < it; ++j)
+    for (uint32_t j = issued > STAGES ? issued - STAGES : 0u; j < issued; ++j)
       mbar_wait(smem_u32(&full[j % STAGES]), (j / STAGES) & 1u, &never, status, kDevTimeoutDrain);
   }
 };
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
           ++it;
         }
       }
-      if (!ok) pipe.drain_loads(it, p.status);
+      pipe.issued = it;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
             umma_bf16(d, sdesc_sw128(w0 + k * 2048, W_BYTES / 2, 1024), bdesc, idesc, add);
             umma_bf16(d + NTOK, sdesc_sw128(w0 + W_BYTES + k * 2048, W_BYTES / 2, 1024), bdesc, idesc, add);
           }
-          umma_commit(smem_u32(&pipe.empty[s]));
+          if (p.fault != 1) umma_commit(smem_u32(&pipe.empty[s]));
         }
         if (ok) umma_commit(smem_u32(&pipe.tfull[acc]));
       }
@@ -584,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && pipe.abort) pipe.drain_loads(p.status);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::kTmem);
@@ -697,18 +700,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
       Place z = first;
       for (uint32_t i = 0; i < ahead; ++i, step(z)) load_z(i, z);
       uint32_t it = ahead;
-      bool ok = true;
       for (uint32_t u = u0 + ahead; u < u1; ++u, ++it, step(w)) {
         const uint32_t s = it % STAGES;
-        if (!mbar_wait(smem_u32(&pipe.empty[s]), ((it / STAGES) & 1u) ^ 1u, abort, p.status, kDevTimeoutProducer)) {
-          ok = false;
-          break;
-        }
+        if (!mbar_wait(smem_u32(&pipe.empty[s]), ((it / STAGES) & 1u) ^ 1u, abort, p.status, kDevTimeoutProducer)) break;
         load_w(s, w);
         load_z(s, w);
       }
       pdl_trigger();
-      if (!ok) pipe.drain_loads(it, p.status);
+      pipe.issued = it;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -735,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
           for (int k = 0; k < BK / 16; ++k)
             umma_bf16(tmem_base + acc * 2 * NTOK, sdesc_sw128(w0 + k * 2048, W_BYTES / 2, 1024),
                       sdesc_sw128(z0 + k * 32, 16, 1024), idesc, (u > first || k > 0) ? 1u : 0u);
-          umma_commit(smem_u32(&pipe.empty[s]));
+          if (p.fault != 1) umma_commit(smem_u32(&pipe.empty[s]));
         }
         if (ok) umma_commit(smem_u32(&pipe.tfull[acc]));
       }
@@ -874,6 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && pipe.abort) pipe.drain_loads(p.status);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::kTmem);
@@ -921,6 +921,7 @@ uint32_t group_of(int64_t cols, int sms, bool lines) {
 
 cudaError_t launch_moe(const MoeParams& call, int sms, cudaStream_t s) {
   MoeParams p = call;
+  p.fault = g_fault_injection;
   auto aligned = [&](const uint16_t* w, int64_t ld, int64_t stride, int64_t bytes) {
     return reinterpret_cast<uintptr_t>(w) % bytes == 0 && ld * 2 % bytes == 0 && (p.E == 1 || stride * 2 % bytes == 0);
   };

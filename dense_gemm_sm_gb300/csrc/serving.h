@@ -86,7 +86,9 @@ struct MoeParams {
   uint16_t* Y; int64_t ldy;
   void* ws;
   uint32_t* status;
-  uint32_t up_group, down_group;  // set by launch_moe: CTAs on neighbouring column tiles
+  // Set by launch_moe: CTAs on neighbouring column tiles; 1: stages are not released (test hook).
+  uint32_t up_group, down_group;
+  int32_t fault;
 };
 int64_t moe_ws_bytes(int64_t T, int64_t I, int64_t top);
 cudaError_t launch_moe(const MoeParams& p, int sms, cudaStream_t s);

@@ -489,8 +489,8 @@ double dg_model_quant_traffic_bytes(int64_t M, int64_t K, int64_t N, int64_t til
 /* Library version string. */
 const char* dg_version(void);
 
-/* Test hook: 0 = off.  1 = the tcgen05 tile kernel's MMA issuer and attention_kv4's
- * computing warps skip their stage releases, so the bounded waits expire and DG_ERR_TIMEOUT is reported (no hang,
+/* Test hook: 0 = off.  1 = the MMA issuers of the tcgen05 tile kernel and of moe_bf16 and
+ * attention_kv4's computing warps skip their stage releases, so the bounded waits expire and DG_ERR_TIMEOUT is reported (no hang,
  * no fault).  Affects launches made after the call. */
 void dg_set_fault_injection(int32_t mode);
 

@@ -64,3 +64,21 @@ def test_attention_that_gives_up(torch, d, hq):
         dg.attention_kv4(cache, batch, 1, hq, 0.02, q, hq * d, hq * d, table, table.shape[1], lens, out, hq * d, hq * d, ws,
                          ws.numel())
     expire(torch, call, out, ws)
+
+
+# More units (64 rows of a 128-column tile) for each CTA than its rings have stages, in both kernels.
+@pytest.mark.parametrize("T", [1, 20, 64])
+def test_experts_that_give_up(torch, T):
+    K, I, E, top = 2048, 4096, 4, 2
+    g = torch.Generator(device="cuda").manual_seed(T)
+
+    def normal(*shape, std=1.0):
+        return torch.randn(shape, generator=g, device="cuda", dtype=torch.bfloat16).mul_(std)
+    x, logits = normal(T, K), torch.randn((T, E), generator=g, device="cuda")
+    wg, wu, wd = normal(E, K, I, std=K ** -0.5), normal(E, K, I, std=K ** -0.5), normal(E, I, K, std=I ** -0.5)
+    out = torch.empty((T, K), dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(dg.dg_moe_workspace_bytes(T, K, I, E, top), dtype=torch.uint8, device="cuda")
+
+    def call():
+        dg.moe_bf16(T, K, I, E, top, True, x, K, logits, E, wg, I, K * I, wu, I, K * I, wd, K, I * K, out, K, ws, ws.numel())
+    expire(torch, call, out, ws)
