@@ -197,20 +197,21 @@ struct Cut {
 struct Sum {
   float m = -INFINITY, l = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  // Adds N parts against their common maximum: their weights do not wait for one another.
+  // Adds N parts against their common maximum: their weights do not wait for one another.  Parts
+  // without a maximum saw no key, or scores that are all NaN: those sums are NaN and stay it.
   template <int N>
   __device__ __forceinline__ void add(const float (&mk)[N], const float (&lk)[N], const float4 (&x)[N]) {
     float top = m;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, mk[i]);
-    if (!(top > -INFINITY)) return;  // nothing seen yet
-    const float a = ex2(m - top);
+    const float ref = top > -INFINITY ? top : 0.f;
+    const float a = ex2(m - ref);
     m = top;
     l *= a;
     v = make_float4(v.x * a, v.y * a, v.z * a, v.w * a);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float b = ex2(mk[i] - top);
+      const float b = ex2(mk[i] - ref);
       l = fmaf(lk[i], b, l);
       v = make_float4(fmaf(x[i].x, b, v.x), fmaf(x[i].y, b, v.y), fmaf(x[i].z, b, v.z), fmaf(x[i].w, b, v.w));
     }

@@ -350,7 +350,7 @@ dg_status kv4_gather(const dg_kv4_cache* cache, int64_t tokens, const int64_t* s
  *     O[b][i][h] = sum_j softmax_j(scale * Q[b][i][h] . K_j) V_j,   j <= lens[b] - Lq + i,
  * K and V of head h / (heads_q / cache->heads).  The tokens are in the cache already: query i
  * of sequence b sits at position lens[b] - Lq + i.  A query that sees no key (lens[b] - Lq + i
- * < 0) gets 0.  FP32 scores, weights and sums; the weights times V's scale are rounded to BF16
+ * < 0) gets 0; one that sees keys and holds NaN or Inf gets NaN.  FP32 scores, weights and sums; the weights times V's scale are rounded to BF16
  * for the second product; O rounded once to BF16.
  *   - Q: element (b, i, h, c) at Q[b * strideQ + i * ldq + h * d + c], likewise O.
  *   - page_table: int32 [batch][ldt] on the device, entry (b, t) the page of tokens

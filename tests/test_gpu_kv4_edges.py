@@ -1,0 +1,67 @@
+"""attention_kv4 and the cache where a call takes another way than small ordinary ones do."""
+import pytest
+
+import dense_gemm_sm_gb300 as dg
+
+from .helpers import torch_mod
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    t = torch_mod()
+    if not t.cuda.is_available():
+        pytest.skip("no CUDA device")
+    dg.load()
+    return t
+
+
+def random_cache(torch, lens, page, heads, d, seed):
+    """A cache of random codes and parameters, and the sequences' pages in random order."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 1
+    data = torch.randint(0, 256, (pages, heads, dg.dg_kv4_block_bytes(page, d)), generator=g, device="cuda", dtype=torch.uint8)
+    params = data.view(pages, heads, page // 16, -1)[..., 16 * d:].view(torch.bfloat16)
+    params.copy_(torch.randn(params.shape, generator=g, device="cuda"))
+    table = torch.full((len(lens), max(need + [1])), -1, dtype=torch.int32, device="cuda")
+    order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    return data, table, g
+
+
+def attend(torch, data, table, lens, q, heads, page, scale):
+    batch, lq, hq, d = q.shape
+    cache = dg.dg_kv4_cache(data, data.shape[0], page, heads, d)
+    ws = torch.zeros(dg.dg_attention_kv4_workspace_bytes(batch, lq, hq, heads, d), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, -3.0)
+    dg.attention_kv4(cache, batch, lq, hq, scale, q, hq * d, lq * hq * d, table, table.shape[1],
+                     torch.tensor(lens, dtype=torch.int32, device="cuda"), out, hq * d, lq * hq * d, ws, ws.numel())
+    torch.cuda.synchronize()
+    assert dg.dg_device_status() == dg.DG_OK
+    return out
+
+
+# Items that are whole in a warp, cut between warps, cut between CTAs, joined in two steps.
+@pytest.mark.parametrize("lens,lq,hq,heads,d", [
+    ([20, 33, 5], 1, 8, 2, 128), ([300, 700], 1, 16, 2, 64), ([3000], 1, 8, 1, 128), ([8192], 1, 32, 8, 128), ([20000], 1, 16, 1, 64),
+    ([6000, 40], 3, 8, 1, 128), ([1500, 9, 0, 2500], 5, 12, 2, 64)])
+def test_a_query_that_is_not_finite_gives_nan_and_only_there(torch, lens, lq, hq, heads, d):
+    data, table, g = random_cache(torch, lens, 64, heads, d, sum(lens))
+    q = torch.randn((len(lens), lq, hq, d), generator=g, device="cuda").to(torch.bfloat16)
+    plain = attend(torch, data, table, lens, q, heads, 64, 0.1)
+    assert bool(plain.isfinite().all())
+    bad = q.clone()
+    where = torch.zeros((len(lens), lq, hq), dtype=torch.bool, device="cuda")
+    for b in range(len(lens)):
+        for i in range(lq):
+            for h, value in ((b % hq, float("nan")), ((b + 3 * i + 5) % hq, float("inf"))):
+                bad[b, i, h, (7 * i + h) % d] = value
+                where[b, i, h] = lens[b] - lq + i >= 0            # a row without a key stays 0
+    out = attend(torch, data, table, lens, bad, heads, 64, 0.1)
+    assert bool(out[where].isnan().all())
+    assert torch.equal(out[~where], plain[~where])
