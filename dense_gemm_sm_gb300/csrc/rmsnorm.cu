@@ -141,6 +141,15 @@ __device__ __forceinline__ void row_reduce(float& sum, float& top, int lanes, bo
   }
 }
 
+// What makes codes of h * gain, and the row's scale, from top = max |h * gain|: f becomes the first
+// factor, inv the second.  A row of zeros has f = 1 / 0 when eps is 0: its codes and scale are 0.
+__device__ __forceinline__ float code_factors(float top, float& f, float& inv) {
+  if (top == 0.f && f > 0.f) f = 0.f;
+  const float amax = top * f;
+  inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 0.f;
+  return __fdiv_rn(amax, 448.f);
+}
+
 // One row per CTA of tpr threads, per warp (8 rows a CTA) or, PART, per tpr = 8 or 16 lanes, C
 // chunks of 8 elements a thread (200000 rows of 128: 19 us, 48 in warps half of which idle; 64 wide
 // with a residual and codes 16 and 74).
@@ -234,9 +243,8 @@ __global__ void __launch_bounds__(1024, M == kShifted && C == 1 ? 2 : 0) rmsnorm
   float f = 1.f / sqrtf(sum / static_cast<float>(static_cast<int>(p.cols)) + p.eps);
   float inv = 1.f;
   if (kCodes) {
-    const float amax = top * f;
-    inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 0.f;
-    if (t == 0 && (!PART || live)) p.scales[r] = __fdiv_rn(amax, 448.f);
+    const float scale = code_factors(top, f, inv);
+    if (t == 0 && (!PART || live)) p.scales[r] = scale;
   }
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -275,12 +283,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(const NormParams p) 
     if (kCodes) top = fmaxf(top, fabsf(h * load1(p.gain + c)));
   }
   row_reduce(sum, top, 32, true, scratch);
-  const float f = 1.f / sqrtf(sum / static_cast<float>(p.cols) + p.eps);
+  float f = 1.f / sqrtf(sum / static_cast<float>(p.cols) + p.eps);
   float inv = 1.f;
   if (kCodes) {
-    const float amax = top * f;
-    inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 0.f;
-    if (threadIdx.x == 0) p.scales[r] = __fdiv_rn(amax, 448.f);
+    const float scale = code_factors(top, f, inv);
+    if (threadIdx.x == 0) p.scales[r] = scale;
   }
 #pragma unroll 4
   for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {

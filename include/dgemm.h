@@ -280,7 +280,8 @@ dg_status attention_bf16(int64_t batch, int64_t Lq, int64_t Lkv, int64_t d, floa
  *                             Q[i] = E4M3(y * (448 / amax))
  * with h, the mean and y in FP32 and one rounding per output (the norm is of the unrounded
  * h).  Q and scales are what gemm_fp8_e4m3 reads, as quantize_rows_e4m3 writes them; a row
- * of zeros gets codes 0 and scale 0, a row holding Inf or NaN unspecified codes.
+ * of zeros gets codes 0 and scale 0 (Y: zeros, or with eps = 0 NaN, which 0 / 0 is), a row
+ * holding Inf or NaN unspecified codes.
  *   - X: rows x cols of x_type (DG_OUT_BF16 or DG_OUT_F32), row stride ldx.  R and H: rows x
  *     cols of r_type, strides ldr and ldh; H may be R (in place).  R and H both null: no
  *     residual, h = X.  gain: cols BF16.  Y: BF16, ldy.  Q: bytes, ldq.
