@@ -58,3 +58,30 @@ def test_rows_of_zeros_without_eps(torch, cols, ld, residual):
     rest = [i for i in range(6) if i not in zero]
     assert not codes[zero].any() and not s[zero].any()
     assert np.all(np.abs(codes[rest]).max(1) == 448) and np.all(s[rest] > 0)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("cols,ld", FORMS)
+def test_rows_whose_reciprocal_passes_fp32(torch, cols, ld, residual):
+    # Largest outputs from 2^-116 down to 2^-140, zeros among the elements: by small rows, by a small
+    # gain, by both, and by a small gain on a row so large that its norm is small.
+    rng = np.random.default_rng(cols + 1)
+    for x_exp, gain_exp, eps in ((-126, 0, 1.0), (-120, -10, 1.0), (0, -124, 1e-5), (50, -121, 1e-5), (-130, 0, 1e-5), (0, -122, 1e-9)):
+        x = ref.bf16(rng.uniform(0.25, 1, (4, cols)) * rng.choice([-1, 1], (4, cols)) * 2.0 ** x_exp)
+        gain = ref.bf16(rng.uniform(0.5, 1, cols) * 2.0 ** gain_exp)
+        x[:, 1::3] = 0
+        x[2] = 0
+        r = (rng.uniform(-0.25, 0.25, (4, cols)) * 2.0 ** x_exp).astype(np.float32) if residual else None
+        if residual:
+            r[:, 1::3] = 0
+            r[2] = 0
+        codes, s = to_codes(torch, x, r, gain, eps, ld)
+        _, y = ref.rmsnorm(x, r, gain, eps)
+        want, scales = ref.rmsnorm_codes(y)
+        # FP32 subnormals: h, h * gain and the largest output are off by up to 2^-150 each.
+        top = np.abs((x if r is None else x.astype(np.float64) + r) * gain.astype(np.float64)).max(1, keepdims=True)
+        tiny = 2.0 ** -149 / np.where(top > 0, top, 1) * 2
+        rel = (cols / 32 + 40) * 2.0 ** -25 + 8 * ref.F32
+        assert np.all(np.abs(codes - want) <= np.abs(want) * (ref.E4M3 + 4 * rel + tiny) + 448 * tiny + 2.0 ** -10)
+        assert np.all(np.abs(s - scales) <= scales * (4 * rel + tiny[:, 0]) + 2.0 ** -148)
+        assert not codes[2].any() and s[2] == 0 and not codes[:, 1::3].any()
