@@ -402,7 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
   const int64_t rest = p.T * p.top * ldz;  // from z rounded to its remainder
   auto put_z = [&](int row, int64_t n, float g, float up) {
     const float z = g / (1.f + expf(-g)) * up;
-    const __nv_bfloat16 hi = __float2bfloat16_rn(z), lo = __float2bfloat16_rn(z - __bfloat162float(hi));
+    const __nv_bfloat16 hi = __float2bfloat16_rn(z);
+    const float left = z - __bfloat162float(hi);
+    // What passes BF16's range is Inf, and has no remainder (Inf - Inf would make a NaN of its sums).
+    const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(left) < INFINITY ? left : 0.f);
     Z[row * ldz + n] = __bfloat16_as_ushort(hi);
     Z[rest + row * ldz + n] = __bfloat16_as_ushort(lo);
   };
