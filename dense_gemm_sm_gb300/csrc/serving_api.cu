@@ -55,12 +55,32 @@ dg_status run_norm(int64_t rows, int64_t cols, const void* X, int64_t ldx, dg_ou
                                   static_cast<cudaStream_t>(stream)));
 }
 
+// Sizes are held against their limits before anything is multiplied with them.
+constexpr int32_t kMaxPage = 4096, kMaxCacheHeads = 4096;
+constexpr int64_t kMaxAttn = 65536;  // sequences, queries of one, query heads
+
+bool attention_takes(int64_t batch, int64_t Lq, int64_t heads_q) {
+  return batch <= kMaxAttn && Lq <= kMaxAttn && heads_q <= kMaxAttn && batch * Lq * heads_q <= INT32_MAX;
+}
+
+// n > 0 rows of `width` elements, ld apart, within `span` elements (no product can overflow).
+bool rows_fit(int64_t n, int64_t ld, int64_t width, int64_t span) {
+  return span >= width && (n == 1 || ld <= (span - width) / (n - 1));
+}
+
+bool moe_takes(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top) {
+  if (T > 64 || top > 16 || E > 512 || K > INT32_MAX || I > INT32_MAX) return false;
+  // Units of 64 x 128 weights of all experts are counted in 31 bits.
+  const int64_t kb = (K + 63) / 64, ib = (I + 63) / 64;
+  return kb <= INT32_MAX / ib / E;
+}
+
 // The cache itself: DG_OK when its pages can be addressed.
 dg_status check_cache(const dg_kv4_cache* c) {
   if (!c || c->pages < 0 || c->page_size <= 0 || c->heads <= 0 || c->d <= 0) return DG_ERR_INVALID_ARG;
   if (c->page_size % kKv4Tokens != 0) return DG_ERR_INVALID_ARG;
   if (c->d != 64 && c->d != 128) return DG_ERR_UNSUPPORTED;
-  if (c->page_size > 4096 || c->heads > 4096 || c->pages > INT32_MAX) return DG_ERR_UNSUPPORTED;
+  if (c->page_size > kMaxPage || c->heads > kMaxCacheHeads || c->pages > INT32_MAX) return DG_ERR_UNSUPPORTED;
   if (c->pages > 0 && !c->data) return DG_ERR_INVALID_ARG;
   if (!aligned(c->data, 16)) return DG_ERR_MISALIGNED;
   return DG_OK;
@@ -118,7 +138,7 @@ dg_status rmsnorm_residual_e4m3(int64_t rows, int64_t cols, const void* X, int64
 }
 
 int64_t dg_kv4_block_bytes(int32_t page_size, int32_t d) {
-  if (page_size <= 0 || page_size % kKv4Tokens != 0 || (d != 64 && d != 128)) return 0;
+  if (page_size <= 0 || page_size > kMaxPage || page_size % kKv4Tokens != 0 || (d != 64 && d != 128)) return 0;
   return static_cast<int64_t>(page_size / kKv4Tokens) * kv4_record_bytes(d);
 }
 
@@ -135,6 +155,7 @@ dg_status kv4_gather(const dg_kv4_cache* cache, int64_t tokens, const int64_t* s
 int64_t dg_attention_kv4_workspace_bytes(int64_t batch, int64_t Lq, int64_t heads_q, int64_t heads_kv, int32_t d) {
   if (batch <= 0 || Lq <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv != 0 || (d != 64 && d != 128))
     return 0;
+  if (heads_kv > kMaxCacheHeads || !attention_takes(batch, Lq, heads_q)) return 0;
   return kv4_attention_ws_bytes(Lq, heads_q, heads_kv, d);
 }
 
@@ -148,20 +169,18 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
   if (!(scale > 0.f) || !std::isfinite(scale)) return DG_ERR_INVALID_ARG;
   if (batch == 0 || Lq == 0 || heads_q == 0) return DG_OK;
   if (heads_q % cache->heads != 0) return DG_ERR_INVALID_ARG;
+  if (!attention_takes(batch, Lq, heads_q) || ldt > (int64_t(1) << 28) / cache->page_size) return DG_ERR_UNSUPPORTED;
+  // The kernel counts units of 32 keys of all (sequence, head, 8 query rows) in 31 bits.
+  if (batch * cache->heads * ((Lq * (heads_q / cache->heads) + 7) / 8) > INT32_MAX / (ldt * cache->page_size / 32 + 1))
+    return DG_ERR_UNSUPPORTED;
   const int d = cache->d;
   const int64_t width = heads_q * d;
   if (!Q || !O || !lens || (ldt > 0 && !page_table)) return DG_ERR_INVALID_ARG;
   if ((Lq > 1 && (ldq < width || ldo < width)) ||
-      (batch > 1 && (strideQ < (Lq - 1) * ldq + width || strideO < (Lq - 1) * ldo + width)))
+      (batch > 1 && (!rows_fit(Lq, ldq, width, strideQ) || !rows_fit(Lq, ldo, width, strideO))))
     return DG_ERR_INVALID_ARG;
   const int64_t need = kv4_attention_ws_bytes(Lq, heads_q, cache->heads, d);
   if (!workspace || workspace_bytes < need) return DG_ERR_INVALID_ARG;
-  if (heads_q > 65536 || Lq > 65536 || batch > 65536 || batch * Lq * heads_q > INT32_MAX ||
-      ldt > (int64_t(1) << 28) / cache->page_size)
-    return DG_ERR_UNSUPPORTED;
-  // The kernel counts units of 32 keys of all (sequence, head, 8 query rows) in 31 bits.
-  if (batch * cache->heads * ((Lq * (heads_q / cache->heads) + 7) / 8) > INT32_MAX / (ldt * cache->page_size / 32 + 1))
-    return DG_ERR_UNSUPPORTED;
   if (!aligned(Q, 16) || !aligned(O, 16) || ldq % 8 || ldo % 8 || strideQ % 8 || strideO % 8 ||
       !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(workspace, 256))
     return DG_ERR_MISALIGNED;
@@ -187,7 +206,7 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
 }
 
 int64_t dg_moe_workspace_bytes(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top) {
-  if (T <= 0 || K <= 0 || I <= 0 || E <= 0 || top <= 0 || top > E || T > 64 || top > 16) return 0;
+  if (T <= 0 || K <= 0 || I <= 0 || E <= 0 || top <= 0 || top > E || !moe_takes(T, K, I, E, top)) return 0;
   return moe_ws_bytes(T, I, top);
 }
 
@@ -199,14 +218,10 @@ dg_status moe_bf16(int64_t T, int64_t K, int64_t I, int64_t E, int64_t top, int3
   if (T < 0 || K < 0 || I < 0 || E <= 0 || top <= 0 || top > E) return DG_ERR_INVALID_ARG;
   if (T == 0 || K == 0) return DG_OK;
   if (I == 0) return DG_ERR_INVALID_ARG;
+  if (!moe_takes(T, K, I, E, top)) return DG_ERR_UNSUPPORTED;
   if (!X || !logits || !Wg || !Wu || !Wd || !Y) return DG_ERR_INVALID_ARG;
   if (ldx < K || ldl < E || ldwg < I || ldwu < I || ldwd < K || ldy < K) return DG_ERR_INVALID_ARG;
-  if (E > 1 && (strideWg < K * ldwg || strideWu < K * ldwu || strideWd < I * ldwd)) return DG_ERR_INVALID_ARG;
-  if (T > 64 || top > 16 || E > 512 || K > INT32_MAX || I > INT32_MAX) return DG_ERR_UNSUPPORTED;
-  {  // units of 64 x 128 weights of all experts, counted in 31 bits
-    const int64_t kb = (K + 63) / 64, ib = (I + 63) / 64;
-    if (kb > INT32_MAX / ib / E) return DG_ERR_UNSUPPORTED;
-  }
+  if (E > 1 && (strideWg / K < ldwg || strideWu / K < ldwu || strideWd / I < ldwd)) return DG_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < moe_ws_bytes(T, I, top)) return DG_ERR_INVALID_ARG;
   if (!aligned(X, 16) || !aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(Wd, 16) || ldx % 8 || ldwg % 8 ||
       ldwu % 8 || ldwd % 8 || strideWg % 8 || strideWu % 8 || strideWd % 8 || !aligned(logits, 4) ||
