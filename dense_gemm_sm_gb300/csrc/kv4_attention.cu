@@ -48,7 +48,11 @@ constexpr int kMinUnits = 4;
 // Items of up to this many units are one CTA's, which mostly saves the join of two (8 cache heads
 // of 128, 8 queries each; us with 0, 16, 32, 64 here: 16 x 512 keys 12.2, 9.1, 9.1, 9.1;
 // 100 x 1024 32.5, 32.6, 30.4, 30.3; 8 x 1024 of four queries 31.8, 31.8, 20.3, 20.3;
-// 1 x 1024 8.9, 8.9, 10.2, 10.2; 1 x 2048 9.8, 9.8, 9.8, 13.4).
+// 1 x 1024 8.9, 8.9, 10.2, 10.2; 1 x 2048 9.8, 9.8, 9.8, 13.4).  With a few more items than one or
+// two a CTA the longest share is then up to twice the even one; even there the joins saved are
+// worth it, but for 9 query rows and more, where it costs up to 5 % (items of 32 units, us with 0 and
+// 32 here, at 152, 160, 200 and 320 items: 4 rows 10.2, 10.2; 14.2, 13.2; 14.9, 13.3; 18.0, 17.5; 16 rows
+// 12.8, 12.8; 18.6, 19.0; 21.4, 19.2; 25.6, 26.3; 32 rows 20.5, 20.5; 31.6, 32.7; 37.0, 33.0; 44.5, 46.4).
 constexpr int kWhole = 32;
 // The reference that weights are taken against (2^(score - reference)) follows the running
 // maximum only when that has outgrown it by this much: weights stay below 2^8, which FP32 sums
