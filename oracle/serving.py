@@ -147,6 +147,29 @@ def kv4_attention(pool, q, table, lens, scale):
     return out, bound
 
 
+# Rows that make every unit of keys visible in the output: with queries of zeros all weights are equal,
+# and each column of the output is the share of the keys whose unit was dealt to it.
+def unit_rows(n, d, turn, unit=32):
+    """[n, d] float32: row j is 1 in the column of its unit of keys, 0 elsewhere; `turn` deals anew."""
+    u = np.arange(n) // unit
+    out = np.zeros((n, d), np.float32)
+    out[np.arange(n), (u + turn * (1 + u // d)) % d] = 1
+    return out
+
+
+def unit_mean(rows, see, units=0, ctas=152, warps=7):
+    """(O, bound) of a query of zeros over the first `see` of unit_rows, in a call of `units` units
+    (0: this sequence's own).
+
+    The value 1 has scale s = bf16(1 / 15) and code 15.  A warp adds, two MMAs a unit, codes offset by
+    128 (at most 143 s a key), takes 136 s a key away and adds 8 s; its share is the even one, or of
+    a CTA that has up to 64 units; then at most 40 parts follow one another.  Weights are 1 and s is BF16, so that P itself is not rounded."""
+    s = float(bf16(np.float32(1) / np.float32(15))[0])
+    o = rows[:see].astype(np.float64).sum(0) / max(see, 1) * 15 * s
+    steps = 2 * (max(-(-64 // warps), -(-max(units, len(rows) // 32 + 1) // (ctas * warps)) + 1)) + 40
+    return o, BF16 * o + steps * 2.0 ** -22 * (143 + 136 + 8) * s
+
+
 # ------------------------------------------------------------------ mixture of experts
 def moe_route(logits, top, renorm):
     """[(expert, weight), ...] per token; experts at -inf (or NaN) are left out."""

@@ -1,7 +1,9 @@
 """attention_kv4 and the cache where a call takes another way than small ordinary ones do."""
+import numpy as np
 import pytest
 
 import dense_gemm_sm_gb300 as dg
+from oracle import serving as ref
 
 from .helpers import torch_mod
 
@@ -65,3 +67,53 @@ def test_a_query_that_is_not_finite_gives_nan_and_only_there(torch, lens, lq, hq
     out = attend(torch, data, table, lens, bad, heads, 64, 0.1)
     assert bool(out[where].isnan().all())
     assert torch.equal(out[~where], plain[~where])
+
+
+# Every unit of keys is visible in these outputs (tests/test_kv4_units.py): a part that a join loses,
+# doubles or takes from an earlier call changes them.  Items of one warp, of one CTA, of neighbouring
+# CTAs, and those joined in two steps; one workspace for calls whose units are dealt differently.
+@pytest.mark.parametrize("lens,lq,hq,heads,d", [
+    ([6000], 1, 16, 1, 128), ([9000, 0, 4000], 2, 16, 1, 64), ([20000], 1, 8, 1, 64), ([20000], 1, 8, 1, 128), ([33000], 1, 32, 1, 128),
+    ([3000, 2600, 2700], 1, 32, 1, 128), ([40, 4100, 4200, 70], 1, 16, 1, 128), ([16768, 16768], 4, 8, 1, 64), ([8192], 1, 32, 8, 128),
+    ([0, 5000, 1, 17], 1, 8, 2, 128), ([1024] * 20, 1, 32, 8, 128), ([1024] * 5, 1, 128, 8, 64), ([700, 33, 1500, 64, 3100] * 3, 1, 16, 4, 64),
+    ([2000] * 40, 1, 8, 8, 128), ([512] * 16, 3, 32, 4, 64)])
+def test_every_unit_of_keys_counts_once(torch, lens, lq, hq, heads, d):
+    batch, page = len(lens), 48
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 1
+    g = torch.Generator(device="cuda").manual_seed(sum(lens) + hq)
+    data = torch.full((pages, heads, dg.dg_kv4_block_bytes(page, d)), 255, dtype=torch.uint8, device="cuda")
+    cache = dg.dg_kv4_cache(data, pages, page, heads, d)
+    order = torch.randperm(pages, generator=g, device="cuda")
+    table = torch.full((batch, max(need)), -1, dtype=torch.int32, device="cuda")
+    q = torch.zeros((batch, lq, hq * d), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.zeros(dg.dg_attention_kv4_workspace_bytes(batch, lq, hq, heads, d), dtype=torch.uint8, device="cuda")
+    L = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    units = sum(-(-n // 32) for n in lens) * heads * -(-(lq * hq // heads) // 8)
+    for call in range(3):
+        want, bound = np.zeros((batch, lq, hq, d)), np.zeros((batch, lq, hq, d))
+        at = 0
+        for b, n in enumerate(lens):
+            mine = order[at:at + need[b]]
+            at += need[b]
+            table[b, :need[b]] = mine.to(torch.int32)
+            if n == 0:
+                continue
+            rows = [ref.unit_rows(n, d, 1 + (3 * b + h + 5 * call) % 11) for h in range(heads)]
+            v = torch.from_numpy(np.stack(rows, 1)).cuda().to(torch.bfloat16)
+            k = torch.randn((n, heads, d), generator=g, device="cuda").to(torch.bfloat16)
+            token = torch.arange(n, device="cuda")
+            dg.kv4_append(cache, n, k, heads * d, v, heads * d, mine[token // page] * page + token % page)
+            for h in range(heads):
+                for i in range(lq):
+                    heads_of = slice(h * (hq // heads), (h + 1) * (hq // heads))
+                    want[b, i, heads_of], bound[b, i, heads_of] = ref.unit_mean(rows[h], max(n - lq + i + 1, 0), units)
+        out.fill_(-3.0)
+        dg.attention_kv4(cache, batch, lq, hq, 0.5, q, hq * d, lq * hq * d, table, table.shape[1], L, out, hq * d, lq * hq * d, ws,
+                         ws.numel())
+        torch.cuda.synchronize()
+        assert dg.dg_device_status() == dg.DG_OK
+        got = out.float().cpu().numpy().astype(np.float64).reshape(want.shape)
+        off = np.abs(got - want) > bound
+        assert not off.any(), f"call {call}: {off.sum()} of {off.size}, first {np.argwhere(off)[0]}"
