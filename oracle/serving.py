@@ -109,6 +109,20 @@ class Kv4Pool:
                     dst[:, 16 * d + 64 * w + 4 * u + b] = (prm[w, at] >> (8 * b)) & 255
         return out.reshape(self.pages, self.heads, -1)
 
+    def pack_all(self):
+        """pack() with whole arrays, for large pools."""
+        d, recs = self.d, self.page_size // 16
+        codes = self.codes.reshape(2, self.pages, recs, 16, self.heads, d)
+        bits = [bf16_bits(x).astype(np.uint32).reshape(2, self.pages, recs, 16, self.heads) for x in (self.scale, self.zero)]
+        out = np.empty((self.pages, self.heads, recs, 16 * (d + 8)), np.uint8)
+        two = codes[..., 0::2] | (codes[..., 1::2] << 4)                                        # [2, pages, recs, 16, heads, d/2]
+        out[..., :8 * d] = two[0].transpose(0, 3, 1, 2, 4).reshape(out.shape[:3] + (8 * d,))
+        v = two[1].reshape(self.pages, recs, 2, 4, 2, self.heads, 8, d // 32, 2)                # half, pair, odd; group, four columns, byte
+        out[..., 8 * d:16 * d] = v.transpose(0, 5, 1, 2, 6, 3, 7, 4, 8).reshape(out.shape[:3] + (8 * d,))
+        words = np.ascontiguousarray((bits[0] | (bits[1] << 16)).transpose(1, 4, 2, 0, 3)).astype("<u4")
+        out[..., 16 * d:] = words.view(np.uint8).reshape(out.shape[:3] + (128,))
+        return out.reshape(self.pages, self.heads, -1)
+
 
 def kv4_attention(pool, q, table, lens, scale):
     """q [batch, Lq, heads_q, d] float64 -> (O, bound) float64, O of a query without keys 0."""

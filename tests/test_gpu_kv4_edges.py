@@ -117,3 +117,47 @@ def test_every_unit_of_keys_counts_once(torch, lens, lq, hq, heads, d):
         got = out.float().cpu().numpy().astype(np.float64).reshape(want.shape)
         off = np.abs(got - want) > bound
         assert not off.any(), f"call {call}: {off.sum()} of {off.size}, first {np.argwhere(off)[0]}"
+
+
+# A prompt's rows: 4 and 8 heads in flight, runs of heads cut over warps, more tokens than the grid
+# has warps; 16-byte, 8-byte and single accesses.
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens,heads,page,pad,offset", [
+    (5000, 8, 64, 0, 0), (3500, 8, 16, 8, 0), (9800, 4, 48, 4, 0), (5003, 12, 32, 1, 0), (5003, 16, 64, 0, 1), (5003, 5, 16, 3, 0),
+    (20011, 8, 128, 0, 4), (3300, 8, 16, 0, 2), (2432, 16, 64, 8, 0)])
+def test_a_prompt_written_and_read_back(torch, tokens, heads, page, pad, offset, d):
+    rng = np.random.default_rng(tokens + d)
+    width, pages = heads * d, -(-tokens // page) + 3
+    ld = width + pad
+    slots = rng.permutation(pages * page)[:tokens]
+    skipped = rng.choice(tokens, 40, replace=False)
+    pool = ref.Kv4Pool(pages, page, heads, d)
+    rows, given = [], slots.copy()
+    given[skipped] = -1 - skipped                             # negative: passed over, read as zeros
+    kept = given >= 0
+    for which in range(2):
+        x = rng.standard_normal((tokens, heads, d)).astype(np.float32) * np.exp(rng.normal(0, 1, (tokens, heads, 1))).astype(np.float32)
+        x[rng.integers(0, tokens, 9), rng.integers(0, heads, 9)] = 1.5
+        x = ref.bf16(x)
+        buf = torch.full((tokens * ld + offset,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        buf[offset:].view(tokens, ld)[:, :width] = torch.from_numpy(x.reshape(tokens, width)).cuda()
+        rows.append(buf[offset:].view(tokens, ld))
+        pool.codes[which, slots[kept]], pool.scale[which, slots[kept]], pool.zero[which, slots[kept]] = \
+            (a[kept] for a in ref.kv4_quantise(x))
+    data = torch.zeros((pages, heads, dg.dg_kv4_block_bytes(page, d)), dtype=torch.uint8, device="cuda")
+    cache = dg.dg_kv4_cache(data, pages, page, heads, d)
+    S = torch.from_numpy(given).cuda()
+    dg.kv4_append(cache, tokens, rows[0], ld, rows[1], ld, S)
+    torch.cuda.synchronize()
+    assert dg.dg_device_status() == dg.DG_OK
+    assert np.array_equal(data.cpu().numpy(), pool.pack_all())
+    bufs = [torch.full((tokens * ld + offset,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    outs = [b[offset:].view(tokens, ld) for b in bufs]
+    dg.kv4_gather(cache, tokens, S, outs[0], ld, outs[1], ld)
+    torch.cuda.synchronize()
+    assert dg.dg_device_status() == dg.DG_OK
+    for which, out in enumerate(outs):
+        want = ref.bf16(pool.rows(which, slots).astype(np.float32)).reshape(tokens, width)
+        want[~kept] = 0
+        assert np.array_equal(out[:, :width].float().cpu().numpy(), want)
+        assert bool((out[:, width:] == 7.0).all()) and bool((bufs[which][:offset] == 7.0).all())

@@ -1,4 +1,5 @@
-"""The rows that make each unit of keys visible: a lost, doubled or stale unit is seen (no GPU)."""
+"""What the tests of the 4-bit cache stand on (no GPU): the rows that make each unit of keys visible,
+so that a lost, doubled or stale unit is seen, and the packing of whole pools."""
 import numpy as np
 import pytest
 
@@ -36,3 +37,12 @@ def test_the_oracle_agrees():
     o, _ = ref.kv4_attention(pool, np.zeros((1, 3, 1, 64)), np.arange(20)[None], [300], 1.0)
     for i in range(3):
         assert np.allclose(o[0, i, 0], ref.unit_mean(rows, 298 + i)[0], rtol=1e-12)
+
+
+@pytest.mark.parametrize("pages,page_size,heads,d", [(3, 16, 1, 64), (2, 48, 3, 128), (1, 64, 2, 64)])
+def test_pools_packed_at_once(pages, page_size, heads, d):
+    rng = np.random.default_rng(pages)
+    pool = ref.Kv4Pool(pages, page_size, heads, d)
+    pool.codes[:] = rng.integers(0, 16, pool.codes.shape)
+    pool.scale[:], pool.zero[:] = (ref.bf16(rng.standard_normal(pool.scale.shape)) for _ in range(2))
+    assert np.array_equal(pool.pack_all(), pool.pack())
