@@ -161,3 +161,33 @@ def test_a_prompt_written_and_read_back(torch, tokens, heads, page, pad, offset,
         want[~kept] = 0
         assert np.array_equal(out[:, :width].float().cpu().numpy(), want)
         assert bool((out[:, width:] == 7.0).all()) and bool((bufs[which][:offset] == 7.0).all())
+
+
+# More sequences than the first four of every lane: their places are searched for.
+@pytest.mark.parametrize("batch,lq,hq,heads,d,lone", [(129, 1, 4, 2, 64, 0), (161, 2, 12, 1, 64, 700), (300, 1, 8, 2, 128, 0), (700, 1, 2, 2, 64, 1500),
+                                                      (1000, 1, 1, 1, 64, 0)])
+def test_batches_of_many_sequences(torch, batch, lq, hq, heads, d, lone):
+    rng = np.random.default_rng(batch)
+    lens = [int(n) for n in rng.integers(0, 90, batch) * (rng.random(batch) < 0.8)]
+    if lone:
+        lens[batch * 2 // 3] = lone                           # one far longer, past every lane's first four
+    lens[-1], page = 40, 16
+    need = [-(-n // page) for n in lens]
+    order = rng.permutation(sum(need) + 2)
+    pool = ref.Kv4Pool(len(order), page, heads, d)
+    table = np.full((batch, max(need)), -9, np.int64)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    slots = np.concatenate([table[b, np.arange(n) // page] * page + np.arange(n) % page for b, n in enumerate(lens)])
+    for which in range(2):
+        x = ref.bf16(rng.standard_normal((len(slots), heads, d)).astype(np.float32))
+        pool.codes[which, slots], pool.scale[which, slots], pool.zero[which, slots] = ref.kv4_quantise(x)
+    q = ref.bf16(rng.standard_normal((batch, lq, hq, d))).astype(np.float64)
+    scale = float(np.float32(1 / np.sqrt(d)))
+    out = attend(torch, torch.from_numpy(pool.pack_all()).cuda(), torch.from_numpy(table.astype(np.int32)).cuda(), lens,
+                 torch.from_numpy(q).cuda().to(torch.bfloat16), heads, page, scale)
+    want, bound = ref.kv4_attention(pool, q, table, lens, scale)
+    off = ~(np.abs(out.float().cpu().numpy() - want) <= bound)
+    assert not off.any(), f"{off.sum()} of {off.size}, first {np.argwhere(off)[0]}"
