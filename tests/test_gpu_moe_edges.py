@@ -51,3 +51,37 @@ def test_an_activation_past_the_range_is_infinite(torch, T, K, least):
     wd[0, 5, ::2], wd[0, 5, 1::2] = 1.0, -2.0
     y = call(torch, x, np.zeros((T, 1)), wg, wu, wd, 1, True)
     assert np.all(y[:, ::2] == np.inf) and np.all(y[:, 1::2] == -np.inf)
+
+
+def check(torch, T, E, top, renorm, logits, K=72, I=40):
+    rng = np.random.default_rng(T + E + top)
+    x = ref.bf16(rng.standard_normal((T, K)))
+    wg, wu = (ref.bf16(rng.standard_normal((E, K, I)) / np.sqrt(K)) for _ in range(2))
+    wd = ref.bf16(rng.standard_normal((E, I, K)) / np.sqrt(I))
+    got = call(torch, x, logits, wg, wu, wd, top, renorm)
+    want, bound = ref.moe(x, logits, wg, wu, wd, top, renorm)
+    off = ~(np.abs(got - want) <= bound)
+    assert not off.any(), f"{off.sum()} of {off.size}, first {np.argwhere(off)[0]}"
+
+
+# More than 16 tokens have a routing launch of their own, whose lanes hold 2, 4 or 16 logits each.
+@pytest.mark.parametrize("E", [40, 64, 65, 100, 128, 129, 300, 512])
+@pytest.mark.parametrize("T,top,renorm", [(17, 1, False), (33, 8, True), (64, 16, False), (48, 11, True)])
+def test_routing_of_many_experts(torch, T, E, top, renorm):
+    rng = np.random.default_rng(E + T)
+    check(torch, T, E, top, renorm, rng.standard_normal((T, E)).astype(np.float32) * 1.5)
+
+
+@pytest.mark.parametrize("T", [5, 16, 21, 64])
+@pytest.mark.parametrize("E,top", [(17, 16), (33, 9), (40, 16), (65, 12), (128, 16), (129, 10), (512, 16)])
+def test_routing_of_ties_and_of_experts_switched_off(torch, T, E, top):
+    # Logits in steps of a half tie at the last place of nearly every row; whole experts and single
+    # logits are off; one row has a single expert left, one none, one equal logits throughout.
+    rng = np.random.default_rng(E * T)
+    logits = np.round(rng.standard_normal((T, E)) * 2).astype(np.float32) / 2
+    logits[:, rng.choice(E, E // 8, replace=False)] = -np.inf
+    logits[rng.random((T, E)) < 0.05] = np.nan
+    logits[0], logits[1], logits[2] = -np.inf, -np.inf, -0.0
+    logits[0, E - 1] = -3.0
+    logits[2, ::2] = 0.0
+    check(torch, T, E, top, T % 2 == 0, logits)
