@@ -364,9 +364,7 @@ cudaError_t launch_res(const NormParams& p, bool r_f32, Mode m, cudaStream_t s) 
 
 }  // namespace
 
-cudaError_t launch_rmsnorm(const NormParams& p, bool x_f32, bool r_f32, bool vec, int sms,
-                           cudaStream_t s) {
-  (void)sms;
+cudaError_t launch_rmsnorm(const NormParams& p, bool x_f32, bool r_f32, bool vec, cudaStream_t s) {
   // Where rows of H and of Y are equally far from an aligned address.
   const uint64_t y = reinterpret_cast<uintptr_t>(p.Y) / (p.scales ? 1 : 2), h = reinterpret_cast<uintptr_t>(p.H) / (r_f32 ? 4 : 2);
   const uint64_t period = r_f32 ? 4 : 8;  // elements of 16 bytes of H

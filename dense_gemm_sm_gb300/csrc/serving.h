@@ -28,8 +28,7 @@ struct NormParams {
   float* scales;                // [rows] (E4M3 output)
 };
 // x_f32 / r_f32: the types of X and of R and H.  vec: every row 16-byte aligned.
-cudaError_t launch_rmsnorm(const NormParams& p, bool x_f32, bool r_f32, bool vec, int sms,
-                           cudaStream_t s);
+cudaError_t launch_rmsnorm(const NormParams& p, bool x_f32, bool r_f32, bool vec, cudaStream_t s);
 
 // ------------------------------------------------------------------ 4-bit key-value cache
 // Record of 16 tokens of one (page, head), bytes: K codes [16][d/2]; V codes [2][8][4][d/32][2][2]

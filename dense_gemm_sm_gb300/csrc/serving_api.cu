@@ -36,9 +36,6 @@ dg_status check_norm(int64_t rows, int64_t cols, const void* X, int64_t ldx, dg_
 dg_status run_norm(int64_t rows, int64_t cols, const void* X, int64_t ldx, dg_out x_type, const void* R,
                    int64_t ldr, dg_out r_type, void* H, int64_t ldh, const uint16_t* gain, float eps, void* Y,
                    int64_t ldy, float* scales, void* stream) {
-  uint32_t* status = nullptr;
-  int sms = 0;
-  if (serving_device(&status, &sms) != cudaSuccess) return DG_ERR_CUDA;
   NormParams p;
   p.rows = rows; p.cols = cols;
   p.X = X; p.ldx = ldx;
@@ -51,8 +48,7 @@ dg_status run_norm(int64_t rows, int64_t cols, const void* X, int64_t ldx, dg_ou
   const bool vec = aligned(X, 16) && ldx % 8 == 0 && aligned(gain, 16) &&
                    (!R || (aligned(R, 16) && aligned(H, 16) && ldr % 8 == 0 && ldh % 8 == 0)) &&
                    aligned(Y, scales ? 8 : 16) && ldy % 8 == 0;
-  return from_cuda(launch_rmsnorm(p, x_type == DG_OUT_F32, r_type == DG_OUT_F32, vec, sms,
-                                  static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_rmsnorm(p, x_type == DG_OUT_F32, r_type == DG_OUT_F32, vec, static_cast<cudaStream_t>(stream)));
 }
 
 // Sizes are held against their limits before anything is multiplied with them.
