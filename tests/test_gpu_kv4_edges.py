@@ -191,3 +191,29 @@ def test_batches_of_many_sequences(torch, batch, lq, hq, heads, d, lone):
     want, bound = ref.kv4_attention(pool, q, table, lens, scale)
     off = ~(np.abs(out.float().cpu().numpy() - want) <= bound)
     assert not off.any(), f"{off.sum()} of {off.size}, first {np.argwhere(off)[0]}"
+
+
+# A piece of a prompt: many blocks of query rows, each with its own last key, some before the first.
+@pytest.mark.parametrize("lens,lq,hq,heads,d", [([500, 150, 0], 200, 8, 2, 64), ([1300], 257, 4, 1, 128), ([90, 64], 90, 6, 3, 128)])
+def test_queries_of_a_prompt(torch, lens, lq, hq, heads, d):
+    rng = np.random.default_rng(lq)
+    page = 32
+    need = [-(-n // page) for n in lens]
+    order = rng.permutation(sum(need) + 1)
+    pool = ref.Kv4Pool(len(order), page, heads, d)
+    table = np.full((len(lens), max(need)), -1, np.int64)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    slots = np.concatenate([table[b, np.arange(n) // page] * page + np.arange(n) % page for b, n in enumerate(lens)])
+    for which in range(2):
+        x = ref.bf16(rng.standard_normal((len(slots), heads, d)).astype(np.float32))
+        pool.codes[which, slots], pool.scale[which, slots], pool.zero[which, slots] = ref.kv4_quantise(x)
+    q = ref.bf16(rng.standard_normal((len(lens), lq, hq, d))).astype(np.float64)
+    scale = float(np.float32(1 / np.sqrt(d)))
+    out = attend(torch, torch.from_numpy(pool.pack_all()).cuda(), torch.from_numpy(table.astype(np.int32)).cuda(), lens,
+                 torch.from_numpy(q).cuda().to(torch.bfloat16), heads, page, scale)
+    want, bound = ref.kv4_attention(pool, q, table, lens, scale)
+    off = ~(np.abs(out.float().cpu().numpy() - want) <= bound)
+    assert not off.any(), f"{off.sum()} of {off.size}, first {np.argwhere(off)[0]}"
