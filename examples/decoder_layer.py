@@ -6,7 +6,8 @@
     ->  logits = y Wr  ->  out = experts(y, logits)
 
 `out` is the next layer's x, the residual stream h is FP32 and updated in place.  Weights are
-random.  The eight calls of a step enqueue eleven kernels at most and allocate nothing once the
+random.  Queries and keys get no position: the library has no call that rotates them, and a model
+that does so would between the projection and the cache.  The eight calls of a step enqueue eleven kernels at most and allocate nothing once the
 first step has run.
 
     python examples/decoder_layer.py [--batch 16] [--context 4000] [--steps 8]

@@ -281,7 +281,9 @@ dg_status attention_bf16(int64_t batch, int64_t Lq, int64_t Lkv, int64_t d, floa
  * with h, the mean and y in FP32 and one rounding per output (the norm is of the unrounded
  * h).  Q and scales are what gemm_fp8_e4m3 reads, as quantize_rows_e4m3 writes them; a row
  * of zeros gets codes 0 and scale 0 (Y: zeros, or with eps = 0 NaN, which 0 / 0 is), a row
- * holding Inf or NaN unspecified codes.
+ * holding Inf or NaN unspecified codes.  Squares are FP32 too: a row whose sum of h^2 passes
+ * 3.4e38 (one |h| of 1.8e19 does) gives zeros, and with eps = 0 elements below 1e-19 are
+ * lost from the mean.
  *   - X: rows x cols of x_type (DG_OUT_BF16 or DG_OUT_F32), row stride ldx.  R and H: rows x
  *     cols of r_type, strides ldr and ldh; H may be R (in place).  R and H both null: no
  *     residual, h = X.  gain: cols BF16.  Y: BF16, ldy.  Q: bytes, ldq.
@@ -305,7 +307,8 @@ dg_status rmsnorm_residual_e4m3(int64_t rows, int64_t cols, const void* X, int64
  * has codes 0..15 and a BF16 scale and zero:
  *     zero = min x,  scale = bf16((max x - min x) / 15),
  *     code = clamp(round_half_even((x - zero) / scale), 0, 15),   x ~ zero + scale * code
- * (IEEE FP32 operations; a constant row has scale 0 and codes 0; rows must be finite).
+ * (IEEE FP32 operations; a constant row has scale 0 and codes 0; rows and their max - min must
+ * be finite in FP32).
  * data: [pages][heads][block], a block of dg_kv4_block_bytes(page_size, d) = page_size *
  * (d + 8) bytes holding page_size / 16 records of 16 tokens:
  *     16 x d/2 bytes        K codes, a token's row after the other, even column in the low half
@@ -352,7 +355,8 @@ dg_status kv4_gather(const dg_kv4_cache* cache, int64_t tokens, const int64_t* s
  * K and V of head h / (heads_q / cache->heads).  The tokens are in the cache already: query i
  * of sequence b sits at position lens[b] - Lq + i.  A query that sees no key (lens[b] - Lq + i
  * < 0) gets 0; one that sees keys and holds NaN or Inf gets NaN.  FP32 scores, weights and sums; the weights times V's scale are rounded to BF16
- * for the second product; O rounded once to BF16.
+ * for the second product; O rounded once to BF16.  Those sums reach 2^16 times V's scale per
+ * key: rows of V whose max - min, times the number of keys, passes 5e34 are not supported.
  *   - Q: element (b, i, h, c) at Q[b * strideQ + i * ldq + h * d + c], likewise O.
  *   - page_table: int32 [batch][ldt] on the device, entry (b, t) the page of tokens
  *     [t * page_size, (t + 1) * page_size); entries past the length are not read.  lens:
