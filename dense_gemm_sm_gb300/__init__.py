@@ -14,5 +14,6 @@ from ._lib import (  # noqa: F401
     attention_bf16, gemm_bf16, gemm_bf16_decode_chain, gemm_bf16_decode_noalloc, gemm_bf16_gate_up_silu, gemm_bf16_strided_batched, gemm_f32, gemm_fp8_e4m3, quantize_rows_e4m3, gemm_f32_strided_batched, library_path, load,
     status_string, rmsnorm_residual_bf16, rmsnorm_residual_e4m3, dg_kv4_cache, dg_kv4_block_bytes,
     kv4_append, kv4_gather, dg_attention_kv4_workspace_bytes, attention_kv4, dg_moe_workspace_bytes,
-    moe_bf16,
+    moe_bf16, attention_kv4_tree, kv4_accept, kv4_copy_pages, quantize_groups_w4, dequantize_groups_w4,
+    dg_gemm_w4_workspace_bytes, gemm_w4_bf16,
 )

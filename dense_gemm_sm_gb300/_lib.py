@@ -28,7 +28,9 @@ EXPORTED = [
     "attention_bf16", "quantize_rows_e4m3", "gemm_fp8_e4m3", "dg_model_quant_traffic_bytes",
     "gemm_bf16_decode_chain", "rmsnorm_residual_bf16", "rmsnorm_residual_e4m3",
     "dg_kv4_block_bytes", "kv4_append", "kv4_gather", "dg_attention_kv4_workspace_bytes",
-    "attention_kv4", "dg_moe_workspace_bytes", "moe_bf16",
+    "attention_kv4", "dg_moe_workspace_bytes", "moe_bf16", "attention_kv4_tree", "kv4_accept",
+    "kv4_copy_pages", "quantize_groups_w4", "dequantize_groups_w4", "dg_gemm_w4_workspace_bytes",
+    "gemm_w4_bf16",
 ]
 
 
@@ -111,11 +113,21 @@ def load(build_if_missing: bool = True):
     lib.dg_moe_workspace_bytes.restype = i64
     lib.moe_bf16.argtypes = [i64, i64, i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64,
                              vp, i64, i64, vp, i64, vp, i64, vp]
+    lib.attention_kv4_tree.argtypes = [pc, i64, i64, i64, f32, vp, i64, i64, vp, i64, vp, vp, vp, vp, i64, i64,
+                                       vp, i64, vp]
+    lib.kv4_accept.argtypes = [pc, i64, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp]
+    lib.kv4_copy_pages.argtypes = [pc, i64, vp, vp, vp]
+    lib.quantize_groups_w4.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp]
+    lib.dequantize_groups_w4.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp]
+    lib.dg_gemm_w4_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.dg_gemm_w4_workspace_bytes.restype = i64
+    lib.gemm_w4_bf16.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp]
     for f in ("gemm_f32", "gemm_f32_strided_batched", "gemm_bf16", "gemm_bf16_strided_batched",
               "gemm_bf16_decode_noalloc", "gemm_bf16_gate_up_silu", "attention_bf16",
               "quantize_rows_e4m3", "gemm_fp8_e4m3", "gemm_bf16_decode_chain",
               "rmsnorm_residual_bf16", "rmsnorm_residual_e4m3", "kv4_append", "kv4_gather",
-              "attention_kv4", "moe_bf16"):
+              "attention_kv4", "moe_bf16", "attention_kv4_tree", "kv4_accept", "kv4_copy_pages",
+              "quantize_groups_w4", "dequantize_groups_w4", "gemm_w4_bf16"):
         getattr(lib, f).restype = ctypes.c_int
     lib.dg_status_string.argtypes = [ctypes.c_int]
     lib.dg_status_string.restype = ctypes.c_char_p
@@ -321,6 +333,59 @@ def attention_kv4(cache, batch, Lq, heads_q, scale, Q, ldq, strideQ, page_table,
                            _ptr(page_table), ldt, _ptr(lens), _ptr(O), ldo, strideO,
                            _ptr(workspace), workspace_bytes, _stream(stream))
     return _ret(st, "attention_kv4", check)
+
+
+def attention_kv4_tree(cache, batch, Lq, heads_q, scale, Q, ldq, strideQ, page_table, ldt, lens, nodes, mask, O,
+                       ldo, strideO, workspace, workspace_bytes, stream=None, check=True) -> int:
+    """Attention of a tree of drafted tokens (each sees the context and its mask's nodes) over the cache."""
+    lib = load()
+    st = lib.attention_kv4_tree(ctypes.byref(cache), batch, Lq, heads_q, scale, _ptr(Q), ldq, strideQ,
+                                _ptr(page_table), ldt, _ptr(lens), _ptr(nodes), _ptr(mask), _ptr(O), ldo,
+                                strideO, _ptr(workspace), workspace_bytes, _stream(stream))
+    return _ret(st, "attention_kv4_tree", check)
+
+
+def kv4_accept(cache, batch, Lq, page_table, ldt, lens, nodes, path, ldp, counts, new_lens, stream=None,
+               check=True) -> int:
+    """Moves the accepted drafted tokens' rows to the front of the tree's slots, and gives the new lengths."""
+    lib = load()
+    st = lib.kv4_accept(ctypes.byref(cache), batch, Lq, _ptr(page_table), ldt, _ptr(lens), _ptr(nodes),
+                        _ptr(path), ldp, _ptr(counts), _ptr(new_lens), _stream(stream))
+    return _ret(st, "kv4_accept", check)
+
+
+def kv4_copy_pages(cache, n, src, dst, stream=None, check=True) -> int:
+    """Page dst[i] of the cache becomes what page src[i] is."""
+    lib = load()
+    st = lib.kv4_copy_pages(ctypes.byref(cache), n, _ptr(src), _ptr(dst), _stream(stream))
+    return _ret(st, "kv4_copy_pages", check)
+
+
+def quantize_groups_w4(N, K, group, W, ldw, Q, ldq, params, ldp, stream=None, check=True) -> int:
+    """Quantises BF16 weights [N, K] to 4 bits: codes Q, one scale and zero per group of k (params)."""
+    lib = load()
+    st = lib.quantize_groups_w4(N, K, group, _ptr(W), ldw, _ptr(Q), ldq, _ptr(params), ldp, _stream(stream))
+    return _ret(st, "quantize_groups_w4", check)
+
+
+def dequantize_groups_w4(N, K, group, Q, ldq, params, ldp, W, ldw, stream=None, check=True) -> int:
+    """The BF16 values that 4-bit weights stand for."""
+    lib = load()
+    st = lib.dequantize_groups_w4(N, K, group, _ptr(Q), ldq, _ptr(params), ldp, _ptr(W), ldw, _stream(stream))
+    return _ret(st, "dequantize_groups_w4", check)
+
+
+def dg_gemm_w4_workspace_bytes(M, N, K) -> int:
+    return load().dg_gemm_w4_workspace_bytes(M, N, K)
+
+
+def gemm_w4_bf16(M, N, K, group, X, ldx, Q, ldq, params, ldp, C, ldc, c_type, workspace, workspace_bytes,
+                 stream=None, check=True) -> int:
+    """C = X W^T for BF16 rows X and 4-bit weights W [N, K] with group scales and zeros."""
+    lib = load()
+    st = lib.gemm_w4_bf16(M, N, K, group, _ptr(X), ldx, _ptr(Q), ldq, _ptr(params), ldp, _ptr(C), ldc, c_type,
+                          _ptr(workspace), workspace_bytes, _stream(stream))
+    return _ret(st, "gemm_w4_bf16", check)
 
 
 def dg_moe_workspace_bytes(T, K, I, E, top) -> int:

@@ -247,7 +247,9 @@ struct Shared {
   uint32_t abort;
 };
 
-template <int D, int NT>
+// TREE: a query sees, of the sequence's newest tokens, those that its mask names, and a sequence may
+// have fewer than Lq queries; the others' rows are zeros.
+template <int D, int NT, bool TREE>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     kv4_attention_kernel(const Kv4AttnParams p, const int qblocks) {
   using C = Cfg<D, NT>;
@@ -284,6 +286,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   const int ips = p.heads * qblocks;  // items of a sequence
   const int rows_all = static_cast<int>(p.Lq) * p.group;
   const uint32_t batch = static_cast<uint32_t>(p.batch);
+  auto nodes_of = [&](uint32_t b) -> int32_t {  // a tree's queries
+    const int32_t n = p.nodes ? p.nodes[b] : static_cast<int32_t>(p.Lq);
+    return min(max(n, 0), static_cast<int32_t>(p.Lq));
+  };
 
   // ---- every warp adds up the units for itself; a lane takes a run of sequences, and keeps the
   // units of the first few
@@ -292,6 +298,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   auto units_of = [&](uint32_t b) {
     const int32_t n = p.lens[b];
     if (blockIdx.x == 0 && (n < 0 || n > cap)) atomicCAS(p.index_word, 0u, kDevBadIndex);
+    if (TREE && blockIdx.x == 0 && p.nodes && (p.nodes[b] < 0 || p.nodes[b] > p.Lq)) atomicCAS(p.index_word, 0u, kDevBadIndex);
     return static_cast<uint32_t>(min(max(n, 0), cap) + kUnit - 1) / kUnit;
   };
   uint32_t kept[kKept], mine = 0;
@@ -482,6 +489,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const int head = seg.item / qblocks;
       const int row0 = (seg.item - head * qblocks) * C::kRows;
       const uint16_t* qbase = p.Q + static_cast<int64_t>(seg.b) * p.strideQ + static_cast<int64_t>(head) * p.group * D;
+      const int nodes = TREE ? nodes_of(seg.b) : 0;
+      const int live = TREE ? nodes * p.group : rows_all;  // query rows that see anything
+      // The keys before this one are visible to all of them.
+      const int shared_keys = seg.len - (TREE ? nodes : static_cast<int>(p.Lq) - 1);
 
       // Q fragments: lane (g, t) takes query row g's elements [t d/4, + d/4).
       uint32_t qf[NT <= 2 ? NT : 1][KS][2];
@@ -492,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         uint4 w[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) w[j] = make_uint4(0, 0, 0, 0);
-        if (row < rows_all) {
+        if (row < live) {
           const uint4* src = reinterpret_cast<const uint4*>(qbase + static_cast<int64_t>(row / p.group) * p.ldq +
                                                             (row % p.group) * D + t * (D / 4));
 #pragma unroll
@@ -548,7 +559,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         {
           const uint32_t st = ring + slot * C::kUnitBytes;
           const int key0 = (seg.u + j) * kUnit;
-          const bool whole = have == (1u << kRecs) - 1 && key0 + kUnit <= seg.len - static_cast<int>(p.Lq) + 1;
+          const bool whole = have == (1u << kRecs) - 1 && key0 + kUnit <= shared_keys;
           // ---- S = K Q^T
           float sc[kRecs][NT][4];
 #pragma unroll
@@ -604,6 +615,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
           if (!whole) {  // the last units, and pages outside the cache
             asm volatile("" ::: "memory");  // a branch: few steps come here
+            uint64_t see[NT][2];  // the tree's nodes that a query sees
+            if constexpr (TREE) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int row = row0 + nt * 8 + 2 * t + e;
+                  see[nt][e] = row < live ? p.mask[static_cast<int64_t>(seg.b) * p.Lq + row / p.group] : 0;
+                }
+            }
 #pragma unroll
             for (int r = 0; r < kRecs; ++r)
 #pragma unroll
@@ -615,8 +636,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int e = 0; e < 2; ++e) {
-                    const int lim = seg.len - static_cast<int>(p.Lq) + (row0 + nt * 8 + 2 * t + e) / p.group;
-                    if (!in || k > lim) sc[r][nt][2 * i + e] = -INFINITY;
+                    bool seen;
+                    if constexpr (TREE) {
+                      const int node = k - shared_keys;  // below 64 where `in`
+                      seen = node < 0 || ((see[nt][e] >> (node & 63)) & 1u);
+                    } else {
+                      seen = k <= seg.len - static_cast<int>(p.Lq) + (row0 + nt * 8 + 2 * t + e) / p.group;
+                    }
+                    if (!in || !seen) sc[r][nt][2 * i + e] = -INFINITY;
                   }
               }
           }
@@ -709,6 +736,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             z[nt][e] += __shfl_xor_sync(~0u, z[nt][e], x);
           }
           z[nt][e] = fmaf(-136.f, ps[nt][e], z[nt][e]);
+          if (TREE && row0 + nt * 8 + 2 * t + e >= live) {  // no query: nothing summed
+            l[nt][e] = z[nt][e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[nt][i][e] = o[nt][i][2 + e] = 0.f;
+          }
         }
       const bool ends = seg.u + n == seg.units;
       if (seg.u == 0 && ends) {
@@ -1047,10 +1079,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TREE>
 cudaError_t launch_variant(const Kv4AttnParams& p, int sms, cudaStream_t s) {
   using C = Cfg<D, NT>;
-  auto kern = kv4_attention_kernel<D, NT>;
+  auto kern = kv4_attention_kernel<D, NT, TREE>;
   static std::atomic<uint64_t> attr_done{0};
   const cudaError_t e = ensure_smem_attr(kern, C::kSmem, attr_done);
   if (e != cudaSuccess) return e;
@@ -1079,13 +1111,20 @@ int64_t kv4_attention_ws_bytes(int64_t Lq, int64_t heads_q, int64_t heads_kv, in
   return nt == 1 ? ws_bytes<64, 1>() : nt == 2 ? ws_bytes<64, 2>() : ws_bytes<64, 4>();
 }
 
-cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) {
+template <bool TREE>
+cudaError_t launch_rows(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) {
   const int nt = tiles_of(p.Lq * p.group);
   if (d == 128)
-    return nt == 1 ? launch_variant<128, 1>(p, sms, s) : nt == 2 ? launch_variant<128, 2>(p, sms, s)
-                                                                : launch_variant<128, 4>(p, sms, s);
-  return nt == 1 ? launch_variant<64, 1>(p, sms, s) : nt == 2 ? launch_variant<64, 2>(p, sms, s)
-                                                             : launch_variant<64, 4>(p, sms, s);
+    return nt == 1   ? launch_variant<128, 1, TREE>(p, sms, s)
+           : nt == 2 ? launch_variant<128, 2, TREE>(p, sms, s)
+                     : launch_variant<128, 4, TREE>(p, sms, s);
+  return nt == 1   ? launch_variant<64, 1, TREE>(p, sms, s)
+         : nt == 2 ? launch_variant<64, 2, TREE>(p, sms, s)
+                   : launch_variant<64, 4, TREE>(p, sms, s);
+}
+
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) {
+  return p.mask ? launch_rows<true>(p, d, sms, s) : launch_rows<false>(p, d, sms, s);
 }
 
 }  // namespace dg

@@ -1,5 +1,5 @@
-// kv4_cache.cu -- writing rows of keys and values into the paged 4-bit cache, and reading them
-// back as BF16.  Per row x of d elements (one token, one head):
+// kv4_cache.cu -- writing rows of keys and values into the paged 4-bit cache, reading them back as
+// BF16, moving the rows of accepted drafted tokens, and copying pages.  Per row x of d elements (one token, one head):
 //   zero = min x,  scale = bf16((max x - min x) / 15),
 //   code_c = clamp(rne((x_c - zero) / scale), 0, 15),  x_c ~ zero + scale * code_c.
 // The minimum of BF16 values is one of them, so zero is exact in BF16; the scale is rounded
@@ -234,6 +234,112 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4Params p,
   }
 }
 
+// ------------------------------------------------------------------ accepted drafted tokens
+// A CTA per sequence, so that lengths may be updated in place and every row is read before one is
+// written; a warp takes a head at a time and holds its rows in shared memory in between: of a row,
+// lane l has two bytes of K's codes and one of the d / 4 pieces of V's, lanes 0 and 1 the parameters.
+constexpr int kMaxTree = 64;
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv4_accept_kernel(const Kv4AcceptParams p) {
+  __shared__ int64_t from[kMaxTree], to[kMaxTree];  // byte offsets of records, for head 0; from < 0: not moved
+  __shared__ int8_t from_u[kMaxTree], to_u[kMaxTree];
+  __shared__ uint32_t rows[kThreads / 32][kMaxTree][34];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t b = blockIdx.x, cap = p.ldt * p.page_size;
+  const int64_t stride = static_cast<int64_t>(p.page_size / kKv4Tokens) * kv4_record_bytes(D);
+  const int32_t len = p.lens[b], nodes = p.nodes ? p.nodes[b] : p.Lq, count = p.counts[b];
+  const bool good = len >= 0 && len <= cap && nodes >= 0 && nodes <= p.Lq && nodes <= len && count >= 0 && count <= nodes;
+  if (!good) {
+    if (tid == 0) {
+      atomicCAS(p.index_word, 0u, kDevBadIndex);
+      p.new_lens[b] = len;
+    }
+    return;
+  }
+  const int32_t base = len - nodes;
+  if (tid < count) {
+    const int32_t node = p.path[b * p.ldp + tid];
+    from[tid] = -1;
+    if (node < 0 || node >= nodes) {
+      atomicCAS(p.index_word, 0u, kDevBadIndex);
+    } else if (node != tid) {
+      int64_t at[2];
+      bool have = true;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int32_t token = base + (i ? tid : node), in = token % p.page_size;
+        const int32_t page = p.table[b * p.ldt + token / p.page_size];
+        have = have && page >= 0 && page < p.pages;
+        at[i] = page * (p.heads * stride) + (in >> 4) * kv4_record_bytes(D);
+        (i ? to_u : from_u)[tid] = static_cast<int8_t>(in & 15);
+      }
+      if (have) {
+        from[tid] = at[0];
+        to[tid] = at[1];
+      } else {
+        atomicCAS(p.index_word, 0u, kDevBadIndex);
+      }
+    }
+  }
+  __syncthreads();  // also: the length is read before it is written, where new_lens is lens
+  if (tid == 0) p.new_lens[b] = base + count;
+  for (int h = warp; h < p.heads; h += kThreads / 32) {
+    for (int k = 0; k < count; ++k) {
+      if (from[k] < 0) continue;
+      const uint8_t* rec = p.data + from[k] + h * stride;
+      const int u = from_u[k];
+      if (lane < D / 4)
+        rows[warp][k][lane] = *reinterpret_cast<const uint16_t*>(rec + u * (D / 2) + 2 * lane) |
+                              static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(rec + 8 * D + v_piece<D>(u, lane))) << 16;
+      if (lane < 2) rows[warp][k][32 + lane] = *reinterpret_cast<const uint32_t*>(rec + 16 * D + 64 * lane + u * 4);
+    }
+    __syncwarp();
+    for (int k = 0; k < count; ++k) {
+      if (from[k] < 0) continue;
+      uint8_t* rec = p.data + to[k] + h * stride;
+      const int u = to_u[k];
+      if (lane < D / 4) {
+        const uint32_t w = rows[warp][k][lane];
+        *reinterpret_cast<uint16_t*>(rec + u * (D / 2) + 2 * lane) = static_cast<uint16_t>(w);
+        *reinterpret_cast<uint16_t*>(rec + 8 * D + v_piece<D>(u, lane)) = static_cast<uint16_t>(w >> 16);
+      }
+      if (lane < 2) *reinterpret_cast<uint32_t*>(rec + 16 * D + 64 * lane + u * 4) = rows[warp][k][32 + lane];
+    }
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------ pages
+// A CTA copies 16 kB of a page at a time.
+constexpr int64_t kPiece = 16384;
+constexpr int kCopyThreads = 256;
+__global__ void __launch_bounds__(kCopyThreads) kv4_copy_kernel(const Kv4CopyParams p, const int64_t pieces) {
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t i = blockIdx.x; i < p.n * pieces; i += gridDim.x) {
+    const int64_t e = i / pieces, at = (i - e * pieces) * kPiece;
+    const int32_t src = p.src[e], dst = p.dst[e];
+    if (src < 0 || dst < 0 || src == dst) continue;
+    if (src >= p.pages || dst >= p.pages) {
+      if (threadIdx.x == 0) atomicCAS(p.index_word, 0u, kDevBadIndex);
+      continue;
+    }
+    const int64_t n = min(kPiece, p.page_bytes - at) / 16;
+    const uint4* from = reinterpret_cast<const uint4*>(p.data + src * p.page_bytes + at);
+    uint4* to = reinterpret_cast<uint4*>(p.data + dst * p.page_bytes + at);
+    constexpr int kEach = kPiece / 16 / kCopyThreads;
+    uint4 v[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (threadIdx.x + j * kCopyThreads < n) v[j] = from[threadIdx.x + j * kCopyThreads];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (threadIdx.x + j * kCopyThreads < n) to[threadIdx.x + j * kCopyThreads] = v[j];
+  }
+}
+
 // Heads of a warp: all of them where the tokens alone fill the GPU's warps, one where they are few.
 struct Shape {
   dim3 grid;
@@ -276,5 +382,15 @@ cudaError_t launch_kv4_gather(const Kv4Params& p, int d, bool vec, int sms, cuda
   return vec ? DG_KV4_LAUNCH(kv4_gather_kernel, 64, true, 8) : DG_KV4_LAUNCH(kv4_gather_kernel, 64, false, 8);
 }
 #undef DG_KV4_LAUNCH
+
+cudaError_t launch_kv4_accept(const Kv4AcceptParams& p, int d, cudaStream_t s) {
+  const dim3 g(static_cast<unsigned>(p.batch)), b(kThreads);
+  return d == 128 ? launch_pdl(kv4_accept_kernel<128>, g, b, 0, s, p) : launch_pdl(kv4_accept_kernel<64>, g, b, 0, s, p);
+}
+
+cudaError_t launch_kv4_copy_pages(const Kv4CopyParams& p, int sms, cudaStream_t s) {
+  const int64_t pieces = (p.page_bytes + kPiece - 1) / kPiece, need = p.n * pieces, cap = static_cast<int64_t>(sms) * 8;
+  return launch_pdl(kv4_copy_kernel, dim3(static_cast<unsigned>(need < cap ? need : cap)), dim3(kCopyThreads), 0, s, p, pieces);
+}
 
 }  // namespace dg

@@ -1,5 +1,5 @@
 // serving.h -- shared declarations of the serving operators: residual RMS norm, the paged
-// 4-bit key-value cache with its attention, and the mixture-of-experts layer.
+// 4-bit key-value cache with its attention, the mixture-of-experts layer, and 4-bit weights.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -51,6 +51,34 @@ struct Kv4Params {
 cudaError_t launch_kv4_append(const Kv4Params& p, int d, bool vec, int sms, cudaStream_t s);
 cudaError_t launch_kv4_gather(const Kv4Params& p, int d, bool vec, int sms, cudaStream_t s);
 
+// Accepted drafted tokens: rows base + path[k] -> base + k of each sequence (base = len - nodes).
+struct Kv4AcceptParams {
+  uint8_t* data;
+  int64_t pages;
+  int32_t page_size, heads;
+  int64_t batch;
+  int32_t Lq;
+  const int32_t* table; int64_t ldt;
+  const int32_t* lens;
+  const int32_t* nodes;             // null: Lq in every sequence
+  const int32_t* path; int64_t ldp;
+  const int32_t* counts;
+  int32_t* new_lens;
+  uint32_t* index_word;
+};
+cudaError_t launch_kv4_accept(const Kv4AcceptParams& p, int d, cudaStream_t s);
+
+struct Kv4CopyParams {
+  uint8_t* data;
+  int64_t pages;
+  int64_t page_bytes;               // of all heads, a multiple of 16
+  int64_t n;
+  const int32_t* src;
+  const int32_t* dst;
+  uint32_t* index_word;
+};
+cudaError_t launch_kv4_copy_pages(const Kv4CopyParams& p, int sms, cudaStream_t s);
+
 struct Kv4AttnParams {
   const uint8_t* data;
   int64_t pages;
@@ -68,6 +96,10 @@ struct Kv4AttnParams {
   void* ws;
   uint32_t* status;
   uint32_t* index_word;
+  // A tree of drafted tokens (mask != null): the newest `nodes` tokens (null: Lq), of which query i
+  // sees those of the bits of mask[b][i].
+  const int32_t* nodes;
+  const uint64_t* mask;
 };
 int64_t kv4_attention_ws_bytes(int64_t Lq, int64_t heads_q, int64_t heads_kv, int d);
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s);
@@ -91,5 +123,32 @@ struct MoeParams {
 };
 int64_t moe_ws_bytes(int64_t T, int64_t I, int64_t top);
 cudaError_t launch_moe(const MoeParams& p, int sms, cudaStream_t s);
+
+// ------------------------------------------------------------------ 4-bit weights
+// Row n of Q: words of 8 codes, code k % 8 at bit 4 (k % 8 / 2) + 16 (k % 2).  params[g * ldp + n]:
+// scale (BF16, low half) and zero (high half) of group g of column n.
+struct W4RowsParams {
+  int64_t N, K;
+  uint16_t* W; int64_t ldw;
+  uint8_t* Q; int64_t ldq;          // bytes
+  uint32_t* params; int64_t ldp;
+};
+// vec: rows of W 16-byte aligned.
+cudaError_t launch_quantize_w4(const W4RowsParams& p, int group, bool vec, int sms, cudaStream_t s);
+cudaError_t launch_dequantize_w4(const W4RowsParams& p, int group, bool vec, int sms, cudaStream_t s);
+
+struct W4GemmParams {
+  int64_t M, N, K;
+  int32_t group;
+  int32_t c_f32;
+  const uint16_t* X; int64_t ldx;
+  const uint8_t* Q; int64_t ldq;
+  const uint32_t* params; int64_t ldp;
+  void* C; int64_t ldc;
+  void* ws;
+  uint32_t* status;
+};
+int64_t gemm_w4_ws_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_gemm_w4(const W4GemmParams& p, int sms, cudaStream_t s);
 
 }  // namespace dg

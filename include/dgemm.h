@@ -381,6 +381,115 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
                         void* stream);
 
 /*
+ * Attention of a tree of drafted tokens over the cache: attention_kv4 in which a query sees, of the
+ * newest tokens, those that its mask names.  Sequence b has n = nodes[b] drafted tokens (Lq where
+ * nodes is null), in the cache already, at positions base + t with base = lens[b] - n, t < n;
+ * query i < n is node i and sees
+ *     every key j < base, and key base + t where bit t of mask[b * Lq + i] is set, t < n
+ * (its ancestors and itself, for a tree; no bit is taken for granted).  A query that sees no key
+ * gets 0, and so do queries i >= n.  base may be negative: positions below 0 have no key.
+ *   - nodes: int32 [batch] on the device, or null; a value outside [0, Lq] is taken as the nearest
+ *     bound and reported (DG_ERR_BAD_INDEX from dg_device_status).  mask: uint64 [batch][Lq] on
+ *     the device.  All else, the workspace (dg_attention_kv4_workspace_bytes) among it, as
+ *     attention_kv4.
+ *   - Errors: as attention_kv4, and a null mask DG_ERR_INVALID_ARG; Lq > 64 DG_ERR_UNSUPPORTED;
+ *     nodes not 4-byte or mask not 8-byte aligned DG_ERR_MISALIGNED.
+ */
+dg_status attention_kv4_tree(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, int64_t heads_q,
+                             float scale, const uint16_t* Q, int64_t ldq, int64_t strideQ,
+                             const int32_t* page_table, int64_t ldt, const int32_t* lens,
+                             const int32_t* nodes, const uint64_t* mask, uint16_t* O, int64_t ldo,
+                             int64_t strideO, void* workspace, int64_t workspace_bytes,
+                             void* stream);
+
+/*
+ * Keeps the accepted ones of a tree's drafted tokens: of sequence b, whose n = nodes[b] (Lq where
+ * nodes is null) newest tokens are at positions base + t, base = lens[b] - n, the rows (codes and
+ * parameters of K and V, all heads) of
+ *     position base + path[b * ldp + k]  go to position base + k   for k < counts[b],
+ * as if all were read before any is written, and new_lens[b] = base + counts[b].  new_lens may be
+ * lens.  What the other drafted tokens' slots hold then is unspecified.
+ *   - page_table, lens, nodes: as attention_kv4_tree.  path: int32 [batch][ldp], counts and
+ *     new_lens: int32 [batch], on the device.  A path may come in any order and name a node twice.
+ *     Sequences of one call do not share the pages of their drafted tokens.
+ *   - A row whose node is outside [0, n) or one of whose pages is outside the cache is not moved.
+ *     A sequence with lens outside [0, ldt * page_size], nodes outside [0, min(Lq, lens)] or
+ *     counts outside [0, n] is left as it is, new_lens[b] = lens[b].  All of these are reported
+ *     (DG_ERR_BAD_INDEX from dg_device_status).
+ *   - Errors: null pointers, ldp < Lq DG_ERR_INVALID_ARG; Lq > 64, batch > 65536, ldt * page_size
+ *     over 2^28 DG_ERR_UNSUPPORTED; pointers not 4-byte aligned DG_ERR_MISALIGNED; the cache's as
+ *     kv4_append.  batch == 0: nothing.
+ */
+dg_status kv4_accept(const dg_kv4_cache* cache, int64_t batch, int64_t Lq,
+                     const int32_t* page_table, int64_t ldt, const int32_t* lens,
+                     const int32_t* nodes, const int32_t* path, int64_t ldp, const int32_t* counts,
+                     int32_t* new_lens, void* stream);
+
+/*
+ * Copies pages, all heads of each: page dst[i] becomes what page src[i] is, for i < n (int32 on
+ * the device).  For sequences that fork (the page that both would write next; full pages can be
+ * shared by their page tables) and pools that are compacted.
+ *   - An entry with a negative page, or with src[i] == dst[i], is passed over; one with a page past
+ *     the cache is passed over and reported (DG_ERR_BAD_INDEX from dg_device_status).
+ *   - The pages of dst are distinct, and none of them is in src (entries that are passed over
+ *     apart): otherwise the page holds bytes of either.
+ *   - Errors: null pointers DG_ERR_INVALID_ARG; n over 2^31 - 1 DG_ERR_UNSUPPORTED; src or dst not
+ *     4-byte aligned DG_ERR_MISALIGNED; the cache's as kv4_append.  n == 0: nothing.
+ */
+dg_status kv4_copy_pages(const dg_kv4_cache* cache, int64_t n, const int32_t* src,
+                         const int32_t* dst, void* stream);
+
+/*
+ * Weights in 4 bits.  W is N x K by output column (row n: the weights of output n, as
+ * quantize_rows_e4m3 and gemm_fp8_e4m3 take them); a group is `group` (32, 64 or 128) consecutive
+ * k of one n, the last of a row may be shorter:
+ *     zero = min w,  scale = bf16((max w - min w) / 15),
+ *     code = clamp(round_half_even((w - zero) / scale), 0, 15),   w ~ zero + scale * code
+ * (IEEE FP32 operations; a constant group has scale 0 and codes 0; W and max - min of a group must
+ * be finite).
+ *   - Q: row n at Q + n * ldq (bytes), 32-bit words of 8 codes: code k in word k / 8, at bit
+ *     4 * (k % 8 / 2) of its low half where k is even, of its high half where k is odd.  Codes past
+ *     K in a row's last word are written as 0 and may be anything when read.
+ *   - params: a word for each group and n, at params[(k / group) * ldp + n]: BF16 scale in the low
+ *     half, BF16 zero in the high half.
+ *   - dequantize_groups_w4 gives bf16(zero + scale * code).
+ *   - Errors: negative sizes, short strides (ldq < 4 * ceil(K / 8), ldp < N, ldw < K), null
+ *     pointers, group <= 0 DG_ERR_INVALID_ARG; another group, N or K over 2^30
+ *     DG_ERR_UNSUPPORTED; Q or params not 16-byte aligned, ldq not a multiple of 16, ldp not one of
+ *     4, W not 2-byte aligned DG_ERR_MISALIGNED.  N == 0 or K == 0: nothing.  Rows of W may begin
+ *     anywhere (16-byte rows take the vector path).
+ */
+dg_status quantize_groups_w4(int64_t N, int64_t K, int32_t group, const uint16_t* W, int64_t ldw,
+                             uint8_t* Q, int64_t ldq, uint32_t* params, int64_t ldp, void* stream);
+dg_status dequantize_groups_w4(int64_t N, int64_t K, int32_t group, const uint8_t* Q, int64_t ldq,
+                               const uint32_t* params, int64_t ldp, uint16_t* W, int64_t ldw,
+                               void* stream);
+
+/*
+ * BF16 rows times 4-bit weights:
+ *     C[m][n] = sum_k X[m][k] * (zero + scale * code)   of n's group of k,
+ * the weights as above.  Codes are multiplied and added exactly as numbers with FP32 sums, a
+ * group's scale and zero are applied to its sum in FP32, and C is rounded once to BF16 or kept in
+ * FP32 (c_type): no weight is rounded.
+ *   - X: M x K BF16, row stride ldx.  C: M x N of c_type, row stride ldc.  Any M; the kernel is
+ *     made for few rows (the weights are read once for each 64 of them).
+ *   - A row of X that holds Inf or NaN gives values that are not finite (NaN where the definition
+ *     has Inf, it may be), in that row only.  Sums of |X| over a group times 31 stay below FP32's
+ *     range.
+ *   - workspace: see above; dg_gemm_w4_workspace_bytes (0 for sizes it does not take).
+ *   - Errors: negative sizes, short strides, null pointers, another c_type, a workspace that is
+ *     too small DG_ERR_INVALID_ARG; a group that is not 32, 64 or 128, sizes over 2^30
+ *     DG_ERR_UNSUPPORTED; X, Q or params not 16-byte or workspace not 256-byte aligned, ldx not a
+ *     multiple of 8, ldq of 16, ldp of 4, C not aligned to its element DG_ERR_MISALIGNED.
+ *     M == 0 or N == 0: nothing; K == 0: C = 0.
+ */
+int64_t dg_gemm_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+dg_status gemm_w4_bf16(int64_t M, int64_t N, int64_t K, int32_t group, const uint16_t* X,
+                       int64_t ldx, const uint8_t* Q, int64_t ldq, const uint32_t* params,
+                       int64_t ldp, void* C, int64_t ldc, dg_out c_type, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/*
  * A mixture-of-experts layer for few tokens (T <= 64), from the router's logits on:
  *     p = softmax(logits[t]) over the E experts, the `top` largest logits chosen (ties: the
  *     lowest expert), w = p, or p over the sum of the chosen p when renorm is non-zero,

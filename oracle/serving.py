@@ -1,7 +1,8 @@
 """The serving operators written out in float64 (numpy), and their error bounds.
 
-Residual RMS norm, the 4-bit key-value cache's rows and layout, attention over it, and the
-mixture-of-experts layer, each from its definition in include/dgemm.h.  Nothing here is shared
+Residual RMS norm, the 4-bit key-value cache's rows and layout, attention over it (of the newest
+tokens, of a tree of drafted ones), accepted rows and copied pages, the mixture-of-experts layer, and
+4-bit weights, each from its definition in include/dgemm.h.  Nothing here is shared
 with the CUDA sources.  A quantised row's codes are decided in IEEE single precision, which is
 part of their definition; everything else is float64.
 
@@ -124,8 +125,36 @@ class Kv4Pool:
         return out.reshape(self.pages, self.heads, -1)
 
 
-def kv4_attention(pool, q, table, lens, scale):
-    """q [batch, Lq, heads_q, d] float64 -> (O, bound) float64, O of a query without keys 0."""
+    def move(self, src, dst):
+        """Rows of slots src to slots dst, all read before any is written."""
+        for x in (self.codes, self.scale, self.zero):
+            x[:, dst] = x[:, src].copy()
+
+    def copy_pages(self, src, dst):
+        at = np.arange(self.page_size)
+        for a, b in zip(src, dst):
+            if 0 <= a < self.pages and 0 <= b < self.pages:
+                self.move(a * self.page_size + at, b * self.page_size + at)
+
+
+def tree_sees(lens, nodes, mask):
+    """What attention_kv4_tree's query i of sequence b sees, for kv4_attention: a function (b, i, n) -> [n]
+    truth values; mask [batch, Lq] whole numbers."""
+    def sees(b, i, n):
+        base = int(lens[b]) - int(nodes[b])
+        if i >= nodes[b]:
+            return np.zeros(n, bool)
+        return np.array([k < base or (int(mask[b][i]) >> (k - base)) & 1 == 1 for k in range(n)], bool)
+    return sees
+
+
+def kv4_attention(pool, q, table, lens, scale, sees=None, middle=0):
+    """q [batch, Lq, heads_q, d] float64 -> (O, bound) float64, O of a query without keys 0.
+
+    `middle`: the code from which V's deviations are counted that the rounded weights multiply.  With
+    P_j = bf16(p_j vs_j) = p_j vs_j (1 + e_j), |e_j| <= 2^-8, and O = sum_j P_j (vc_j - middle) +
+    sum_j p_j (vz_j + middle vs_j), the rounding moves O by sum_j e_j p_j vs_j (vc_j - middle): at
+    most 2^-8 sum_j p_j vs_j |vc_j - middle|."""
     batch, lq, hq, d = q.shape
     g = hq // pool.heads
     out, bound = np.zeros(q.shape), np.zeros(q.shape)
@@ -138,9 +167,9 @@ def kv4_attention(pool, q, table, lens, scale):
         slots = np.where(ok, page, 0) * pool.page_size + np.arange(n) % pool.page_size
         k, v = pool.rows(0, slots), pool.rows(1, slots)
         ks, vs = pool.scale[0, slots].astype(np.float64), pool.scale[1, slots].astype(np.float64)
-        vc = pool.codes[1, slots] * vs[..., None]
+        vc = np.abs(pool.codes[1, slots].astype(np.float64) - middle) * vs[..., None]
         for i in range(lq):
-            see = ok & (np.arange(n) <= n - lq + i)
+            see = ok & (np.arange(n) <= n - lq + i if sees is None else sees(b, i, n))
             if not see.any():
                 continue
             for h in range(hq):
@@ -182,6 +211,51 @@ def unit_mean(rows, see, units=0, ctas=152, warps=7):
     o = rows[:see].astype(np.float64).sum(0) / max(see, 1) * 15 * s
     steps = 2 * (max(-(-64 // warps), -(-max(units, len(rows) // 32 + 1) // (ctas * warps)) + 1)) + 40
     return o, BF16 * o + steps * 2.0 ** -22 * (143 + 136 + 8) * s
+
+
+# ------------------------------------------------------------------ 4-bit weights
+def w4_quantise(w, group):
+    """w [N, K] float32 holding BF16 values -> (codes uint8 [N, K], scale, zero float32 [N, groups])."""
+    parts = [kv4_quantise(w[:, a:a + group]) for a in range(0, w.shape[1], group)]
+    return (np.concatenate([p[0] for p in parts], 1), np.stack([p[1] for p in parts], 1), np.stack([p[2] for p in parts], 1))
+
+
+def w4_value(codes, scale, zero, group):
+    """The float64 values that codes stand for."""
+    g = np.arange(codes.shape[1]) // group
+    return zero[:, g].astype(np.float64) + scale[:, g].astype(np.float64) * codes
+
+
+def w4_pack(codes, ldq):
+    """Bytes [N, ldq] of codes, element by element from the layout's definition; the rest 0."""
+    n, k = codes.shape
+    out = np.zeros((n, ldq), np.uint8)
+    for j in range(k):
+        bit = 4 * (j % 8 // 2) + 16 * (j % 2)
+        out[:, j // 8 * 4 + bit // 8] |= codes[:, j] << (bit % 8)
+    return out
+
+
+def w4_params(scale, zero, ldp):
+    """Words [groups, ldp]; the rest 0."""
+    n, g = scale.shape
+    out = np.zeros((g, ldp), np.uint32)
+    out[:, :n] = (bf16_bits(scale).astype(np.uint32) | (bf16_bits(zero).astype(np.uint32) << 16)).T
+    return out
+
+
+def w4_gemm(x, codes, scale, zero, group, rounding):
+    """(C, bound) float64 of x [M, K] (float32 holding BF16) times the weights; `rounding`: of C's type.
+
+    A group's sum may be taken of codes offset by 16 (at most 31 each), the offset and the zero
+    come with the sum of x; groups, and at most 40 parts, are added one after the other."""
+    x = x.astype(np.float64)
+    c = x @ w4_value(codes, scale, zero, group).T
+    groups = scale.shape[1]
+    ax = np.stack([np.abs(x[:, a:a + group]).sum(1) for a in range(0, x.shape[1], group)], 1)
+    size = ax @ (47 * scale.astype(np.float64) + np.abs(zero)).T
+    err = (sum_err(min(group, x.shape[1])) + (groups + 40) * 2 * F32) * size
+    return c, err + rounding * (np.abs(c) + err)
 
 
 # ------------------------------------------------------------------ mixture of experts
