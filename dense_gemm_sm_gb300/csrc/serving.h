@@ -147,8 +147,9 @@ struct W4GemmParams {
   void* C; int64_t ldc;
   void* ws;
   uint32_t* status;
+  int32_t fault;                    // set at launch: 1: stages are not released (test hook)
 };
-int64_t gemm_w4_ws_bytes(int64_t M, int64_t N, int64_t K);
+int64_t gemm_w4_ws_bytes(int64_t M, int64_t N, int64_t K);  // 0: more units than the kernel counts
 cudaError_t launch_gemm_w4(const W4GemmParams& p, int sms, cudaStream_t s);
 
 }  // namespace dg

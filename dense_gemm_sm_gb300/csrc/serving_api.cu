@@ -366,7 +366,9 @@ dg_status gemm_w4_bf16(int64_t M, int64_t N, int64_t K, int32_t group, const uin
     if (!X || ldx < K) return DG_ERR_INVALID_ARG;
     const dg_status st = check_w4(N, K, group, Q, ldq, params, ldp);
     if (st != DG_OK) return st;
-    if (!workspace || workspace_bytes < gemm_w4_ws_bytes(M, N, K)) return DG_ERR_INVALID_ARG;
+    const int64_t need = gemm_w4_ws_bytes(M, N, K);
+    if (need == 0) return DG_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < need) return DG_ERR_INVALID_ARG;
     if (!aligned(X, 16) || ldx % 8 || !aligned(workspace, 256)) return DG_ERR_MISALIGNED;
   }
   if (!aligned(C, f32 ? 4 : 2)) return DG_ERR_MISALIGNED;

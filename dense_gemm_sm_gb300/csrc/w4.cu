@@ -127,40 +127,436 @@ dim3 rows_grid(const W4RowsParams& p, int sms) {
 }
 
 // ------------------------------------------------------------------ product
-// One warp per output column, its lanes over the words of the column, eight rows of X at a time.
-__global__ void __launch_bounds__(kThreads) gemm_w4_kernel(const W4GemmParams p) {
-  pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t words = (p.K + 7) / 8;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t n = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); n < p.N; n += warps) {
-    for (int64_t m0 = 0; m0 < p.M; m0 += 8) {
-      float acc[8] = {};
-      for (int64_t w = lane; w < words; w += 32) {
-        const uint32_t codes = reinterpret_cast<const uint32_t*>(p.Q + n * p.ldq)[w];
-        const uint32_t prm = p.params[8 * w / p.group * p.ldp + n];
-        const float scale = lo_of(prm), zero = hi_of(prm);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (8 * w + k >= p.K) break;
-          const float v = fmaf(scale, static_cast<float>((codes >> code_at(k)) & 15u), zero);
-#pragma unroll
-          for (int m = 0; m < 8; ++m)
-            if (m0 + m < p.M) acc[m] = fmaf(v, __uint_as_float(static_cast<uint32_t>(p.X[(m0 + m) * p.ldx + 8 * w + k]) << 16), acc[m]);
+// C[m][n] = sum over groups g of  s_gn sum_k x_mk c_nk + z_gn sum_k x_mk,  k in g.
+//
+// Weights are read once for each 64 rows of X, half a byte each: HBM bounds the call while the
+// codes get to the tensor cores without being rounded or passing through shared memory twice.
+//   * Columns of W are the 128 rows of a tcgen05.mma and rows of X its narrow operand (16, 32 or 64
+//     of them, straight from TMA).  A lane of the expanding warps holds one column's 128 codes of a
+//     unit and writes them, as BF16, to tensor memory, from where the MMA reads its A operand.
+//   * A code c becomes the BF16 number 16 + c by a shift and one AND-OR for two of them: 16 is the
+//     least offset that keeps all four bits of c in a mantissa, and the layout has neighbouring k in
+//     the two halves of a word, so that pairs come out in the operand's order.
+//   * A group's sums stay apart: D = sum x (16 + c) and, by a second product with an operand of ones,
+//     S = sum x are read from tensor memory when the group ends, and acc += s D + (z - 16 s) S in
+//     FP32.  Codes and x are exact in BF16, so no weight is rounded.
+// Units of 128 columns x 128 k of all column tiles are cut evenly over one CTA per SM; a tile cut between
+// CTAs is finished by the last of them to arrive, which adds the parts in CTA order (results do not depend on
+// arrival).  More than 64 rows of X: each column tile is computed for one block of 64 after the other,
+// by CTAs that run together, so the weights come from L2 after the first.
+constexpr int kMaxCtas = 160;               // CTAs that the workspace has room for
+constexpr int kUnitK = 128;
+constexpr uint32_t kCodeBytes = 128 * kUnitK / 2, kParamBytes = 4 * 128 * 4;
+constexpr int kEpiWarps = 4, kExpandGroups = 2;
+constexpr int kProducer = kEpiWarps + 4 * kExpandGroups, kIssuer = kProducer + 1;
+constexpr int kGemmThreads = 32 * (kIssuer + 1);
+constexpr uint32_t kMinUnits = 4;           // of a CTA
+// Tensor memory: 256 columns of (D, S) slots, the expanded operand in a buffer for each expanding
+// warpgroup, the ones.
+constexpr uint32_t kACol = 256, kOnesCol = kACol + 64 * kExpandGroups, kTmemCols = 512;
+constexpr int64_t kCounterBytes = 1024;
+static_assert(kMaxCtas * 4 <= kCounterBytes, "counters");
+
+template <int NTOK>
+struct Cfg {
+  static constexpr int kStages = NTOK == 16 ? 14 : NTOK == 32 ? 11 : 8;
+  static constexpr uint32_t kXBytes = NTOK * kUnitK * 2;
+  static constexpr uint32_t kStage = kCodeBytes + kXBytes + kParamBytes;
+  static constexpr int kSlots = 128 / NTOK;
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage;
+  static_assert(kStage % 1024 == 0 && kSmem + 1024 <= 227 * 1024, "shared memory, with the static part");
+};
+
+struct Control {
+  uint64_t full[14], empty[14], afull[kExpandGroups], aempty[kExpandGroups], dfull[8], dempty[8], drain;
+  uint32_t tmem_base, abort, ok, is_last;
+};
+
+// Units cut evenly over workers, the first `rem` of them one unit longer.
+struct Split {
+  uint32_t q, rem;
+  __device__ __forceinline__ Split(uint32_t units, uint32_t workers) : q(units / workers), rem(units - q * workers) {}
+  __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * q + (c < rem ? c : rem); }
+  __device__ __forceinline__ uint32_t worker(uint32_t x) const {  // that has unit x
+    const uint32_t long_units = rem * (q + 1);
+    return x < long_units ? x / (q + 1) : rem + (x - long_units) / q;
+  }
+};
+
+struct Maps {
+  CUtensorMap codes, x, params;
+};
+
+__device__ __forceinline__ uint32_t take_ticket(uint32_t* a) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(a) : "memory");
+  return old;
+}
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] B[smem]: row m of A in lane m, two BF16 of k per 32-bit column, low half first.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t a, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t a, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t w;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(a));
+  return w;
+}
+
+// Codes -> BF16 pairs 16 + code: bits 3-6 of 0x4180.
+struct Magic {
+  uint32_t mask, offset;  // in registers: as constants the AND and the OR are two instructions
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
+    asm volatile("mov.b32 %0, 0x41804180;" : "=r"(offset));
+  }
+  __device__ __forceinline__ uint32_t pair(uint32_t w) const {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(offset));  // (a & b) | c
+    return d;
+  }
+};
+
+template <int NTOK>
+__global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_constant__ Maps maps, const W4GemmParams p) {
+  using C = Cfg<NTOK>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Control ctl;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  volatile uint32_t* abort = &ctl.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&ctl.full[s]), 1);
+      mbar_init(smem_u32(&ctl.empty[s]), 1 + kEpiWarps);
+    }
+    for (int a = 0; a < kExpandGroups; ++a) {
+      mbar_init(smem_u32(&ctl.afull[a]), 4);
+      mbar_init(smem_u32(&ctl.aempty[a]), 1);
+    }
+    for (int a = 0; a < C::kSlots; ++a) {
+      mbar_init(smem_u32(&ctl.dfull[a]), 1);
+      mbar_init(smem_u32(&ctl.dempty[a]), kEpiWarps);
+    }
+    mbar_init(smem_u32(&ctl.drain), 1);
+    ctl.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kIssuer) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kProducer && lane == 0) {
+    tma_prefetch_map(&maps.codes);
+    tma_prefetch_map(&maps.x);
+    tma_prefetch_map(&maps.params);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+  const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's lanes
+  if (warp < kEpiWarps) {
+    tmem_st_x8(tl + kOnesCol, 0x3F803F80u);
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const uint32_t kb = static_cast<uint32_t>((p.K + kUnitK - 1) / kUnitK);
+  const uint32_t blocks = static_cast<uint32_t>((p.M + NTOK - 1) / NTOK);
+  const uint32_t tiles = static_cast<uint32_t>((p.N + 127) / 128) * blocks;
+  const Split split(tiles * kb, gridDim.x);
+  const uint32_t u0 = split.start(blockIdx.x), n = split.start(blockIdx.x + 1) - u0;
+  const int groups = kUnitK / p.group, ksteps = p.group / 16;
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0) {
+      uint32_t tile = u0 / kb, k = u0 - tile * kb;
+      const uint32_t bytes = kCodeBytes + C::kXBytes + 512u * groups;
+      uint32_t i = 0;
+      pdl_wait();
+      for (; i < n; ++i) {
+        const uint32_t s = i % C::kStages;
+        if (!mbar_wait(smem_u32(&ctl.empty[s]), ((i / C::kStages) & 1u) ^ 1u, abort, p.status, kDevTimeoutProducer)) break;
+        const uint32_t f = smem_u32(&ctl.full[s]), to = ring + s * C::kStage;
+        const int32_t col = static_cast<int32_t>(tile / blocks * 128), row = static_cast<int32_t>(tile % blocks * NTOK);
+        mbar_arrive_expect_tx(f, bytes);
+        tma_load_2d(to, &maps.codes, f, static_cast<int32_t>(k * (kUnitK / 2)), col);
+        tma_load_2d(to + kCodeBytes, &maps.x, f, static_cast<int32_t>(k * kUnitK), row);
+        tma_load_2d(to + kCodeBytes + NTOK * 128, &maps.x, f, static_cast<int32_t>(k * kUnitK + 64), row);
+        tma_load_2d(to + kCodeBytes + C::kXBytes, &maps.params, f, col, static_cast<int32_t>(k * groups));
+        if (++k == kb) {
+          k = 0;
+          ++tile;
         }
       }
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(~0u, acc[m], o);
-        if (lane != 0 || m0 + m >= p.M) continue;
-        if (p.c_f32) static_cast<float*>(p.C)[(m0 + m) * p.ldc + n] = acc[m];
-        else static_cast<__nv_bfloat16*>(p.C)[(m0 + m) * p.ldc + n] = __float2bfloat16_rn(acc[m]);
+      pdl_trigger();
+      ctl.ok = i;  // read only after the CTA's last barrier: stages that were filled
+    }
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, NTOK, false, false);
+      const uint64_t x0 = sdesc_sw128(ring + kCodeBytes, 16, 1024);
+      uint32_t count = 0;
+      bool ok = true;
+      pdl_wait();  // bounded waits start when this grid's data can arrive
+      for (uint32_t i = 0; ok && i < n; ++i) {
+        const uint32_t s = i % C::kStages, b = i % kExpandGroups;
+        if (!mbar_wait(smem_u32(&ctl.full[s]), (i / C::kStages) & 1u, abort, p.status, kDevTimeoutMma) ||
+            !mbar_wait(smem_u32(&ctl.afull[b]), (i / kExpandGroups) & 1u, abort, p.status, kDevTimeoutMma))
+          break;
+        const uint64_t x = x0 + s * (C::kStage >> 4);
+        const uint32_t a = tmem + kACol + 64 * b;
+        for (int g = 0; g < groups; ++g, ++count) {
+          const uint32_t slot = count % C::kSlots, d = tmem + slot * 2 * NTOK;
+          if (!mbar_wait(smem_u32(&ctl.dempty[slot]), ((count / C::kSlots) & 1u) ^ 1u, abort, p.status, kDevTimeoutMma)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          for (int j = 0; j < ksteps; ++j) {
+            const int kk = g * ksteps + j;
+            umma_ts(d, a + kk * 8, x + ((kk >> 2) * NTOK * 128 + (kk & 3) * 32) / 16, idesc, j > 0);
+          }
+          for (int j = 0; j < ksteps; ++j) {
+            const int kk = g * ksteps + j;
+            umma_ts(d + NTOK, tmem + kOnesCol, x + ((kk >> 2) * NTOK * 128 + (kk & 3) * 32) / 16, idesc, j > 0);
+          }
+          umma_commit(smem_u32(&ctl.dfull[slot]));
+        }
+        if (!ok) break;
+        umma_commit(smem_u32(&ctl.aempty[b]));
+        if (p.fault != 1) umma_commit(smem_u32(&ctl.empty[s]));
       }
+      umma_commit(smem_u32(&ctl.drain));
+      uint32_t never = 0;
+      mbar_wait(smem_u32(&ctl.drain), 0, &never, p.status, kDevTimeoutDrain);
+    }
+  } else if (warp >= kEpiWarps) {
+    // ------------------------------------------------------------ expansion: a warpgroup takes every other unit
+    const Magic magic;
+    const uint32_t g = (warp - kEpiWarps) / 4, row = (warp & 3) * 32 + lane;
+    const uint32_t at = row * 64, swz = (row >> 1) & 3;  // 64-byte rows, 16-byte pieces swizzled
+    pdl_wait();
+    for (uint32_t i = g; i < n; i += kExpandGroups) {
+      const uint32_t s = i % C::kStages;
+      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), (i / C::kStages) & 1u, abort, p.status, kDevTimeoutMma))) break;
+      uint32_t v[2][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 w = lds128(ring + s * C::kStage + at + ((c ^ swz) << 4));
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t* to = &v[c >> 1][(c & 1) * 16 + 4 * j];
+          to[0] = magic.pair(ws[j] << 3);
+          to[1] = magic.pair(ws[j] >> 1);
+          to[2] = magic.pair(ws[j] >> 5);
+          to[3] = magic.pair(ws[j] >> 9);
+        }
+      }
+      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.aempty[g]), ((i / kExpandGroups) & 1u) ^ 1u, abort, p.status, kDevTimeoutMma))) break;
+      tc_fence_after();
+      tmem_st_x32(tl + kACol + 64 * g, v[0]);
+      tmem_st_x32(tl + kACol + 64 * g + 32, v[1]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.afull[g]));
+    }
+  } else {
+    // ------------------------------------------------------------ groups' sums, and the tiles' join: a thread per column
+    const int col = warp * 32 + lane;
+    uint32_t* counters = static_cast<uint32_t*>(p.ws);
+    float4* parts = reinterpret_cast<float4*>(static_cast<uint8_t*>(p.ws) + kCounterBytes);
+    uint32_t i = 0, count = 0;
+    pdl_wait();
+    while (i < n) {
+      const uint32_t tile = (u0 + i) / kb, first = tile * kb, k0 = u0 + i - first, units = min(kb - k0, n - i);
+      float acc[NTOK];
+#pragma unroll
+      for (int t = 0; t < NTOK; ++t) acc[t] = 0.f;
+      bool ok = true;
+      for (const uint32_t to = i + units; ok && i < to; ++i) {
+        const uint32_t s = i % C::kStages;
+        ok = __all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), (i / C::kStages) & 1u, abort, p.status, kDevTimeoutEpilogue));
+        for (int g = 0; ok && g < groups; ++g, ++count) {
+          const uint32_t slot = count % C::kSlots, d = tl + slot * 2 * NTOK;
+          const uint32_t prm = lds32(ring + s * C::kStage + kCodeBytes + C::kXBytes + g * 512 + col * 4);
+          const float scale = lo_of(prm), zero = fmaf(-16.f, scale, hi_of(prm));
+          ok = __all_sync(~0u, mbar_wait(smem_u32(&ctl.dfull[slot]), (count / C::kSlots) & 1u, abort, p.status, kDevTimeoutEpilogue));
+          if (!ok) break;
+          tc_fence_after();
+          constexpr int kAtOnce = NTOK < 32 ? NTOK : 32;
+#pragma unroll
+          for (int c = 0; c < NTOK; c += kAtOnce) {
+            uint32_t dv[kAtOnce], sv[kAtOnce];
+            if constexpr (kAtOnce == 16) {
+              tmem_ld_32x32b_x16(d + c, dv);
+              tmem_ld_32x32b_x16(d + NTOK + c, sv);
+            } else {
+              tmem_ld_32x32b_x32(d + c, dv);
+              tmem_ld_32x32b_x32(d + NTOK + c, sv);
+            }
+            tmem_ld_wait();
+            if (c + kAtOnce == NTOK) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&ctl.dempty[slot]));
+            }
+#pragma unroll
+            for (int t = 0; t < kAtOnce; ++t)
+              acc[c + t] = fmaf(scale, __uint_as_float(dv[t]), fmaf(zero, __uint_as_float(sv[t]), acc[c + t]));
+          }
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(smem_u32(&ctl.empty[s]));
+      }
+      // One decision of the four warps, so that none is left alone in a barrier.
+      if (!ok) *abort = 1;
+      epi_bar();
+      if (threadIdx.x == 0) ctl.is_last = *abort ? 2u : 0u;
+      epi_bar();
+      if (ctl.is_last == 2u) break;
+      const int64_t m0 = static_cast<int64_t>(tile % blocks) * NTOK, c0 = static_cast<int64_t>(tile / blocks) * 128 + col;
+      const int m = static_cast<int>(p.M - m0 < NTOK ? p.M - m0 : NTOK), nq = (m + 3) / 4;
+      bool write = units == kb;
+      if (!write) {
+        // A part of a tile of several CTAs: [4 rows of X][column] float4.  A CTA has at most two, the one
+        // that its share begins in and the one that it ends in, and is the first of at most one.
+        auto part_of = [&](uint32_t c) {
+          return parts + (static_cast<int64_t>(c) * 2 + (split.start(c) >= first ? 0 : 1)) * (NTOK / 4) * 128 + col;
+        };
+        float4* mine = part_of(blockIdx.x);
+#pragma unroll
+        for (int q = 0; q < NTOK / 4; ++q)
+          if (q < nq) __stcg(mine + q * 128, make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]));
+        const uint32_t lo = split.worker(first), hi = split.worker(first + kb - 1);
+        epi_bar();  // the ticket's release covers the four warps' stores
+        if (threadIdx.x == 0) {
+          const bool last = take_ticket(counters + lo) == hi - lo;
+          if (last) counters[lo] = 0;  // all tickets are taken: ready for the next call
+          ctl.is_last = last;
+        }
+        epi_bar();
+        write = ctl.is_last != 0;
+        if (write) {
+#pragma unroll
+          for (int t = 0; t < NTOK; ++t) acc[t] = 0.f;
+          constexpr int kChunk = NTOK / 4 < 8 ? NTOK / 4 : 8;  // loads in flight: registers
+#pragma unroll
+          for (int q0 = 0; q0 < NTOK / 4; q0 += kChunk) {
+            if (q0 >= nq) break;
+#pragma unroll NTOK == 16 ? 2 : 1
+            for (uint32_t c = lo; c <= hi; ++c) {
+              const float4* src = part_of(c);
+              float4 v[kChunk];
+#pragma unroll
+              for (int q = 0; q < kChunk; ++q) v[q] = q0 + q < nq ? __ldcg(src + (q0 + q) * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int q = 0; q < kChunk; ++q) {
+                float* to = &acc[4 * (q0 + q)];
+                to[0] += v[q].x;
+                to[1] += v[q].y;
+                to[2] += v[q].z;
+                to[3] += v[q].w;
+              }
+            }
+          }
+        }
+      }
+      if (write && c0 < p.N) {
+        if (p.c_f32) {
+          float* to = static_cast<float*>(p.C) + m0 * p.ldc + c0;
+#pragma unroll
+          for (int t = 0; t < NTOK; ++t)
+            if (t < m) to[t * p.ldc] = acc[t];
+        } else {
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.C) + m0 * p.ldc + c0;
+#pragma unroll
+          for (int t = 0; t < NTOK; ++t)
+            if (t < m) to[t * p.ldc] = __float2bfloat16_rn(acc[t]);
+        }
+      }
+      epi_bar();  // is_last is written again only after all have read it
     }
   }
+
+  tc_fence_before();
+  __syncthreads();
+  if (ctl.abort && warp == kProducer && lane == 0) {
+    // Some wait ran out: the copies in flight land before the CTA ends.
+    const uint32_t issued = ctl.ok;
+    uint32_t never = 0;
+    for (uint32_t j = issued > C::kStages ? issued - C::kStages : 0u; j < issued; ++j)
+      mbar_wait(smem_u32(&ctl.full[j % C::kStages]), (j / C::kStages) & 1u, &never, p.status, kDevTimeoutDrain);
+  }
+  if (warp == kIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
+
+template <int NTOK>
+cudaError_t launch_ntok(const W4GemmParams& p, int sms, cudaStream_t s) {
+  using C = Cfg<NTOK>;
+  Maps m;
+  // A single row has no stride of its own.
+  const int64_t words = (p.K + 7) / 8, ldq = p.N > 1 ? p.ldq : (4 * words + 15) / 16 * 16, ldx = p.M > 1 ? p.ldx : (p.K + 7) / 8 * 8;
+  const int64_t groups = (p.K + p.group - 1) / p.group, ldp = groups > 1 ? p.ldp : (p.N + 3) / 4 * 4;
+  if (!make_tile_map(&m.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.Q, 4 * words, p.N, ldq, 1, 0, kUnitK / 2, 128,
+                     CU_TENSOR_MAP_SWIZZLE_64B, 1) ||
+      !make_tile_map(&m.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.X, p.K, p.M, ldx, 1, 0, 64, NTOK, CU_TENSOR_MAP_SWIZZLE_128B, 1) ||
+      !make_tile_map(&m.params, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.params, p.N, groups, ldp, 1, 0, 128, kUnitK / p.group,
+                     CU_TENSOR_MAP_SWIZZLE_NONE, 1))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> attr_done{0};
+  const cudaError_t e = ensure_smem_attr(gemm_w4_kernel<NTOK>, C::kSmem, attr_done);
+  if (e != cudaSuccess) return e;
+  const int64_t units = (p.N + 127) / 128 * ((p.M + NTOK - 1) / NTOK) * ((p.K + kUnitK - 1) / kUnitK);
+  int64_t ctas = (units + kMinUnits - 1) / kMinUnits;
+  if (ctas > sms) ctas = sms;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  W4GemmParams q = p;
+  q.fault = g_fault_injection;
+  return launch_pdl(gemm_w4_kernel<NTOK>, dim3(static_cast<unsigned>(ctas)), dim3(kGemmThreads), C::kSmem, s, m, q);
+}
+
+int ntok_of(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
 }  // namespace
 
@@ -181,11 +577,16 @@ cudaError_t launch_dequantize_w4(const W4RowsParams& p, int group, bool vec, int
              : launch_pdl(dequantize_w4_kernel<false>, g, b, 0, s, p, group / 8);
 }
 
-int64_t gemm_w4_ws_bytes(int64_t, int64_t, int64_t) { return 256; }
+int64_t gemm_w4_ws_bytes(int64_t M, int64_t N, int64_t K) {
+  // Units are counted in 31 bits.
+  const int64_t rows = (M + 63) / 64, tiles = (N + 127) / 128, kb = (K + kUnitK - 1) / kUnitK;
+  if (rows > INT32_MAX / tiles / kb) return 0;
+  return kCounterBytes + int64_t(kMaxCtas) * 2 * ntok_of(M) * 128 * 4;
+}
 
 cudaError_t launch_gemm_w4(const W4GemmParams& p, int sms, cudaStream_t s) {
-  const int64_t need = (p.N + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<int64_t>(sms) * 8;
-  return launch_pdl(gemm_w4_kernel, dim3(static_cast<unsigned>(need < cap ? need : cap)), dim3(kThreads), 0, s, p);
+  const int ntok = ntok_of(p.M);
+  return ntok == 16 ? launch_ntok<16>(p, sms, s) : ntok == 32 ? launch_ntok<32>(p, sms, s) : launch_ntok<64>(p, sms, s);
 }
 
 }  // namespace dg
