@@ -137,39 +137,46 @@ dim3 rows_grid(const W4RowsParams& p, int sms) {
 //   * A code c becomes the BF16 number 16 + c by a shift and one AND-OR for two of them: 16 is the
 //     least offset that keeps all four bits of c in a mantissa, and the layout has neighbouring k in
 //     the two halves of a word, so that pairs come out in the operand's order.
-//   * A group's sums stay apart: D = sum x (16 + c) and, by a second product with an operand of ones,
-//     S = sum x are read from tensor memory when the group ends, and acc += s D + (z - 16 s) S in
+//   * A group's sums stay apart: D = sum x (16 + c) is read from tensor memory when its group ends, S = sum x
+//     comes from two warps of their own (mma.sync with an operand of ones), and acc += s D + (z - 16 s) S in
 //     FP32.  Codes and x are exact in BF16, so no weight is rounded.
-// Units of 128 columns x 128 k of all column tiles are cut evenly over one CTA per SM; a tile cut between
+// Units of 128 columns x 256 k of all column tiles are cut evenly over one CTA per SM; a tile cut between
 // CTAs is finished by the last of them to arrive, which adds the parts in CTA order (results do not depend on
 // arrival).  More than 64 rows of X: each column tile is computed for one block of 64 after the other,
 // by CTAs that run together, so the weights come from L2 after the first.
+// Warps: 0-3 groups' sums and joins (a thread per column), 4-11 expansion (a warpgroup for each half of a
+// unit), 12 copies, 13 products, 14-15 sums of X.
 constexpr int kMaxCtas = 160;               // CTAs that the workspace has room for
-constexpr int kUnitK = 128;
-constexpr uint32_t kCodeBytes = 128 * kUnitK / 2, kParamBytes = 4 * 128 * 4;
-constexpr int kEpiWarps = 4, kExpandGroups = 2;
-constexpr int kProducer = kEpiWarps + 4 * kExpandGroups, kIssuer = kProducer + 1;
-constexpr int kGemmThreads = 32 * (kIssuer + 1);
-constexpr uint32_t kMinUnits = 4;           // of a CTA
-// Tensor memory: 256 columns of (D, S) slots, the expanded operand in a buffer for each expanding
-// warpgroup, the ones.
-constexpr uint32_t kACol = 256, kOnesCol = kACol + 64 * kExpandGroups, kTmemCols = 512;
+constexpr int kUnitK = 256, kHalfK = 128;
+constexpr uint32_t kCodeBytes = 128 * kUnitK / 2;
+constexpr int kEpiWarps = 4, kSumWarps = 2;
+constexpr int kProducer = 12, kIssuer = 13, kFirstSum = 14;
+constexpr int kGemmThreads = 32 * (kFirstSum + kSumWarps);
+constexpr uint32_t kMinUnits = 2;           // of a CTA
+// Tensor memory: 256 columns of D, four buffers of an expanded half of a unit.
+constexpr uint32_t kACol = 256, kTmemCols = 512;
+constexpr int kABuffers = 4;
 constexpr int64_t kCounterBytes = 1024;
 static_assert(kMaxCtas * 4 <= kCounterBytes, "counters");
 
-template <int NTOK>
+template <int NTOK, int GROUP>
 struct Cfg {
-  static constexpr int kStages = NTOK == 16 ? 14 : NTOK == 32 ? 11 : 8;
-  static constexpr uint32_t kXBytes = NTOK * kUnitK * 2;
-  static constexpr uint32_t kStage = kCodeBytes + kXBytes + kParamBytes;
-  static constexpr int kSlots = 128 / NTOK;
-  static constexpr uint32_t kSmem = 1024 + kStages * kStage;
-  static_assert(kStage % 1024 == 0 && kSmem + 1024 <= 227 * 1024, "shared memory, with the static part");
+  static constexpr int kStages = NTOK == 16 ? 7 : NTOK == 32 ? 6 : 4;
+  static constexpr int kGroups = kUnitK / GROUP;             // of a unit
+  // Groups whose D is read together: 64 columns, within a half of a unit.
+  static constexpr int kTogether = kHalfK / GROUP < 64 / NTOK ? kHalfK / GROUP : 64 / NTOK;
+  static constexpr int kReads = kGroups / kTogether;         // of a unit
+  static constexpr int kSlots = 256 / (kTogether * NTOK) < 8 ? 256 / (kTogether * NTOK) : 8;
+  static constexpr uint32_t kXBox = NTOK * 128, kXBytes = 4 * kXBox, kParamBytes = kGroups * 512;
+  static constexpr uint32_t kStage = kCodeBytes + kXBytes + 4096;
+  static constexpr uint32_t kSumBytes = kGroups * NTOK * 4;  // of a stage
+  static constexpr uint32_t kSmem = 1024 + kStages * (kStage + kSumBytes);
+  static_assert(kStage % 1024 == 0 && kParamBytes <= 4096 && kSmem + 1024 <= 227 * 1024, "shared memory, with the static part");
 };
 
 struct Control {
-  uint64_t full[14], empty[14], afull[kExpandGroups], aempty[kExpandGroups], dfull[8], dempty[8], drain;
-  uint32_t tmem_base, abort, ok, is_last;
+  uint64_t full[7], empty[7], sums[7], afull[kABuffers], aempty[kABuffers], dfull[8], dempty[8], drain;
+  uint32_t tmem_base, abort, issued, verdict;
 };
 
 // Units cut evenly over workers, the first `rem` of them one unit longer.
@@ -216,9 +223,6 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t a, const uint32_t (&r)[32])
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_x8(uint32_t a, uint32_t v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(a), "r"(v) : "memory");
-}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -246,12 +250,22 @@ struct Magic {
   }
 };
 
-template <int NTOK>
+// The sums of eight rows of X over 16 k: a row of the product with ones.
+__device__ __forceinline__ void mma_ones(float (&c)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%4,%4,%4}, {%5,%6}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(0x3F803F80u), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+
+template <int NTOK, int GROUP>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_constant__ Maps maps, const W4GemmParams p) {
-  using C = Cfg<NTOK>;
+  using C = Cfg<NTOK, GROUP>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control ctl;
-  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u, sum_ring = ring + C::kStages * C::kStage;
   volatile uint32_t* abort = &ctl.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -259,8 +273,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&ctl.full[s]), 1);
       mbar_init(smem_u32(&ctl.empty[s]), 1 + kEpiWarps);
+      mbar_init(smem_u32(&ctl.sums[s]), kSumWarps);
     }
-    for (int a = 0; a < kExpandGroups; ++a) {
+    for (int a = 0; a < kABuffers; ++a) {
       mbar_init(smem_u32(&ctl.afull[a]), 4);
       mbar_init(smem_u32(&ctl.aempty[a]), 1);
     }
@@ -276,109 +291,128 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
     tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kProducer && lane == 0) {
-    tma_prefetch_map(&maps.codes);
-    tma_prefetch_map(&maps.x);
-    tma_prefetch_map(&maps.params);
-  }
+  if (warp == kProducer && lane < 3) tma_prefetch_map(lane == 0 ? &maps.codes : lane == 1 ? &maps.params : &maps.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's lanes
-  if (warp < kEpiWarps) {
-    tmem_st_x8(tl + kOnesCol, 0x3F803F80u);
-    tmem_st_wait();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
 
   const uint32_t kb = static_cast<uint32_t>((p.K + kUnitK - 1) / kUnitK);
   const uint32_t blocks = static_cast<uint32_t>((p.M + NTOK - 1) / NTOK);
   const uint32_t tiles = static_cast<uint32_t>((p.N + 127) / 128) * blocks;
   const Split split(tiles * kb, gridDim.x);
   const uint32_t u0 = split.start(blockIdx.x), n = split.start(blockIdx.x + 1) - u0;
-  const int groups = kUnitK / p.group, ksteps = p.group / 16;
 
   if (warp == kProducer) {
-    // ------------------------------------------------------------ copies
-    if (lane == 0) {
-      uint32_t tile = u0 / kb, k = u0 - tile * kb;
-      const uint32_t bytes = kCodeBytes + C::kXBytes + 512u * groups;
-      uint32_t i = 0;
-      pdl_wait();
-      for (; i < n; ++i) {
-        const uint32_t s = i % C::kStages;
-        if (!mbar_wait(smem_u32(&ctl.empty[s]), ((i / C::kStages) & 1u) ^ 1u, abort, p.status, kDevTimeoutProducer)) break;
-        const uint32_t f = smem_u32(&ctl.full[s]), to = ring + s * C::kStage;
-        const int32_t col = static_cast<int32_t>(tile / blocks * 128), row = static_cast<int32_t>(tile % blocks * NTOK);
-        mbar_arrive_expect_tx(f, bytes);
-        tma_load_2d(to, &maps.codes, f, static_cast<int32_t>(k * (kUnitK / 2)), col);
-        tma_load_2d(to + kCodeBytes, &maps.x, f, static_cast<int32_t>(k * kUnitK), row);
-        tma_load_2d(to + kCodeBytes + NTOK * 128, &maps.x, f, static_cast<int32_t>(k * kUnitK + 64), row);
-        tma_load_2d(to + kCodeBytes + C::kXBytes, &maps.params, f, col, static_cast<int32_t>(k * groups));
-        if (++k == kb) {
-          k = 0;
-          ++tile;
-        }
+    // ------------------------------------------------------------ copies: a lane for each of a stage
+    uint32_t tile = u0 / kb, k = u0 - tile * kb, col = tile / blocks, row = tile - col * blocks, s = 0, ph = 1, i = 0;
+    const int box = lane - 2;  // of X
+    const CUtensorMap* map = lane == 0 ? &maps.codes : lane == 1 ? &maps.params : &maps.x;
+    const uint32_t to = ring + (lane == 0 ? 0u : lane == 1 ? kCodeBytes + C::kXBytes : kCodeBytes + box * C::kXBox);
+    pdl_wait();
+    for (; i < n; ++i) {
+      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.empty[s]), ph, abort, p.status, kDevTimeoutProducer))) break;
+      const uint32_t f = smem_u32(&ctl.full[s]);
+      if (lane == 0) mbar_arrive_expect_tx(f, kCodeBytes + C::kXBytes + C::kParamBytes);
+      __syncwarp();
+      const int32_t x = lane == 0 ? k * (kUnitK / 2) : lane == 1 ? col * 128 : k * kUnitK + box * 64;
+      const int32_t y = lane == 0 ? col * 128 : lane == 1 ? k * C::kGroups : row * NTOK;
+      if (lane < 6) tma_load_2d(to + s * C::kStage, map, f, x, y);
+      if (++s == C::kStages) s = 0, ph ^= 1u;
+      if (++k == kb) {
+        k = 0;
+        if (++row == blocks) row = 0, ++col;
       }
-      pdl_trigger();
-      ctl.ok = i;  // read only after the CTA's last barrier: stages that were filled
     }
+    pdl_trigger();
+    if (lane == 0) ctl.issued = i;
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, NTOK, false, false);
       const uint64_t x0 = sdesc_sw128(ring + kCodeBytes, 16, 1024);
-      uint32_t count = 0;
+      uint32_t s = 0, slot = 0, dph = 1, a = 0, aph = 0;
       bool ok = true;
       pdl_wait();  // bounded waits start when this grid's data can arrive
-      for (uint32_t i = 0; ok && i < n; ++i) {
-        const uint32_t s = i % C::kStages, b = i % kExpandGroups;
-        if (!mbar_wait(smem_u32(&ctl.full[s]), (i / C::kStages) & 1u, abort, p.status, kDevTimeoutMma) ||
-            !mbar_wait(smem_u32(&ctl.afull[b]), (i / kExpandGroups) & 1u, abort, p.status, kDevTimeoutMma))
-          break;
+      for (uint32_t i = 0; i < n; ++i) {
         const uint64_t x = x0 + s * (C::kStage >> 4);
-        const uint32_t a = tmem + kACol + 64 * b;
-        for (int g = 0; g < groups; ++g, ++count) {
-          const uint32_t slot = count % C::kSlots, d = tmem + slot * 2 * NTOK;
-          if (!mbar_wait(smem_u32(&ctl.dempty[slot]), ((count / C::kSlots) & 1u) ^ 1u, abort, p.status, kDevTimeoutMma)) {
-            ok = false;
-            break;
-          }
+#pragma unroll
+        for (int r = 0; r < C::kReads; ++r) {
+          constexpr int kSteps = GROUP / 16, kHalfReads = C::kReads / 2;
+          // (The warps that expanded the half have seen its stage filled.)
+          if (r % kHalfReads == 0) ok = ok && mbar_wait(smem_u32(&ctl.afull[a]), aph, abort, p.status, kDevTimeoutMma);
+          ok = ok && mbar_wait(smem_u32(&ctl.dempty[slot]), dph, abort, p.status, kDevTimeoutMma);
+          if (!ok) break;
           tc_fence_after();
-          for (int j = 0; j < ksteps; ++j) {
-            const int kk = g * ksteps + j;
-            umma_ts(d, a + kk * 8, x + ((kk >> 2) * NTOK * 128 + (kk & 3) * 32) / 16, idesc, j > 0);
-          }
-          for (int j = 0; j < ksteps; ++j) {
-            const int kk = g * ksteps + j;
-            umma_ts(d + NTOK, tmem + kOnesCol, x + ((kk >> 2) * NTOK * 128 + (kk & 3) * 32) / 16, idesc, j > 0);
+          const uint32_t d = tmem + slot * (C::kTogether * NTOK), at = tmem + kACol + 64 * a;
+#pragma unroll
+          for (int j = 0; j < C::kTogether * kSteps; ++j) {
+            const int step = r * C::kTogether * kSteps + j, in = step % (kHalfK / 16);  // 16 k each: of the unit, of the half
+            umma_ts(d + j / kSteps * NTOK, at + in * 8, x + ((step >> 2) * C::kXBox + (step & 3) * 32) / 16, idesc, j % kSteps > 0);
           }
           umma_commit(smem_u32(&ctl.dfull[slot]));
+          if (++slot == C::kSlots) slot = 0, dph ^= 1u;
+          if (r % kHalfReads == kHalfReads - 1) {
+            umma_commit(smem_u32(&ctl.aempty[a]));
+            if (++a == kABuffers) a = 0, aph ^= 1u;
+          }
         }
         if (!ok) break;
-        umma_commit(smem_u32(&ctl.aempty[b]));
         if (p.fault != 1) umma_commit(smem_u32(&ctl.empty[s]));
+        if (++s == C::kStages) s = 0;
       }
       umma_commit(smem_u32(&ctl.drain));
       uint32_t never = 0;
       mbar_wait(smem_u32(&ctl.drain), 0, &never, p.status, kDevTimeoutDrain);
     }
-  } else if (warp >= kEpiWarps) {
-    // ------------------------------------------------------------ expansion: a warpgroup takes every other unit
-    const Magic magic;
-    const uint32_t g = (warp - kEpiWarps) / 4, row = (warp & 3) * 32 + lane;
-    const uint32_t at = row * 64, swz = (row >> 1) & 3;  // 64-byte rows, 16-byte pieces swizzled
+  } else if (warp >= kFirstSum) {
+    // ------------------------------------------------------------ sums of X: a warp takes every other eight rows
+    constexpr int kTiles = NTOK / 8 / kSumWarps;
+    const int w = warp - kFirstSum, r8 = lane & 7, piece = lane >> 3;
+    uint32_t s = 0, ph = 0;
     pdl_wait();
-    for (uint32_t i = g; i < n; i += kExpandGroups) {
-      const uint32_t s = i % C::kStages;
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), (i / C::kStages) & 1u, abort, p.status, kDevTimeoutMma))) break;
+    for (uint32_t i = 0; i < n; ++i) {
+      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), ph, abort, p.status, kDevTimeoutMma))) break;
+      const uint32_t x = ring + s * C::kStage + kCodeBytes + r8 * 128, out = sum_ring + s * C::kSumBytes + lane * 8;
+      float c[kTiles][4];
+#pragma unroll
+      for (int step = 0; step < kUnitK / 32; ++step) {  // 32 k
+        if (step % (GROUP / 32) == 0) {
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) c[t][0] = c[t][1] = c[t][2] = c[t][3] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          uint32_t b[4];
+          ldmatrix_x4(x + (step >> 1) * C::kXBox + (t * kSumWarps + w) * 1024 + ((((step & 1) * 4 + piece) ^ r8) << 4), b);
+          mma_ones(c[t], b[0], b[1]);
+          mma_ones(c[t], b[2], b[3]);
+        }
+        if (step % (GROUP / 32) == GROUP / 32 - 1 && lane < 4) {  // rows of the product are alike
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t)
+            asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(out + (step / (GROUP / 32) * NTOK + (t * kSumWarps + w) * 8) * 4),
+                         "f"(c[t][0]), "f"(c[t][1])
+                         : "memory");
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.sums[s]));
+      if (++s == C::kStages) s = 0, ph ^= 1u;
+    }
+  } else if (warp >= kEpiWarps) {
+    // ------------------------------------------------------------ expansion
+    const Magic magic;
+    const uint32_t half = (warp - kEpiWarps) / 4, row = (warp & 3) * 32 + lane, swz = row & 7;  // 128-byte rows, 16-byte pieces swizzled
+    uint32_t s = 0, ph = 0, a = half, aph = 1;
+    pdl_wait();
+    for (uint32_t i = 0; i < n; ++i) {
+      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), ph, abort, p.status, kDevTimeoutMma))) break;
       uint32_t v[2][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint4 w = lds128(ring + s * C::kStage + at + ((c ^ swz) << 4));
+        const uint4 w = lds128(ring + s * C::kStage + row * 128 + (((half * 4 + c) ^ swz) << 4));
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -389,21 +423,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
           to[3] = magic.pair(ws[j] >> 9);
         }
       }
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.aempty[g]), ((i / kExpandGroups) & 1u) ^ 1u, abort, p.status, kDevTimeoutMma))) break;
+      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.aempty[a]), aph, abort, p.status, kDevTimeoutMma))) break;
       tc_fence_after();
-      tmem_st_x32(tl + kACol + 64 * g, v[0]);
-      tmem_st_x32(tl + kACol + 64 * g + 32, v[1]);
+      tmem_st_x32(tl + kACol + 64 * a, v[0]);
+      tmem_st_x32(tl + kACol + 64 * a + 32, v[1]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl.afull[g]));
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.afull[a]));
+      if (++s == C::kStages) s = 0, ph ^= 1u;
+      if ((a += 2) >= kABuffers) a = half, aph ^= 1u;
     }
   } else {
-    // ------------------------------------------------------------ groups' sums, and the tiles' join: a thread per column
+    // ------------------------------------------------------------ groups' sums, and the tiles' join
     const int col = warp * 32 + lane;
     uint32_t* counters = static_cast<uint32_t*>(p.ws);
     float4* parts = reinterpret_cast<float4*>(static_cast<uint8_t*>(p.ws) + kCounterBytes);
-    uint32_t i = 0, count = 0;
+    uint32_t i = 0, s = 0, ph = 0, slot = 0, dph = 0;
     pdl_wait();
     while (i < n) {
       const uint32_t tile = (u0 + i) / kb, first = tile * kb, k0 = u0 + i - first, units = min(kb - k0, n - i);
@@ -412,46 +448,51 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
       for (int t = 0; t < NTOK; ++t) acc[t] = 0.f;
       bool ok = true;
       for (const uint32_t to = i + units; ok && i < to; ++i) {
-        const uint32_t s = i % C::kStages;
-        ok = __all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), (i / C::kStages) & 1u, abort, p.status, kDevTimeoutEpilogue));
-        for (int g = 0; ok && g < groups; ++g, ++count) {
-          const uint32_t slot = count % C::kSlots, d = tl + slot * 2 * NTOK;
-          const uint32_t prm = lds32(ring + s * C::kStage + kCodeBytes + C::kXBytes + g * 512 + col * 4);
-          const float scale = lo_of(prm), zero = fmaf(-16.f, scale, hi_of(prm));
-          ok = __all_sync(~0u, mbar_wait(smem_u32(&ctl.dfull[slot]), (count / C::kSlots) & 1u, abort, p.status, kDevTimeoutEpilogue));
+        // (The sums' barrier follows the stage's: parameters are there too.)
+        ok = __all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), ph, abort, p.status, kDevTimeoutEpilogue) &&
+                                 mbar_wait(smem_u32(&ctl.sums[s]), ph, abort, p.status, kDevTimeoutEpilogue));
+#pragma unroll
+        for (int r = 0; r < C::kReads; ++r) {
+          ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&ctl.dfull[slot]), dph, abort, p.status, kDevTimeoutEpilogue));
           if (!ok) break;
           tc_fence_after();
-          constexpr int kAtOnce = NTOK < 32 ? NTOK : 32;
+          constexpr int kCols = C::kTogether * NTOK, kAtOnce = kCols < 32 ? kCols : 32;
+          const uint32_t d = tl + slot * kCols;
 #pragma unroll
-          for (int c = 0; c < NTOK; c += kAtOnce) {
-            uint32_t dv[kAtOnce], sv[kAtOnce];
-            if constexpr (kAtOnce == 16) {
-              tmem_ld_32x32b_x16(d + c, dv);
-              tmem_ld_32x32b_x16(d + NTOK + c, sv);
-            } else {
-              tmem_ld_32x32b_x32(d + c, dv);
-              tmem_ld_32x32b_x32(d + NTOK + c, sv);
-            }
+          for (int c = 0; c < kCols; c += kAtOnce) {
+            uint32_t dv[kAtOnce];
+            if constexpr (kAtOnce == 16) tmem_ld_32x32b_x16(d + c, dv);
+            else tmem_ld_32x32b_x32(d + c, dv);
             tmem_ld_wait();
-            if (c + kAtOnce == NTOK) {
+            if (c + kAtOnce == kCols) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(smem_u32(&ctl.dempty[slot]));
             }
 #pragma unroll
-            for (int t = 0; t < kAtOnce; ++t)
-              acc[c + t] = fmaf(scale, __uint_as_float(dv[t]), fmaf(zero, __uint_as_float(sv[t]), acc[c + t]));
+            for (int t = 0; t < kAtOnce; t += 4) {
+              const int g = r * C::kTogether + (c + t) / NTOK, tok = (c + t) % NTOK;
+              const uint32_t prm = lds32(ring + s * C::kStage + kCodeBytes + C::kXBytes + g * 512 + col * 4);
+              const float scale = lo_of(prm), zero = fmaf(-16.f, scale, hi_of(prm));
+              const uint4 x = lds128(sum_ring + s * C::kSumBytes + (g * NTOK + tok) * 4);
+              acc[tok] = fmaf(scale, __uint_as_float(dv[t]), fmaf(zero, __uint_as_float(x.x), acc[tok]));
+              acc[tok + 1] = fmaf(scale, __uint_as_float(dv[t + 1]), fmaf(zero, __uint_as_float(x.y), acc[tok + 1]));
+              acc[tok + 2] = fmaf(scale, __uint_as_float(dv[t + 2]), fmaf(zero, __uint_as_float(x.z), acc[tok + 2]));
+              acc[tok + 3] = fmaf(scale, __uint_as_float(dv[t + 3]), fmaf(zero, __uint_as_float(x.w), acc[tok + 3]));
+            }
           }
+          if (++slot == C::kSlots) slot = 0, dph ^= 1u;
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(smem_u32(&ctl.empty[s]));
+        if (++s == C::kStages) s = 0, ph ^= 1u;
       }
       // One decision of the four warps, so that none is left alone in a barrier.
       if (!ok) *abort = 1;
       epi_bar();
-      if (threadIdx.x == 0) ctl.is_last = *abort ? 2u : 0u;
+      if (threadIdx.x == 0) ctl.verdict = *abort;
       epi_bar();
-      if (ctl.is_last == 2u) break;
+      if (ctl.verdict) break;
       const int64_t m0 = static_cast<int64_t>(tile % blocks) * NTOK, c0 = static_cast<int64_t>(tile / blocks) * 128 + col;
       const int m = static_cast<int>(p.M - m0 < NTOK ? p.M - m0 : NTOK), nq = (m + 3) / 4;
       bool write = units == kb;
@@ -470,10 +511,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
         if (threadIdx.x == 0) {
           const bool last = take_ticket(counters + lo) == hi - lo;
           if (last) counters[lo] = 0;  // all tickets are taken: ready for the next call
-          ctl.is_last = last;
+          ctl.verdict = last;
         }
         epi_bar();
-        write = ctl.is_last != 0;
+        write = ctl.verdict != 0;
         if (write) {
 #pragma unroll
           for (int t = 0; t < NTOK; ++t) acc[t] = 0.f;
@@ -512,7 +553,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
             if (t < m) to[t * p.ldc] = __float2bfloat16_rn(acc[t]);
         }
       }
-      epi_bar();  // is_last is written again only after all have read it
+      epi_bar();  // verdict is written again only after all have read it
     }
   }
 
@@ -520,7 +561,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
   __syncthreads();
   if (ctl.abort && warp == kProducer && lane == 0) {
     // Some wait ran out: the copies in flight land before the CTA ends.
-    const uint32_t issued = ctl.ok;
+    const uint32_t issued = ctl.issued;
     uint32_t never = 0;
     for (uint32_t j = issued > C::kStages ? issued - C::kStages : 0u; j < issued; ++j)
       mbar_wait(smem_u32(&ctl.full[j % C::kStages]), (j / C::kStages) & 1u, &never, p.status, kDevTimeoutDrain);
@@ -531,21 +572,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
   }
 }
 
-template <int NTOK>
-cudaError_t launch_ntok(const W4GemmParams& p, int sms, cudaStream_t s) {
-  using C = Cfg<NTOK>;
+template <int NTOK, int GROUP>
+cudaError_t launch_variant(const W4GemmParams& p, int sms, cudaStream_t s) {
+  using C = Cfg<NTOK, GROUP>;
   Maps m;
   // A single row has no stride of its own.
   const int64_t words = (p.K + 7) / 8, ldq = p.N > 1 ? p.ldq : (4 * words + 15) / 16 * 16, ldx = p.M > 1 ? p.ldx : (p.K + 7) / 8 * 8;
-  const int64_t groups = (p.K + p.group - 1) / p.group, ldp = groups > 1 ? p.ldp : (p.N + 3) / 4 * 4;
+  const int64_t groups = (p.K + GROUP - 1) / GROUP, ldp = groups > 1 ? p.ldp : (p.N + 3) / 4 * 4;
   if (!make_tile_map(&m.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.Q, 4 * words, p.N, ldq, 1, 0, kUnitK / 2, 128,
-                     CU_TENSOR_MAP_SWIZZLE_64B, 1) ||
+                     CU_TENSOR_MAP_SWIZZLE_128B, 1) ||
       !make_tile_map(&m.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.X, p.K, p.M, ldx, 1, 0, 64, NTOK, CU_TENSOR_MAP_SWIZZLE_128B, 1) ||
-      !make_tile_map(&m.params, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.params, p.N, groups, ldp, 1, 0, 128, kUnitK / p.group,
+      !make_tile_map(&m.params, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, p.params, p.N, groups, ldp, 1, 0, 128, C::kGroups,
                      CU_TENSOR_MAP_SWIZZLE_NONE, 1))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> attr_done{0};
-  const cudaError_t e = ensure_smem_attr(gemm_w4_kernel<NTOK>, C::kSmem, attr_done);
+  const cudaError_t e = ensure_smem_attr(gemm_w4_kernel<NTOK, GROUP>, C::kSmem, attr_done);
   if (e != cudaSuccess) return e;
   const int64_t units = (p.N + 127) / 128 * ((p.M + NTOK - 1) / NTOK) * ((p.K + kUnitK - 1) / kUnitK);
   int64_t ctas = (units + kMinUnits - 1) / kMinUnits;
@@ -553,7 +594,14 @@ cudaError_t launch_ntok(const W4GemmParams& p, int sms, cudaStream_t s) {
   if (ctas > kMaxCtas) ctas = kMaxCtas;
   W4GemmParams q = p;
   q.fault = g_fault_injection;
-  return launch_pdl(gemm_w4_kernel<NTOK>, dim3(static_cast<unsigned>(ctas)), dim3(kGemmThreads), C::kSmem, s, m, q);
+  return launch_pdl(gemm_w4_kernel<NTOK, GROUP>, dim3(static_cast<unsigned>(ctas)), dim3(kGemmThreads), C::kSmem, s, m, q);
+}
+
+template <int NTOK>
+cudaError_t launch_ntok(const W4GemmParams& p, int sms, cudaStream_t s) {
+  return p.group == 32   ? launch_variant<NTOK, 32>(p, sms, s)
+         : p.group == 64 ? launch_variant<NTOK, 64>(p, sms, s)
+                         : launch_variant<NTOK, 128>(p, sms, s);
 }
 
 int ntok_of(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
