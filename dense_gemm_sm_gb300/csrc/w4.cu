@@ -201,13 +201,30 @@ __device__ __forceinline__ uint32_t take_ticket(uint32_t* a) {
 }
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] B[smem]: row m of A in lane m, two BF16 of k per 32-bit column, low half first.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p;
+}
+// D[tmem] (+)= A[tmem] B[smem]: row m of A in lane m, two BF16 of k per 32-bit column, low half first.  The
+// whole warp comes here and its elected lane issues: operands are then uniform over a converged warp, and an
+// MMA takes 10 cycles to issue where a branch of one lane took 45 (128 x 16 x 16, one after the other).
+template <bool ACCUMULATE>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "n"(ACCUMULATE ? 1 : 0), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 
@@ -267,7 +284,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
   __shared__ Control ctl;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u, sum_ring = ring + C::kStages * C::kStage;
   volatile uint32_t* abort = &ctl.abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform to the compiler too)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -295,7 +312,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem_base;
+  const uint32_t tmem = __shfl_sync(~0u, ctl.tmem_base, 0);
   const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's lanes
 
   const uint32_t kb = static_cast<uint32_t>((p.K + kUnitK - 1) / kUnitK);
@@ -329,43 +346,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
     if (lane == 0) ctl.issued = i;
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, NTOK, false, false);
-      const uint64_t x0 = sdesc_sw128(ring + kCodeBytes, 16, 1024);
-      uint32_t s = 0, slot = 0, dph = 1, a = 0, aph = 0;
-      bool ok = true;
-      pdl_wait();  // bounded waits start when this grid's data can arrive
-      for (uint32_t i = 0; i < n; ++i) {
-        const uint64_t x = x0 + s * (C::kStage >> 4);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, NTOK, false, false);
+    const uint64_t x0 = sdesc_sw128(ring + kCodeBytes, 16, 1024);
+    const uint32_t lead = elect();
+    uint32_t s = 0, slot = 0, dph = 1, a = 0, aph = 0;
+    bool ok = true;
+    pdl_wait();  // bounded waits start when this grid's data can arrive
+    for (uint32_t i = 0; i < n; ++i) {
+      const uint64_t x = x0 + s * (C::kStage >> 4);
 #pragma unroll
-        for (int r = 0; r < C::kReads; ++r) {
-          constexpr int kSteps = GROUP / 16, kHalfReads = C::kReads / 2;
-          // (The warps that expanded the half have seen its stage filled.)
-          if (r % kHalfReads == 0) ok = ok && mbar_wait(smem_u32(&ctl.afull[a]), aph, abort, p.status, kDevTimeoutMma);
-          ok = ok && mbar_wait(smem_u32(&ctl.dempty[slot]), dph, abort, p.status, kDevTimeoutMma);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + slot * (C::kTogether * NTOK), at = tmem + kACol + 64 * a;
-#pragma unroll
-          for (int j = 0; j < C::kTogether * kSteps; ++j) {
-            const int step = r * C::kTogether * kSteps + j, in = step % (kHalfK / 16);  // 16 k each: of the unit, of the half
-            umma_ts(d + j / kSteps * NTOK, at + in * 8, x + ((step >> 2) * C::kXBox + (step & 3) * 32) / 16, idesc, j % kSteps > 0);
-          }
-          umma_commit(smem_u32(&ctl.dfull[slot]));
-          if (++slot == C::kSlots) slot = 0, dph ^= 1u;
-          if (r % kHalfReads == kHalfReads - 1) {
-            umma_commit(smem_u32(&ctl.aempty[a]));
-            if (++a == kABuffers) a = 0, aph ^= 1u;
-          }
-        }
+      for (int r = 0; r < C::kReads; ++r) {
+        constexpr int kSteps = GROUP / 16, kHalfReads = C::kReads / 2;
+        // (The warps that expanded the half have seen its stage filled.)
+        if (r % kHalfReads == 0) ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&ctl.afull[a]), aph, abort, p.status, kDevTimeoutMma));
+        ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&ctl.dempty[slot]), dph, abort, p.status, kDevTimeoutMma));
         if (!ok) break;
-        if (p.fault != 1) umma_commit(smem_u32(&ctl.empty[s]));
-        if (++s == C::kStages) s = 0;
+        tc_fence_after();
+        const uint32_t d = tmem + slot * (C::kTogether * NTOK), at = tmem + kACol + 64 * a;
+#pragma unroll
+        for (int j = 0; j < C::kTogether * kSteps; ++j) {
+          const int step = r * C::kTogether * kSteps + j, in = step % (kHalfK / 16);  // 16 k each: of the unit, of the half
+          const uint64_t b = x + ((step >> 2) * C::kXBox + (step & 3) * 32) / 16;
+          if (j % kSteps == 0) umma_ts<false>(d + j / kSteps * NTOK, at + in * 8, b, idesc, lead);
+          else umma_ts<true>(d + j / kSteps * NTOK, at + in * 8, b, idesc, lead);
+        }
+        commit(&ctl.dfull[slot], lead);
+        if (++slot == C::kSlots) slot = 0, dph ^= 1u;
+        if (r % kHalfReads == kHalfReads - 1) {
+          commit(&ctl.aempty[a], lead);
+          if (++a == kABuffers) a = 0, aph ^= 1u;
+        }
       }
-      umma_commit(smem_u32(&ctl.drain));
-      uint32_t never = 0;
-      mbar_wait(smem_u32(&ctl.drain), 0, &never, p.status, kDevTimeoutDrain);
+      if (!ok) break;
+      if (p.fault != 1) commit(&ctl.empty[s], lead);
+      if (++s == C::kStages) s = 0;
     }
+    commit(&ctl.drain, lead);
+    uint32_t never = 0;
+    mbar_wait(smem_u32(&ctl.drain), 0, &never, p.status, kDevTimeoutDrain);
+    __syncwarp();
   } else if (warp >= kFirstSum) {
     // ------------------------------------------------------------ sums of X: a warp takes every other eight rows
     constexpr int kTiles = NTOK / 8 / kSumWarps;
