@@ -235,79 +235,96 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const Kv4Params p,
 }
 
 // ------------------------------------------------------------------ accepted drafted tokens
-// A CTA per sequence, so that lengths may be updated in place and every row is read before one is
-// written; a warp takes a head at a time and holds its rows in shared memory in between: of a row,
-// lane l has two bytes of K's codes and one of the d / 4 pieces of V's, lanes 0 and 1 the parameters.
-constexpr int kMaxTree = 64;
+// A cluster per sequence, so that lengths may be updated in place; its CTAs take a head at a time, in whose
+// registers all of the head's rows are before one is written: a warp has every eighth row, lane l two
+// bytes of K's codes and one of the d / 4 pieces of V's, lanes 0 and 1 the parameters.  Latency bounds
+// it, so that a head's loads are all in flight (128 sequences of up to 64 rows, 8 heads: 40 us with one row at a
+// time and all heads in a CTA, 20 with eight rows).
+constexpr int kMaxTree = 64, kAcceptWarps = 8, kRowsOfWarp = kMaxTree / kAcceptWarps, kMaxAcceptCluster = 8;
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_accept_kernel(const Kv4AcceptParams p) {
-  __shared__ int64_t from[kMaxTree], to[kMaxTree];  // byte offsets of records, for head 0; from < 0: not moved
+__global__ void __launch_bounds__(32 * kAcceptWarps) kv4_accept_kernel(const Kv4AcceptParams p, const int ranks) {
+  __shared__ int64_t from[kMaxTree], to[kMaxTree];  // byte offsets of records, for head 0
   __shared__ int8_t from_u[kMaxTree], to_u[kMaxTree];
-  __shared__ uint32_t rows[kThreads / 32][kMaxTree][34];
+  __shared__ int moved;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t b = blockIdx.x, cap = p.ldt * p.page_size;
+  const int rank = static_cast<int>(blockIdx.x) % ranks;
+  const int64_t b = blockIdx.x / ranks, cap = p.ldt * p.page_size;
   const int64_t stride = static_cast<int64_t>(p.page_size / kKv4Tokens) * kv4_record_bytes(D);
   const int32_t len = p.lens[b], nodes = p.nodes ? p.nodes[b] : p.Lq, count = p.counts[b];
   const bool good = len >= 0 && len <= cap && nodes >= 0 && nodes <= p.Lq && nodes <= len && count >= 0 && count <= nodes;
-  if (!good) {
-    if (tid == 0) {
-      atomicCAS(p.index_word, 0u, kDevBadIndex);
-      p.new_lens[b] = len;
-    }
-    return;
-  }
   const int32_t base = len - nodes;
+  if (tid == 0) moved = 0;
+  cluster_sync();  // (of all threads) the length is read before it is written, where new_lens is lens
+  if (tid == 0 && rank == 0) {
+    p.new_lens[b] = good ? base + count : len;
+    if (!good) atomicCAS(p.index_word, 0u, kDevBadIndex);
+  }
+  if (!good) return;
   if (tid < count) {
     const int32_t node = p.path[b * p.ldp + tid];
-    from[tid] = -1;
     if (node < 0 || node >= nodes) {
       atomicCAS(p.index_word, 0u, kDevBadIndex);
     } else if (node != tid) {
       int64_t at[2];
+      int in[2];
       bool have = true;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int32_t token = base + (i ? tid : node), in = token % p.page_size;
+        const int32_t token = base + (i ? tid : node);
         const int32_t page = p.table[b * p.ldt + token / p.page_size];
+        in[i] = token % p.page_size;
         have = have && page >= 0 && page < p.pages;
-        at[i] = page * (p.heads * stride) + (in >> 4) * kv4_record_bytes(D);
-        (i ? to_u : from_u)[tid] = static_cast<int8_t>(in & 15);
+        at[i] = page * (p.heads * stride) + (in[i] >> 4) * kv4_record_bytes(D);
       }
       if (have) {
-        from[tid] = at[0];
-        to[tid] = at[1];
+        const int k = atomicAdd(&moved, 1);  // in any order: places to write are distinct
+        from[k] = at[0];
+        to[k] = at[1];
+        from_u[k] = static_cast<int8_t>(in[0] & 15);
+        to_u[k] = static_cast<int8_t>(in[1] & 15);
       } else {
         atomicCAS(p.index_word, 0u, kDevBadIndex);
       }
     }
   }
-  __syncthreads();  // also: the length is read before it is written, where new_lens is lens
-  if (tid == 0) p.new_lens[b] = base + count;
-  for (int h = warp; h < p.heads; h += kThreads / 32) {
-    for (int k = 0; k < count; ++k) {
-      if (from[k] < 0) continue;
-      const uint8_t* rec = p.data + from[k] + h * stride;
+  __syncthreads();
+  const int n = moved;
+  for (int h = rank; h < p.heads; h += ranks) {
+    uint16_t kw[kRowsOfWarp], vw[kRowsOfWarp];
+    uint32_t pw[kRowsOfWarp];
+#pragma unroll
+    for (int x = 0; x < kRowsOfWarp; ++x) {
+      const int k = warp + x * kAcceptWarps;
+      if (k >= n) continue;
       const int u = from_u[k];
-      if (lane < D / 4)
-        rows[warp][k][lane] = *reinterpret_cast<const uint16_t*>(rec + u * (D / 2) + 2 * lane) |
-                              static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(rec + 8 * D + v_piece<D>(u, lane))) << 16;
-      if (lane < 2) rows[warp][k][32 + lane] = *reinterpret_cast<const uint32_t*>(rec + 16 * D + 64 * lane + u * 4);
-    }
-    __syncwarp();
-    for (int k = 0; k < count; ++k) {
-      if (from[k] < 0) continue;
-      uint8_t* rec = p.data + to[k] + h * stride;
-      const int u = to_u[k];
+      const uint8_t* rec = p.data + from[k] + h * stride;
       if (lane < D / 4) {
-        const uint32_t w = rows[warp][k][lane];
-        *reinterpret_cast<uint16_t*>(rec + u * (D / 2) + 2 * lane) = static_cast<uint16_t>(w);
-        *reinterpret_cast<uint16_t*>(rec + 8 * D + v_piece<D>(u, lane)) = static_cast<uint16_t>(w >> 16);
+        kw[x] = *reinterpret_cast<const uint16_t*>(rec + u * (D / 2) + 2 * lane);
+        vw[x] = *reinterpret_cast<const uint16_t*>(rec + 8 * D + v_piece<D>(u, lane));
       }
-      if (lane < 2) *reinterpret_cast<uint32_t*>(rec + 16 * D + 64 * lane + u * 4) = rows[warp][k][32 + lane];
+      if (lane < 2) pw[x] = *reinterpret_cast<const uint32_t*>(rec + 16 * D + 64 * lane + u * 4);
     }
-    __syncwarp();
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kRowsOfWarp; ++x) {
+      const int k = warp + x * kAcceptWarps;
+      if (k >= n) continue;
+      const int u = to_u[k];
+      uint8_t* rec = p.data + to[k] + h * stride;
+      if (lane < D / 4) {
+        *reinterpret_cast<uint16_t*>(rec + u * (D / 2) + 2 * lane) = kw[x];
+        *reinterpret_cast<uint16_t*>(rec + 8 * D + v_piece<D>(u, lane)) = vw[x];
+      }
+      if (lane < 2) *reinterpret_cast<uint32_t*>(rec + 16 * D + 64 * lane + u * 4) = pw[x];
+    }
   }
 }
 
@@ -383,9 +400,27 @@ cudaError_t launch_kv4_gather(const Kv4Params& p, int d, bool vec, int sms, cuda
 }
 #undef DG_KV4_LAUNCH
 
+template <int D>
+cudaError_t launch_accept(const Kv4AcceptParams& p, cudaStream_t s) {
+  unsigned cluster = 1;
+  while (cluster < kMaxAcceptCluster && static_cast<int>(2 * cluster) <= p.heads) cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster * static_cast<unsigned>(p.batch));
+  cfg.blockDim = dim3(32 * kAcceptWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kv4_accept_kernel<D>, p, static_cast<int>(cluster));
+}
+
 cudaError_t launch_kv4_accept(const Kv4AcceptParams& p, int d, cudaStream_t s) {
-  const dim3 g(static_cast<unsigned>(p.batch)), b(kThreads);
-  return d == 128 ? launch_pdl(kv4_accept_kernel<128>, g, b, 0, s, p) : launch_pdl(kv4_accept_kernel<64>, g, b, 0, s, p);
+  return d == 128 ? launch_accept<128>(p, s) : launch_accept<64>(p, s);
 }
 
 cudaError_t launch_kv4_copy_pages(const Kv4CopyParams& p, int sms, cudaStream_t s) {

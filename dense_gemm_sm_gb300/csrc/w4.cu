@@ -33,97 +33,162 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ constexpr int code_at(int k) { return 4 * (k >> 1) + 16 * (k & 1); }
 
 // ------------------------------------------------------------------ rows
-// A lane holds 8 elements, one word of codes; G / 8 neighbouring lanes hold a group, so that a warp
-// reads 512 contiguous bytes and writes 128.
-template <int G, bool VEC>
-__global__ void __launch_bounds__(kThreads) quantize_w4_kernel(const W4RowsParams p) {
+// HBM-bound: 2 bytes of W, half a byte of codes and 4 / group of parameters an element.  A warp takes 1024 k of
+// a row, its four loads together (256 k where those would not fill the GPU's warps twice); a lane holds 8 elements of each, one word of codes, and group / 8
+// neighbouring lanes a group.  Neighbouring warps take neighbouring rows, whose parameters lie together.
+// Minimum and maximum are reduced as one BF16 pair (maximum, -minimum), quotients come from a reciprocal,
+// correctly rounded by one step with their exact remainder, codes are put together from the low bits of
+// 1.5 * 2^23 + code.
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// a / b rounded to nearest, for y = 1 / b rounded to nearest: the quotient's approximation a y
+// corrected by its remainder, which is exact (P. Markstein, "Computation of elementary functions
+// on the IBM RISC System/6000 processor", 1990: right unless all bits of b's significand are set;
+// no intermediate result may underflow).
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+  const float q = a * y;
+  return fmaf(fmaf(-q, b, a), y, q);
+}
+
+// A warp's piece: row, first word.
+struct Piece {
+  int64_t n, w;
+  __device__ __forceinline__ Piece(int64_t i, int64_t rows, int words) {
+    const int64_t block = static_cast<uint64_t>(i) >> 32 || static_cast<uint64_t>(rows) >> 32
+                              ? i / rows
+                              : static_cast<uint32_t>(i) / static_cast<uint32_t>(rows);
+    n = i - block * rows;
+    w = block * words;
+  }
+};
+
+template <int G, bool VEC, int X>
+__global__ void __launch_bounds__(kThreads) quantize_w4_kernel(const W4RowsParams p, const int64_t pieces) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t words = (p.K + 7) / 8, per_row = (words + 31) / 32;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); i < p.N * per_row; i += warps) {
-    const int64_t n = i / per_row, w = (i - n * per_row) * 32 + lane;
-    const uint16_t* src = p.W + n * p.ldw + 8 * w;
-    const int64_t left = p.K - 8 * w;  // elements of this word: 8, fewer at the row's end, none past it
-    uint32_t v[4];
-    if (VEC && left >= 8) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(src));
-      v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    } else {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); i < pieces; i += warps) {
+    const Piece at(i, p.N, 32 * X);
+    const uint16_t* src = p.W + at.n * p.ldw + 8 * (at.w + lane);
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.Q + at.n * p.ldq) + at.w + lane;
+    uint32_t* prm = p.params + at.n + (8 * (at.w + lane) / G) * p.ldp;
+    // Elements from this lane's first word on: 8 or more of them for a whole word, none past the row's end.
+    const int64_t rest = p.K - 8 * (at.w + lane);
+    uint32_t v[X][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t a = 2 * j < left ? src[2 * j] : 0, b = 2 * j + 1 < left ? src[2 * j + 1] : 0;
-        v[j] = a | b << 16;
+    for (int x = 0; x < X; ++x) {
+      const int64_t left = rest - 256 * x;
+      if (VEC && left >= 8) {
+        const uint4 q = __ldcs(reinterpret_cast<const uint4*>(src + 256 * x));
+        v[x][0] = q.x; v[x][1] = q.y; v[x][2] = q.z; v[x][3] = q.w;
+      } else {
+        // Past the row's end: its last element again, which changes no range.
+        const uint16_t* e = src + 256 * x;
+        const int last = left >= 8 ? 7 : static_cast<int>(left) - 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[x][j] = left <= 0 ? 0u : e[min(2 * j, last)] | static_cast<uint32_t>(e[min(2 * j + 1, last)]) << 16;
       }
     }
-    float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (2 * j < left) lo = fminf(lo, lo_of(v[j])), hi = fmaxf(hi, lo_of(v[j]));
-      if (2 * j + 1 < left) lo = fminf(lo, hi_of(v[j])), hi = fmaxf(hi, hi_of(v[j]));
-    }
+    for (int x = 0; x < X; ++x) {
+      const int64_t left = rest - 256 * x;
+      // (maximum, -minimum) of the lane's elements, then of the group; lanes past the end: -inf.
+      const uint32_t hi2 = max2(max2(v[x][0], v[x][1]), max2(v[x][2], v[x][3]));
+      const uint32_t lo2 = max2(max2(v[x][0] ^ 0x80008000u, v[x][1] ^ 0x80008000u), max2(v[x][2] ^ 0x80008000u, v[x][3] ^ 0x80008000u));
+      uint32_t ext = max2(__byte_perm(hi2, lo2, 0x5410), __byte_perm(hi2, lo2, 0x7632));
+      if (left <= 0) ext = 0xFF80FF80u;
 #pragma unroll
-    for (int o = G / 16; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
-    }
-    if (left <= 0) continue;
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-    const float scale = __bfloat162float(sb);
-    uint32_t codes = 0;
+      for (int o = G / 16; o > 0; o >>= 1) ext = max2(ext, __shfl_xor_sync(~0u, ext, o));
+      if (left <= 0) continue;
+      const float hi = lo_of(ext), lo = __uint_as_float((ext & 0xFFFF0000u) ^ 0x80000000u);
+      const float range = __fsub_rn(hi, lo);
+      const bool plain = range >= 1e-30f;  // nothing below underflows
+      const __nv_bfloat16 sb = __float2bfloat16_rn(plain ? quotient(range, 15.f, 1.f / 15.f) : __fdiv_rn(range, 15.f));
+      const float scale = __bfloat162float(sb);
+      uint32_t codes = 0;
+      if (plain) {
+        // A quotient is at most 15 (1 + 2^-8): rounded, at most 15.
+        const float inv = __frcp_rn(scale);
+        constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, in the low bits
+        uint32_t c[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = k & 1 ? hi_of(v[k >> 1]) : lo_of(v[k >> 1]);
-      const float q = scale > 0.f && k < left ? rintf(__fdiv_rn(__fsub_rn(x, lo), scale)) : 0.f;
-      codes |= static_cast<uint32_t>(fminf(fmaxf(q, 0.f), 15.f)) << code_at(k);
+        for (int k = 0; k < 8; ++k) {
+          const float e = k & 1 ? hi_of(v[x][k >> 1]) : lo_of(v[x][k >> 1]);
+          c[k] = __float_as_uint(quotient(__fsub_rn(e, lo), scale, inv) + kRound);
+        }
+        // The low half of a word is the code alone.
+        codes = __byte_perm(((c[6] * 16 + c[4]) * 16 + c[2]) * 16 + c[0], ((c[7] * 16 + c[5]) * 16 + c[3]) * 16 + c[1], 0x5410);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float e = k & 1 ? hi_of(v[x][k >> 1]) : lo_of(v[x][k >> 1]);
+          const float q = scale > 0.f ? rintf(__fdiv_rn(__fsub_rn(e, lo), scale)) : 0.f;
+          codes |= static_cast<uint32_t>(fminf(fmaxf(q, 0.f), 15.f)) << code_at(k);
+        }
+      }
+      if (left < 8) {  // codes past K are 0
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k >= left) codes &= ~(15u << code_at(k));
+      }
+      out[32 * x] = codes;
+      if (lane % (G / 8) == 0)
+        prm[256 / G * x * p.ldp] = static_cast<uint32_t>(__bfloat16_as_ushort(sb)) | (__float_as_uint(lo) & 0xFFFF0000u);
     }
-    reinterpret_cast<uint32_t*>(p.Q + n * p.ldq)[w] = codes;
-    if (lane % (G / 8) == 0)
-      p.params[8 * w / G * p.ldp + n] =
-          static_cast<uint32_t>(__bfloat16_as_ushort(sb)) | (__float_as_uint(lo) & 0xFFFF0000u);
   }
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) dequantize_w4_kernel(const W4RowsParams p, const int group_words) {
+template <int G, bool VEC, int X>
+__global__ void __launch_bounds__(kThreads) dequantize_w4_kernel(const W4RowsParams p, const int64_t pieces) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t words = (p.K + 7) / 8, per_row = (words + 31) / 32;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); i < p.N * per_row; i += warps) {
-    const int64_t n = i / per_row, w = (i - n * per_row) * 32 + lane;
-    if (w >= words) continue;
-    const uint32_t codes = reinterpret_cast<const uint32_t*>(p.Q + n * p.ldq)[w];
-    const uint32_t prm = p.params[w / group_words * p.ldp + n];
-    const float scale = lo_of(prm), zero = hi_of(prm);
-    uint32_t v[4];
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); i < pieces; i += warps) {
+    const Piece at(i, p.N, 32 * X);
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.Q + at.n * p.ldq) + at.w + lane;
+    const uint32_t* prm = p.params + at.n + (8 * (at.w + lane) / G) * p.ldp;
+    uint16_t* out = p.W + at.n * p.ldw + 8 * (at.w + lane);
+    const int64_t rest = p.K - 8 * (at.w + lane);
+    uint32_t codes[X], words[X];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // zero + scale * code: the product of 8 and 4 significant bits is exact in FP32.
-      const float a = fmaf(scale, static_cast<float>((codes >> (4 * j)) & 15u), zero);
-      const float b = fmaf(scale, static_cast<float>((codes >> (4 * j + 16)) & 15u), zero);
-      v[j] = pack2(a, b);
+    for (int x = 0; x < X; ++x) {
+      if (rest <= 256 * x) continue;
+      codes[x] = __ldg(src + 32 * x);
+      words[x] = __ldg(prm + 256 / G * x * p.ldp);
     }
-    uint16_t* dst = p.W + n * p.ldw + 8 * w;
-    const int64_t left = p.K - 8 * w;
-    if (VEC && left >= 8) {
-      *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
-    } else {
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      const int64_t left = rest - 256 * x;
+      if (left <= 0) continue;
+      const float scale = lo_of(words[x]), zero = hi_of(words[x]);
+      uint32_t v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (2 * j < left) dst[2 * j] = static_cast<uint16_t>(v[j]);
-        if (2 * j + 1 < left) dst[2 * j + 1] = static_cast<uint16_t>(v[j] >> 16);
+        // zero + scale * code: the product of 8 and 4 significant bits is exact in FP32.
+        const float a = fmaf(scale, static_cast<float>((codes[x] >> (4 * j)) & 15u), zero);
+        const float b = fmaf(scale, static_cast<float>((codes[x] >> (4 * j + 16)) & 15u), zero);
+        v[j] = pack2(a, b);
+      }
+      uint16_t* dst = out + 256 * x;
+      if (VEC && left >= 8) {
+        __stcs(reinterpret_cast<uint4*>(dst), make_uint4(v[0], v[1], v[2], v[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (2 * j < left) dst[2 * j] = static_cast<uint16_t>(v[j]);
+          if (2 * j + 1 < left) dst[2 * j + 1] = static_cast<uint16_t>(v[j] >> 16);
+        }
       }
     }
   }
-}
-
-dim3 rows_grid(const W4RowsParams& p, int sms) {
-  const int64_t need = (p.N * (((p.K + 7) / 8 + 31) / 32) + kThreads / 32 - 1) / (kThreads / 32);
-  const int64_t cap = static_cast<int64_t>(sms) * 8;
-  return dim3(static_cast<unsigned>(need < cap ? need : cap));
 }
 
 // ------------------------------------------------------------------ product
@@ -627,22 +692,27 @@ int ntok_of(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
 }  // namespace
 
-cudaError_t launch_quantize_w4(const W4RowsParams& p, int group, bool vec, int sms, cudaStream_t s) {
-  const dim3 g = rows_grid(p, sms), b(kThreads);
-#define DG_W4_CASE(G) \
-  if (group == G) return vec ? launch_pdl(quantize_w4_kernel<G, true>, g, b, 0, s, p) : launch_pdl(quantize_w4_kernel<G, false>, g, b, 0, s, p);
-  DG_W4_CASE(32)
-  DG_W4_CASE(64)
-  DG_W4_CASE(128)
-#undef DG_W4_CASE
+#define DG_W4_ROWS(KERNEL, G, VEC)                                                              \
+  if (group == G && vec == VEC)                                                                \
+    return big ? launch_pdl(KERNEL<G, VEC, 4>, g, b, 0, s, p, pieces) : launch_pdl(KERNEL<G, VEC, 1>, g, b, 0, s, p, pieces);
+#define DG_W4_ALL(KERNEL)                                                                      \
+  auto count = [&](int words) { return p.N * (((p.K + 7) / 8 + words - 1) / words); };         \
+  const bool big = count(128) >= static_cast<int64_t>(sms) * 128;                              \
+  const int64_t pieces = count(big ? 128 : 32), need = (pieces + kThreads / 32 - 1) / (kThreads / 32), cap = static_cast<int64_t>(sms) * 64; \
+  const dim3 g(static_cast<unsigned>(need < cap ? need : cap)), b(kThreads);                   \
+  DG_W4_ROWS(KERNEL, 32, true)                                                                 \
+  DG_W4_ROWS(KERNEL, 32, false)                                                                \
+  DG_W4_ROWS(KERNEL, 64, true)                                                                 \
+  DG_W4_ROWS(KERNEL, 64, false)                                                                \
+  DG_W4_ROWS(KERNEL, 128, true)                                                                \
+  DG_W4_ROWS(KERNEL, 128, false)                                                               \
   return cudaErrorInvalidValue;
-}
 
-cudaError_t launch_dequantize_w4(const W4RowsParams& p, int group, bool vec, int sms, cudaStream_t s) {
-  const dim3 g = rows_grid(p, sms), b(kThreads);
-  return vec ? launch_pdl(dequantize_w4_kernel<true>, g, b, 0, s, p, group / 8)
-             : launch_pdl(dequantize_w4_kernel<false>, g, b, 0, s, p, group / 8);
-}
+cudaError_t launch_quantize_w4(const W4RowsParams& p, int group, bool vec, int sms, cudaStream_t s) { DG_W4_ALL(quantize_w4_kernel) }
+
+cudaError_t launch_dequantize_w4(const W4RowsParams& p, int group, bool vec, int sms, cudaStream_t s) { DG_W4_ALL(dequantize_w4_kernel) }
+#undef DG_W4_ROWS
+#undef DG_W4_ALL
 
 int64_t gemm_w4_ws_bytes(int64_t M, int64_t N, int64_t K) {
   // Units are counted in 31 bits.
