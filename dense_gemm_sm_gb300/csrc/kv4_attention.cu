@@ -1124,7 +1124,10 @@ cudaError_t launch_rows(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) 
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) {
-  return p.mask ? launch_rows<true>(p, d, sms, s) : launch_rows<false>(p, d, sms, s);
+  if (!p.mask) return launch_rows<false>(p, d, sms, s);
+  // Trees of more than 16 query rows a cache head (which the workspace then has room for).
+  if (p.Lq * p.group > 16) return launch_kv4_tree(p, d, sms, s);
+  return launch_rows<true>(p, d, sms, s);
 }
 
 }  // namespace dg

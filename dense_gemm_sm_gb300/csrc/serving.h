@@ -103,6 +103,9 @@ struct Kv4AttnParams {
 };
 int64_t kv4_attention_ws_bytes(int64_t Lq, int64_t heads_q, int64_t heads_kv, int d);
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s);
+// Trees of more than 16 query rows a cache head.
+int64_t kv4_tree_ws_bytes(int d);
+cudaError_t launch_kv4_tree(const Kv4AttnParams& p, int d, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------------ mixture of experts
 struct MoeParams {
