@@ -44,7 +44,6 @@ constexpr float kSlack = 8.f;       // the reference follows the maximum only wh
 constexpr int64_t kCounterBytes = 1024;  // of kv4_attention.cu's kernel, left as they are
 // Tensor memory: S (two buffers), O and the column of sums of P, P.
 constexpr uint32_t kOCol = 256, kPCol = 448, kTmemCols = 512;
-constexpr int kJoinSlices = 8;
 
 template <int D>
 struct Cfg {
@@ -67,7 +66,7 @@ struct Cut {
 };
 
 struct Shared {
-  float a[2][kKeys], b[2][kKeys], vs[2][kKeys], vz[2][kKeys];  // of a unit's keys
+  alignas(16) float a[2][kKeys], b[2][kKeys], vs[2][kKeys], vz[2][kKeys];  // of a unit's keys
   uint32_t valid[2][kKeys / 32];
   float top[2][2][kRows];                                      // halves' maxima
   float l[2][kRows], z[2][kRows], q[2][kRows];
@@ -123,9 +122,7 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   return d;
 }
 __device__ __forceinline__ ulonglong2 lds_f4(const float* a) {  // four of them
-  ulonglong2 v;
-  asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(smem_u32(a)));
-  return v;
+  return *reinterpret_cast<const ulonglong2*>(a);
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -286,12 +283,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
   auto key_units = [](int32_t len) { return (len + kKeys - 1) / kKeys; };
   auto row_blocks = [&](int32_t nodes) { return (nodes * p.group + kRows - 1) / kRows; };
   if (warp == 0) {
+    // A lane takes a run of sequences, and keeps what it read of the first.
     const uint32_t per = (batch + 31) / 32, b_lo = min(lane * per, batch), b_hi = min(b_lo + per, batch);
+    int32_t len0 = 0, nodes0 = 0;
     uint32_t mine = 0;
     for (uint32_t b = b_lo; b < b_hi; ++b) {
-      const int32_t n = p.lens[b], m = p.nodes ? p.nodes[b] : 0;
+      const int32_t n = p.lens[b], m = p.nodes ? p.nodes[b] : static_cast<int32_t>(p.Lq);
       if (blockIdx.x == 0 && (n < 0 || n > cap || m < 0 || m > p.Lq)) atomicCAS(p.index_word, 0u, kDevBadIndex);
-      mine += key_units(len_of(b)) * row_blocks(nodes_of(b)) * p.heads;
+      const int32_t len = min(max(n, 0), cap), nodes = min(max(m, 0), static_cast<int32_t>(p.Lq));
+      if (b == b_lo) len0 = len, nodes0 = nodes;
+      mine += key_units(len) * row_blocks(nodes) * p.heads;
     }
     uint32_t incl = mine;
 #pragma unroll
@@ -308,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       if (lane == owner) {
         uint32_t at = incl - mine, b = b_lo;
         for (;; ++b) {
-          const int32_t len = len_of(b), nodes = nodes_of(b), units = key_units(len), blocks = row_blocks(nodes);
+          const int32_t len = b == b_lo ? len0 : len_of(b), nodes = b == b_lo ? nodes0 : nodes_of(b);
+          const int32_t units = key_units(len), blocks = row_blocks(nodes);
           const uint32_t n = units * blocks * p.heads;
           if (r < at + n) {
             const int32_t item = (r - at) / units;
@@ -319,12 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
         }
       }
     }
-  }
-  // ---- queries that see nothing
-  for (uint32_t b = blockIdx.x; b < batch; b += gridDim.x) {
-    const int32_t from = len_of(b) > 0 ? nodes_of(b) : 0, words = p.group * p.heads * (D / 8);  // of 16 bytes, a query
-    for (int i = tid; i < (static_cast<int32_t>(p.Lq) - from) * words; i += kThreads)
-      *reinterpret_cast<uint4*>(p.O + b * p.strideO + static_cast<int64_t>(from + i / words) * p.ldo + i % words * 8) = make_uint4(0, 0, 0, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -391,6 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       }
     }
     if (lane == 0) sh.issued = i;
+    // ---- queries that see nothing
+    for (uint32_t b = blockIdx.x; b < batch; b += gridDim.x) {
+      const int32_t from = len_of(b) > 0 ? nodes_of(b) : 0, words = p.group * p.heads * (D / 8);  // of 16 bytes, a query
+      for (int i = lane; i < (static_cast<int32_t>(p.Lq) - from) * words; i += 32)
+        *reinterpret_cast<uint4*>(p.O + b * p.strideO + static_cast<int64_t>(from + i / words) * p.ldo + i % words * 8) = make_uint4(0, 0, 0, 0);
+    }
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ products
     constexpr uint32_t idS = idesc_bf16_f32(128, kKeys, false, false), idO = idesc_bf16_f32(128, C::kN, false, false);
@@ -643,9 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
         // The reference moves for a maximum far above it, and to the first key's.
         const float move = top > -INFINITY && (fresh || top > kSlack) ? top : 0.f;
         const bool moves = __any_sync(~0u, move != 0.f);
+        const float r = fresh ? 1.f : ex2(-move);  // (the first key's may be far below 0, and there is nothing to scale)
         fresh = fresh && !(top > -INFINITY);
         if (moves) {
-          const float r = ex2(-move);
           l *= r;
           z *= r;
           ref += move;
@@ -681,7 +683,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
         tc_fence_after();
         tmem_st_x32(tl + kPCol + half * 32, pw);
         if (moves && x > 0) {  // this half's columns of O, and the sums of P
-          const float r = ex2(-move);
 #pragma unroll
           for (int c = 0; c < D / 2; c += 32) {
             uint32_t o[32];
@@ -788,45 +789,56 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
   }
 }
 
-// Joins the parts of the items that were cut, in CTA order: a block for a slice of the columns of the item that
-// CTA blockIdx.x of the other kernel is the first of, a thread per row.
+// Joins the parts of the items that were cut, in CTA order: a block for 16 columns of the item that
+// CTA blockIdx.x of the other kernel is the first of, a thread per row and four columns.
+constexpr int kJoinThreads = 4 * kRows;
 template <int D>
-__global__ void __launch_bounds__(kRows) kv4_tree_join_kernel(const Kv4AttnParams p, const Cut* cuts) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_tree_join_kernel(const Kv4AttnParams p, const Cut* cuts) {
   using C = Cfg<D>;
   pdl_trigger();
   pdl_wait();
   const Cut cut = cuts[blockIdx.x];
-  const int row = threadIdx.x;
+  const int row = threadIdx.x % kRows, col = blockIdx.y * (kJoinThreads / kRows) + threadIdx.x / kRows;  // float4
   if (!cut.valid || row >= cut.live) return;
   const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.ws) + kCounterBytes);
   auto part = [&](int k) { return parts + (2 * static_cast<int64_t>(k) + (k == cut.lo ? cut.slot : 0)) * C::kPart; };
-  constexpr int kCols = D / 4 / kJoinSlices;  // float4
+  constexpr int kAtOnce = 8;  // parts whose loads are in flight
   float top = -INFINITY;
-#pragma unroll 4
-  for (int k = cut.lo; k <= cut.hi; ++k) top = fmaxf(top, __ldcg(part(k) + kRows * D + row));
+#pragma unroll 1
+  for (int k = cut.lo; k <= cut.hi; k += kAtOnce) {
+    float m[kAtOnce];
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) m[x] = __ldcg(part(min(k + x, cut.hi)) + kRows * D + row);
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) top = fmaxf(top, m[x]);
+  }
   const float ref = top > -INFINITY ? top : 0.f;
   float l = 0.f;
-  float4 v[kCols];
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int k = cut.lo; k <= cut.hi; k += kAtOnce) {
+    float m[kAtOnce], n[kAtOnce];
+    float4 f[kAtOnce];
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = cut.lo; k <= cut.hi; ++k) {
-    const float* q = part(k);
-    const float w = ex2(__ldcg(q + kRows * D + row) - ref);
-    l = fmaf(w, __ldcg(q + kRows * D + kRows + row), l);
+    for (int x = 0; x < kAtOnce; ++x) {
+      const float* q = part(min(k + x, cut.hi));
+      m[x] = __ldcg(q + kRows * D + row);
+      n[x] = __ldcg(q + kRows * D + kRows + row);
+      f[x] = __ldcg(reinterpret_cast<const float4*>(q) + col * kRows + row);
+    }
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      const float4 f = __ldcg(reinterpret_cast<const float4*>(q) + (blockIdx.y * kCols + c) * kRows + row);
-      v[c] = make_float4(fmaf(w, f.x, v[c].x), fmaf(w, f.y, v[c].y), fmaf(w, f.z, v[c].z), fmaf(w, f.w, v[c].w));
+    for (int x = 0; x < kAtOnce; ++x) {
+      if (k + x > cut.hi) break;
+      const float w = ex2(m[x] - ref);
+      l = fmaf(w, n[x], l);
+      v = make_float4(fmaf(w, f[x].x, v.x), fmaf(w, f[x].y, v.y), fmaf(w, f[x].z, v.z), fmaf(w, f[x].w, v.w));
     }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int r = cut.row0 + row, i = r / p.group;
   uint16_t* out = p.O + static_cast<int64_t>(cut.b) * p.strideO + static_cast<int64_t>(i) * p.ldo +
-                  static_cast<int64_t>(cut.head * p.group + r - i * p.group) * D + blockIdx.y * (4 * kCols);
-#pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(pack2(v[c].x * inv, v[c].y * inv), pack2(v[c].z * inv, v[c].w * inv));
+                  static_cast<int64_t>(cut.head * p.group + r - i * p.group) * D + col * 4;
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
 }
 
 template <int D>
@@ -841,7 +853,7 @@ cudaError_t launch_d(const Kv4AttnParams& p, int sms, cudaStream_t s) {
   const unsigned ctas = static_cast<unsigned>(sms < kMaxCtas ? sms : kMaxCtas);
   e = launch_pdl(kv4_tree_kernel<D>, dim3(ctas), dim3(kThreads), C::kSmem, s, q, cuts);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_tree_join_kernel<D>, dim3(ctas, kJoinSlices), dim3(kRows), 0, s, q, static_cast<const Cut*>(cuts));
+  return launch_pdl(kv4_tree_join_kernel<D>, dim3(ctas, D / 4 / (kJoinThreads / kRows)), dim3(kJoinThreads), 0, s, q, static_cast<const Cut*>(cuts));
 }
 
 }  // namespace

@@ -152,6 +152,25 @@ def test_tree_strides_and_peaked_scores(torch):
     check(torch, [700], None, 33, 8, 1, 128, 64, std=30.0)
 
 
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("lq,ctx", [(3, 40), (40, 0), (40, 200), (64, 3000)])
+def test_tree_scores_far_from_zero(torch, lq, ctx, sign):
+    # All scores at about +-900 in units of log2; the context's first unit far below what follows.
+    rng = np.random.default_rng(ctx + lq)
+    n, heads, d, page_size = ctx + lq, 2, 128, 32
+    pool = ref.Kv4Pool(-(-n // page_size), page_size, heads, d)
+    k = np.ones((n, heads, d), np.float32) + 0.02 * rng.standard_normal((n, heads, d)).astype(np.float32)
+    k[:min(ctx, 128)] *= 1.5
+    pool.append(ref.bf16(k), rows(rng, (n, heads, d)), np.arange(n))
+    q = ref.bf16(sign * (30 + rng.standard_normal((1, lq, 8, d)))).astype(np.float64)
+    table, mask = np.arange(pool.pages)[None], trees(rng, 1, lq)
+    scale = float(np.float32(0.17))
+    got = attend(torch, pool, torch.from_numpy(pool.pack()).cuda(), table, [n], None, mask, q, scale)
+    sync(torch)
+    want, bound = oracle(pool, q, table, [n], scale, ref.tree_sees([n], [lq], mask))
+    assert np.isfinite(got).all() and np.all(np.abs(got - want) <= bound)
+
+
 @pytest.mark.parametrize("lens,lq,hq,heads,d", [([6000], 16, 8, 1, 128), ([9000, 0, 4000], 8, 8, 1, 64), ([5000, 300], 64, 8, 2, 128),
                                                ([2000] * 9, 30, 8, 2, 64)])
 def test_tree_long_contexts_in_one_workspace(torch, lens, lq, hq, heads, d):
