@@ -348,6 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
     } while (at.units * at.blocks == 0);
   };
 
+
+
   if (warp == kCopier) {
     // ------------------------------------------------------------ copies: a lane for each record of a unit
     const int32_t page_recs = p.page_size / kKv4Tokens;
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       const uint32_t mask = __ballot_sync(~0u, have);
       const uint8_t* src = p.data + (static_cast<int64_t>(page) * p.heads + at.item / at.blocks) * head_bytes + static_cast<int64_t>(in) * C::kRec;
       const int32_t keys = min(kKeys, at.len - at.u * kKeys);
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&sh.cempty[s]), ph, abort, p.status, kDevTimeoutProducer))) break;
+      if (!mbar_wait_warp(smem_u32(&sh.cempty[s]), ph, abort, p.status, kDevTimeoutProducer)) break;
       const uint32_t f = smem_u32(&sh.cfull[s]);
       if (lane == 0) {
         sh.stage_mask[s] = mask;
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
     int32_t left = 0;  // units of the piece that S goes on with
     uint32_t s_rest = n;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(~0u, mbar_wait(smem_u32(bar), parity, abort, p.status, kDevTimeoutMma));
+      return mbar_wait_warp(smem_u32(bar), parity, abort, p.status, kDevTimeoutMma);
     };
     auto scores = [&](uint32_t j) -> bool {
       const uint32_t b = j & 1, ph = (j >> 1) & 1;
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
     const int t = tid - 32 * kFirstExpand;
     uint32_t s = 0, ph = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(~0u, mbar_wait(smem_u32(bar), parity, abort, p.status, kDevTimeoutMma));
+      return mbar_wait_warp(smem_u32(bar), parity, abort, p.status, kDevTimeoutMma);
     };
     for (uint32_t j = 0; j < n; ++j) {
       const uint32_t b = j & 1, bph = (j >> 1) & 1;
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
     const uint32_t tl = tmem + (static_cast<uint32_t>(quadrant * 32) << 16);
     float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kCounterBytes);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(~0u, mbar_wait(smem_u32(bar), parity, abort, p.status, kDevTimeoutEpilogue));
+      return mbar_wait_warp(smem_u32(bar), parity, abort, p.status, kDevTimeoutEpilogue);
     };
     float qsum = 0.f;
     uint64_t see = 0;  // the row's nodes
@@ -582,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       const int32_t units = min(static_cast<uint32_t>(now.units - now.u), n - j);
       const int head = now.item / now.blocks, row0 = (now.item - head * now.blocks) * kRows;
       const int ctx = now.len - now.nodes;
+      const bool dead = row0 + quadrant * 32 >= now.nodes * p.group;
       const uint64_t mask = see;
       const uint64_t q2 = f2(qsum, qsum);
       float ref = 0.f, l = 0.f, z = 0.f;
@@ -591,6 +594,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       for (int32_t x = 0; x < units; ++x, ++j) {
         const uint32_t b = j & 1, ph = (j >> 1) & 1;
         ok = ok && wait(&sh.sfull[b], ph) && wait(&sh.nfull[b], ph);
+        if (dead) {  // none of the warp's rows is a query's: P is zeros
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sh.sfree[b]));
+            mbar_arrive(smem_u32(&sh.nempty[b]));
+          }
+          if (j > 0) ok = ok && wait(&sh.odone, (j - 1) & 1);
+          if (!ok) break;
+          uint32_t zero[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) zero[k] = 0;
+          tc_fence_after();
+          tmem_st_x32(tl + kPCol + half * 32, zero);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.pfull));
+          continue;
+        }
         uint32_t sv[2][32];
         float top = -INFINITY;
         if (ok) {

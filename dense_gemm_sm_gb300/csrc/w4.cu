@@ -202,45 +202,52 @@ __global__ void __launch_bounds__(kThreads) dequantize_w4_kernel(const W4RowsPar
 //   * A code c becomes the BF16 number 16 + c by a shift and one AND-OR for two of them: 16 is the
 //     least offset that keeps all four bits of c in a mantissa, and the layout has neighbouring k in
 //     the two halves of a word, so that pairs come out in the operand's order.
-//   * A group's sums stay apart: D = sum x (16 + c) is read from tensor memory when its group ends, S = sum x
-//     comes from two warps of their own (mma.sync with an operand of ones), and acc += s D + (z - 16 s) S in
-//     FP32.  Codes and x are exact in BF16, so no weight is rounded.
+//   * A group's sums stay apart: D = sum x (16 + c) is read from tensor memory when its group ends, and
+//     acc += s D + (z - 16 s) S, S = sum x, in FP32.  S comes from two warps of their own (mma.sync with an
+//     operand of ones); for 64 rows that would take them 2000 cycles a unit, and S comes from the same pipe as D,
+//     by products with ones in tensor memory.  Codes and x are exact in BF16, so no weight is rounded.
 // Units of 128 columns x 256 k of all column tiles are cut evenly over one CTA per SM; a tile cut between
 // CTAs is finished by the last of them to arrive, which adds the parts in CTA order (results do not depend on
 // arrival).  More than 64 rows of X: each column tile is computed for one block of 64 after the other,
 // by CTAs that run together, so the weights come from L2 after the first.
-// Warps: 0-3 groups' sums and joins (a thread per column), 4-11 expansion (a warpgroup for each half of a
-// unit), 12 copies, 13 products, 14-15 sums of X.
+// Warps: 0-3 groups' sums and joins (a thread per column), then two or three warpgroups that expand halves of
+// units in turn, a warp that copies, one that issues products, and two for the sums of X.
 constexpr int kMaxCtas = 160;               // CTAs that the workspace has room for
 constexpr int kUnitK = 256, kHalfK = 128;
 constexpr uint32_t kCodeBytes = 128 * kUnitK / 2;
-constexpr int kEpiWarps = 4, kSumWarps = 2;
-constexpr int kProducer = 12, kIssuer = 13, kFirstSum = 14;
-constexpr int kGemmThreads = 32 * (kFirstSum + kSumWarps);
+constexpr int kEpiWarps = 4;
 constexpr uint32_t kMinUnits = 2;           // of a CTA
-// Tensor memory: 256 columns of D, four buffers of an expanded half of a unit.
-constexpr uint32_t kACol = 256, kTmemCols = 512;
-constexpr int kABuffers = 4;
+// Tensor memory: 256 columns of D (and S), buffers of an expanded half of a unit, ones.
+constexpr uint32_t kACol = 256, kOnesCol = 448, kTmemCols = 512;
 constexpr int64_t kCounterBytes = 1024;
 static_assert(kMaxCtas * 4 <= kCounterBytes, "counters");
 
 template <int NTOK, int GROUP>
 struct Cfg {
+  static constexpr bool kOnes = NTOK == 64;                  // S by the same pipe as D
+  // Expanding warpgroups: three where registers allow it (16 rows of the FFN's width 12.4 us with two).
+  static constexpr int kExpand = kOnes ? 2 : 3;
+  static constexpr int kSumWarps = kOnes ? 0 : 2;
+  static constexpr int kProducer = kEpiWarps + 4 * kExpand, kIssuer = kProducer + 1, kFirstSum = kIssuer + 1;
+  static constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
+  static constexpr int kABuffers = kOnes ? 3 : 4;
   static constexpr int kStages = NTOK == 16 ? 7 : NTOK == 32 ? 6 : 4;
   static constexpr int kGroups = kUnitK / GROUP;             // of a unit
-  // Groups whose D is read together: 64 columns, within a half of a unit.
-  static constexpr int kTogether = kHalfK / GROUP < 64 / NTOK ? kHalfK / GROUP : 64 / NTOK;
+  // Groups whose D is read together: all of a unit where they are at most 128 columns.
+  static constexpr int kMost = 128 / NTOK / (kOnes ? 2 : 1), kTogether = kGroups < kMost ? kGroups : kMost;
   static constexpr int kReads = kGroups / kTogether;         // of a unit
-  static constexpr int kSlots = 256 / (kTogether * NTOK) < 8 ? 256 / (kTogether * NTOK) : 8;
+  static constexpr int kSlot = kTogether * NTOK * (kOnes ? 2 : 1);  // columns of one
+  static constexpr int kSlots = 256 / kSlot < 8 ? 256 / kSlot : 8;
+  static_assert(kSlots >= 2 && (kReads == 1 || kReads % 2 == 0), "reads");
   static constexpr uint32_t kXBox = NTOK * 128, kXBytes = 4 * kXBox, kParamBytes = kGroups * 512;
   static constexpr uint32_t kStage = kCodeBytes + kXBytes + 4096;
-  static constexpr uint32_t kSumBytes = kGroups * NTOK * 4;  // of a stage
+  static constexpr uint32_t kSumBytes = kOnes ? 0 : kGroups * NTOK * 4;  // of a stage
   static constexpr uint32_t kSmem = 1024 + kStages * (kStage + kSumBytes);
   static_assert(kStage % 1024 == 0 && kParamBytes <= 4096 && kSmem + 1024 <= 227 * 1024, "shared memory, with the static part");
 };
 
 struct Control {
-  uint64_t full[7], empty[7], sums[7], afull[kABuffers], aempty[kABuffers], dfull[8], dempty[8], drain;
+  uint64_t full[7], empty[7], sums[7], afull[4], aempty[4], dfull[8], dempty[8], drain;
   uint32_t tmem_base, abort, issued, verdict;
 };
 
@@ -305,6 +312,9 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t a, const uint32_t (&r)[32])
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_x8(uint32_t a, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -343,8 +353,9 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t a, uint32_t (&r)[4]) {
 }
 
 template <int NTOK, int GROUP>
-__global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_constant__ Maps maps, const W4GemmParams p) {
+__global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(const __grid_constant__ Maps maps, const W4GemmParams p) {
   using C = Cfg<NTOK, GROUP>;
+  constexpr int kABuffers = C::kABuffers, kProducer = C::kProducer, kIssuer = C::kIssuer, kFirstSum = C::kFirstSum;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Control ctl;
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u, sum_ring = ring + C::kStages * C::kStage;
@@ -355,7 +366,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&ctl.full[s]), 1);
       mbar_init(smem_u32(&ctl.empty[s]), 1 + kEpiWarps);
-      mbar_init(smem_u32(&ctl.sums[s]), kSumWarps);
+      if (!C::kOnes) mbar_init(smem_u32(&ctl.sums[s]), C::kSumWarps);
     }
     for (int a = 0; a < kABuffers; ++a) {
       mbar_init(smem_u32(&ctl.afull[a]), 4);
@@ -379,6 +390,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, ctl.tmem_base, 0);
   const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's lanes
+  if constexpr (C::kOnes) {
+    if (warp < kEpiWarps) {
+      tmem_st_x8(tl + kOnesCol, 0x3F803F80u);
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
 
   const uint32_t kb = static_cast<uint32_t>((p.K + kUnitK - 1) / kUnitK);
   const uint32_t blocks = static_cast<uint32_t>((p.M + NTOK - 1) / NTOK);
@@ -394,7 +414,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
     const uint32_t to = ring + (lane == 0 ? 0u : lane == 1 ? kCodeBytes + C::kXBytes : kCodeBytes + box * C::kXBox);
     pdl_wait();
     for (; i < n; ++i) {
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.empty[s]), ph, abort, p.status, kDevTimeoutProducer))) break;
+      if (!mbar_wait_warp(smem_u32(&ctl.empty[s]), ph, abort, p.status, kDevTimeoutProducer)) break;
       const uint32_t f = smem_u32(&ctl.full[s]);
       if (lane == 0) mbar_arrive_expect_tx(f, kCodeBytes + C::kXBytes + C::kParamBytes);
       __syncwarp();
@@ -421,25 +441,39 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
       const uint64_t x = x0 + s * (C::kStage >> 4);
 #pragma unroll
       for (int r = 0; r < C::kReads; ++r) {
-        constexpr int kSteps = GROUP / 16, kHalfReads = C::kReads / 2;
-        // (The warps that expanded the half have seen its stage filled.)
-        if (r % kHalfReads == 0) ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&ctl.afull[a]), aph, abort, p.status, kDevTimeoutMma));
-        ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&ctl.dempty[slot]), dph, abort, p.status, kDevTimeoutMma));
+        constexpr int kSteps = GROUP / 16, kHalfReads = C::kReads > 1 ? C::kReads / 2 : 1, kHalves = C::kReads > 1 ? 1 : 2;
+        // Lanes wait for different barriers at once, as every wait takes 60 cycles and more: the expanded halves and the place
+        // of D.  (The warps that expanded a half have seen its stage filled.)
+        const bool half = r % kHalfReads == 0 && lane < kHalves;  // a begins anew with r, and has an even number of buffers then
+        const uint32_t bar = half ? smem_u32(&ctl.afull[a + lane]) : smem_u32(&ctl.dempty[slot]);
+        ok = mbar_wait_warp(bar, half ? aph : dph, abort, p.status, kDevTimeoutMma);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + slot * (C::kTogether * NTOK), at = tmem + kACol + 64 * a;
+        const uint32_t d = tmem + slot * C::kSlot;
 #pragma unroll
         for (int j = 0; j < C::kTogether * kSteps; ++j) {
           const int step = r * C::kTogether * kSteps + j, in = step % (kHalfK / 16);  // 16 k each: of the unit, of the half
           const uint64_t b = x + ((step >> 2) * C::kXBox + (step & 3) * 32) / 16;
-          if (j % kSteps == 0) umma_ts<false>(d + j / kSteps * NTOK, at + in * 8, b, idesc, lead);
-          else umma_ts<true>(d + j / kSteps * NTOK, at + in * 8, b, idesc, lead);
+          const uint32_t at = tmem + kACol + 64 * a + (kHalves == 2 ? step / (kHalfK / 16) * 64 : 0) + in * 8;
+          if (j % kSteps == 0) umma_ts<false>(d + j / kSteps * NTOK, at, b, idesc, lead);
+          else umma_ts<true>(d + j / kSteps * NTOK, at, b, idesc, lead);
+        }
+        if constexpr (C::kOnes) {
+          static_assert(C::kTogether == 1, "S lies behind its D");
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j) {
+            const int step = r * kSteps + j;
+            const uint64_t b = x + ((step >> 2) * C::kXBox + (step & 3) * 32) / 16;
+            if (j == 0) umma_ts<false>(d + NTOK, tmem + kOnesCol, b, idesc, lead);
+            else umma_ts<true>(d + NTOK, tmem + kOnesCol, b, idesc, lead);
+          }
         }
         commit(&ctl.dfull[slot], lead);
         if (++slot == C::kSlots) slot = 0, dph ^= 1u;
         if (r % kHalfReads == kHalfReads - 1) {
-          commit(&ctl.aempty[a], lead);
-          if (++a == kABuffers) a = 0, aph ^= 1u;
+#pragma unroll
+          for (int e = 0; e < kHalves; ++e) commit(&ctl.aempty[a + e], lead);
+          if ((a += kHalves) == kABuffers) a = 0, aph ^= 1u;
         }
       }
       if (!ok) break;
@@ -452,32 +486,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
     __syncwarp();
   } else if (warp >= kFirstSum) {
     // ------------------------------------------------------------ sums of X: a warp takes every other eight rows
-    constexpr int kTiles = NTOK / 8 / kSumWarps;
+    if constexpr (!C::kOnes) {
+    constexpr int kTiles = NTOK / 8 / C::kSumWarps;
     const int w = warp - kFirstSum, r8 = lane & 7, piece = lane >> 3;
     uint32_t s = 0, ph = 0;
     pdl_wait();
     for (uint32_t i = 0; i < n; ++i) {
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), ph, abort, p.status, kDevTimeoutMma))) break;
+      if (!mbar_wait_warp(smem_u32(&ctl.full[s]), ph, abort, p.status, kDevTimeoutMma)) break;
       const uint32_t x = ring + s * C::kStage + kCodeBytes + r8 * 128, out = sum_ring + s * C::kSumBytes + lane * 8;
-      float c[kTiles][4];
+      float c[kTiles][2][4];  // two chains
 #pragma unroll
       for (int step = 0; step < kUnitK / 32; ++step) {  // 32 k
         if (step % (GROUP / 32) == 0) {
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) c[t][0] = c[t][1] = c[t][2] = c[t][3] = 0.f;
+          for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) c[t][e][0] = c[t][e][1] = c[t][e][2] = c[t][e][3] = 0.f;
         }
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           uint32_t b[4];
-          ldmatrix_x4(x + (step >> 1) * C::kXBox + (t * kSumWarps + w) * 1024 + ((((step & 1) * 4 + piece) ^ r8) << 4), b);
-          mma_ones(c[t], b[0], b[1]);
-          mma_ones(c[t], b[2], b[3]);
+          ldmatrix_x4(x + (step >> 1) * C::kXBox + (t * C::kSumWarps + w) * 1024 + ((((step & 1) * 4 + piece) ^ r8) << 4), b);
+          mma_ones(c[t][0], b[0], b[1]);
+          mma_ones(c[t][1], b[2], b[3]);
         }
         if (step % (GROUP / 32) == GROUP / 32 - 1 && lane < 4) {  // rows of the product are alike
 #pragma unroll
           for (int t = 0; t < kTiles; ++t)
-            asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(out + (step / (GROUP / 32) * NTOK + (t * kSumWarps + w) * 8) * 4),
-                         "f"(c[t][0]), "f"(c[t][1])
+            asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(out + (step / (GROUP / 32) * NTOK + (t * C::kSumWarps + w) * 8) * 4),
+                         "f"(c[t][0][0] + c[t][1][0]), "f"(c[t][0][1] + c[t][1][1])
                          : "memory");
         }
       }
@@ -485,38 +522,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
       if (lane == 0) mbar_arrive(smem_u32(&ctl.sums[s]));
       if (++s == C::kStages) s = 0, ph ^= 1u;
     }
+    }
   } else if (warp >= kEpiWarps) {
     // ------------------------------------------------------------ expansion
     const Magic magic;
-    const uint32_t half = (warp - kEpiWarps) / 4, row = (warp & 3) * 32 + lane, swz = row & 7;  // 128-byte rows, 16-byte pieces swizzled
-    uint32_t s = 0, ph = 0, a = half, aph = 1;
+    const uint32_t g = (warp - kEpiWarps) / 4, row = (warp & 3) * 32 + lane, swz = row & 7;  // 128-byte rows, 16-byte pieces swizzled
     pdl_wait();
-    for (uint32_t i = 0; i < n; ++i) {
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), ph, abort, p.status, kDevTimeoutMma))) break;
-      uint32_t v[2][32];
+    for (uint32_t h = g; h < 2 * n; h += C::kExpand) {  // half h & 1 of unit h >> 1
+      const uint32_t i = h >> 1, s = i % C::kStages, a = h % kABuffers, to = tl + kACol + 64 * a;
+      const uint32_t bar = lane == 0 ? smem_u32(&ctl.full[s]) : smem_u32(&ctl.aempty[a]);
+      if (!mbar_wait_warp(bar, lane == 0 ? (i / C::kStages) & 1u : ((h / kABuffers) & 1u) ^ 1u, abort, p.status, kDevTimeoutMma)) break;
+      const uint32_t from = ring + s * C::kStage + row * 128;
+      uint32_t v[32];
+      auto expand = [&](uint32_t c) {  // two pieces
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint4 w = lds128(ring + s * C::kStage + row * 128 + (((half * 4 + c) ^ swz) << 4));
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        for (int y = 0; y < 2; ++y) {
+          const uint4 w = lds128(from + (((h & 1) * 4 + c + y) ^ swz) * 16);
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t* to = &v[c >> 1][(c & 1) * 16 + 4 * j];
-          to[0] = magic.pair(ws[j] << 3);
-          to[1] = magic.pair(ws[j] >> 1);
-          to[2] = magic.pair(ws[j] >> 5);
-          to[3] = magic.pair(ws[j] >> 9);
+          for (int j = 0; j < 4; ++j) {
+            v[y * 16 + 4 * j] = magic.pair(ws[j] << 3);
+            v[y * 16 + 4 * j + 1] = magic.pair(ws[j] >> 1);
+            v[y * 16 + 4 * j + 2] = magic.pair(ws[j] >> 5);
+            v[y * 16 + 4 * j + 3] = magic.pair(ws[j] >> 9);
+          }
         }
-      }
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&ctl.aempty[a]), aph, abort, p.status, kDevTimeoutMma))) break;
+      };
+      expand(0);
       tc_fence_after();
-      tmem_st_x32(tl + kACol + 64 * a, v[0]);
-      tmem_st_x32(tl + kACol + 64 * a + 32, v[1]);
+      tmem_st_x32(to, v);
+      expand(2);
+      tmem_st_x32(to + 32, v);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl.afull[a]));
-      if (++s == C::kStages) s = 0, ph ^= 1u;
-      if ((a += 2) >= kABuffers) a = half, aph ^= 1u;
     }
   } else {
     // ------------------------------------------------------------ groups' sums, and the tiles' join
@@ -532,21 +572,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
       for (int t = 0; t < NTOK; ++t) acc[t] = 0.f;
       bool ok = true;
       for (const uint32_t to = i + units; ok && i < to; ++i) {
-        // (The sums' barrier follows the stage's: parameters are there too.)
-        ok = __all_sync(~0u, mbar_wait(smem_u32(&ctl.full[s]), ph, abort, p.status, kDevTimeoutEpilogue) &&
-                                 mbar_wait(smem_u32(&ctl.sums[s]), ph, abort, p.status, kDevTimeoutEpilogue));
 #pragma unroll
         for (int r = 0; r < C::kReads; ++r) {
-          ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&ctl.dfull[slot]), dph, abort, p.status, kDevTimeoutEpilogue));
+          // The stage (its parameters), the sums of X, D.
+          const bool first = r == 0 && lane < (C::kOnes ? 1 : 2);
+          const uint32_t bar = first ? (lane == 0 ? smem_u32(&ctl.full[s]) : smem_u32(&ctl.sums[s])) : smem_u32(&ctl.dfull[slot]);
+          ok = mbar_wait_warp(bar, first ? ph : dph, abort, p.status, kDevTimeoutEpilogue);
           if (!ok) break;
           tc_fence_after();
-          constexpr int kCols = C::kTogether * NTOK, kAtOnce = kCols < 32 ? kCols : 32;
-          const uint32_t d = tl + slot * kCols;
+          constexpr int kCols = C::kTogether * NTOK, kAtOnce = kCols < 32 || C::kOnes ? 16 : 32;
+          const uint32_t d = tl + slot * C::kSlot;
 #pragma unroll
           for (int c = 0; c < kCols; c += kAtOnce) {
-            uint32_t dv[kAtOnce];
+            uint32_t dv[kAtOnce], sv[C::kOnes ? kAtOnce : 1];
             if constexpr (kAtOnce == 16) tmem_ld_32x32b_x16(d + c, dv);
             else tmem_ld_32x32b_x32(d + c, dv);
+            if constexpr (C::kOnes) tmem_ld_32x32b_x16(d + NTOK + c, sv);
             tmem_ld_wait();
             if (c + kAtOnce == kCols) {
               tc_fence_before();
@@ -558,7 +599,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_w4_kernel(const __grid_c
               const int g = r * C::kTogether + (c + t) / NTOK, tok = (c + t) % NTOK;
               const uint32_t prm = lds32(ring + s * C::kStage + kCodeBytes + C::kXBytes + g * 512 + col * 4);
               const float scale = lo_of(prm), zero = fmaf(-16.f, scale, hi_of(prm));
-              const uint4 x = lds128(sum_ring + s * C::kSumBytes + (g * NTOK + tok) * 4);
+              uint4 x;
+              if constexpr (C::kOnes) x = make_uint4(sv[t], sv[t + 1], sv[t + 2], sv[t + 3]);
+              else x = lds128(sum_ring + s * C::kSumBytes + (g * NTOK + tok) * 4);
               acc[tok] = fmaf(scale, __uint_as_float(dv[t]), fmaf(zero, __uint_as_float(x.x), acc[tok]));
               acc[tok + 1] = fmaf(scale, __uint_as_float(dv[t + 1]), fmaf(zero, __uint_as_float(x.y), acc[tok + 1]));
               acc[tok + 2] = fmaf(scale, __uint_as_float(dv[t + 2]), fmaf(zero, __uint_as_float(x.z), acc[tok + 2]));
@@ -678,7 +721,7 @@ cudaError_t launch_variant(const W4GemmParams& p, int sms, cudaStream_t s) {
   if (ctas > kMaxCtas) ctas = kMaxCtas;
   W4GemmParams q = p;
   q.fault = g_fault_injection;
-  return launch_pdl(gemm_w4_kernel<NTOK, GROUP>, dim3(static_cast<unsigned>(ctas)), dim3(kGemmThreads), C::kSmem, s, m, q);
+  return launch_pdl(gemm_w4_kernel<NTOK, GROUP>, dim3(static_cast<unsigned>(ctas)), dim3(C::kThreads), C::kSmem, s, m, q);
 }
 
 template <int NTOK>
