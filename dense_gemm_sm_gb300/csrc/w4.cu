@@ -210,8 +210,11 @@ __global__ void __launch_bounds__(kThreads) dequantize_w4_kernel(const W4RowsPar
 // CTAs is finished by the last of them to arrive, which adds the parts in CTA order (results do not depend on
 // arrival).  More than 64 rows of X: each column tile is computed for one block of 64 after the other,
 // by CTAs that run together, so the weights come from L2 after the first.
-// Warps: 0-3 groups' sums and joins (a thread per column), then two or three warpgroups that expand halves of
-// units in turn, a warp that copies, one that issues products, and two for the sums of X.
+// Warps: 0-3 groups' sums and joins (a thread per column), 4-11 expansion (a warpgroup for each half of a
+// unit), 12 copies, 13 issues products, 14-15 sums of X.
+// Measured: 16 rows times 100003 columns of 4096 in 54 us, 4.1 TB/s; without the expansion's arithmetic 49, with
+// copies alone 42 (timing copies).  A third expanding warpgroup (56 us) and rings of their own for codes, X and
+// parameters (59) were slower: more warps share the same logic pipe.
 constexpr int kMaxCtas = 160;               // CTAs that the workspace has room for
 constexpr int kUnitK = 256, kHalfK = 128;
 constexpr uint32_t kCodeBytes = 128 * kUnitK / 2;
@@ -225,10 +228,8 @@ static_assert(kMaxCtas * 4 <= kCounterBytes, "counters");
 template <int NTOK, int GROUP>
 struct Cfg {
   static constexpr bool kOnes = NTOK == 64;                  // S by the same pipe as D
-  // Expanding warpgroups: three where registers allow it (16 rows of the FFN's width 12.4 us with two).
-  static constexpr int kExpand = kOnes ? 2 : 3;
   static constexpr int kSumWarps = kOnes ? 0 : 2;
-  static constexpr int kProducer = kEpiWarps + 4 * kExpand, kIssuer = kProducer + 1, kFirstSum = kIssuer + 1;
+  static constexpr int kProducer = kEpiWarps + 8, kIssuer = kProducer + 1, kFirstSum = kIssuer + 1;
   static constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
   static constexpr int kABuffers = kOnes ? 3 : 4;
   static constexpr int kStages = NTOK == 16 ? 7 : NTOK == 32 ? 6 : 4;
@@ -526,18 +527,18 @@ __global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(
   } else if (warp >= kEpiWarps) {
     // ------------------------------------------------------------ expansion
     const Magic magic;
-    const uint32_t g = (warp - kEpiWarps) / 4, row = (warp & 3) * 32 + lane, swz = row & 7;  // 128-byte rows, 16-byte pieces swizzled
+    const uint32_t half = (warp - kEpiWarps) / 4, row = (warp & 3) * 32 + lane, swz = row & 7;  // 128-byte rows, 16-byte pieces swizzled
+    uint32_t s = 0, ph = 0, a = half, aph = 1;
     pdl_wait();
-    for (uint32_t h = g; h < 2 * n; h += C::kExpand) {  // half h & 1 of unit h >> 1
-      const uint32_t i = h >> 1, s = i % C::kStages, a = h % kABuffers, to = tl + kACol + 64 * a;
+    for (uint32_t i = 0; i < n; ++i) {
       const uint32_t bar = lane == 0 ? smem_u32(&ctl.full[s]) : smem_u32(&ctl.aempty[a]);
-      if (!mbar_wait_warp(bar, lane == 0 ? (i / C::kStages) & 1u : ((h / kABuffers) & 1u) ^ 1u, abort, p.status, kDevTimeoutMma)) break;
-      const uint32_t from = ring + s * C::kStage + row * 128;
+      if (!mbar_wait_warp(bar, lane == 0 ? ph : aph, abort, p.status, kDevTimeoutMma)) break;
+      const uint32_t from = ring + s * C::kStage + row * 128, to = tl + kACol + 64 * a;
       uint32_t v[32];
       auto expand = [&](uint32_t c) {  // two pieces
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const uint4 w = lds128(from + (((h & 1) * 4 + c + y) ^ swz) * 16);
+          const uint4 w = lds128(from + ((half * 4 + c + y) ^ swz) * 16);
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -557,6 +558,8 @@ __global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl.afull[a]));
+      if (++s == C::kStages) s = 0, ph ^= 1u;
+      if ((a += 2) >= kABuffers) a -= kABuffers, aph ^= 1u;
     }
   } else {
     // ------------------------------------------------------------ groups' sums, and the tiles' join
