@@ -98,7 +98,9 @@ def test_product_workspace():
     need = dg.dg_gemm_w4_workspace_bytes(4, 10, 100)
     assert need > 0
     assert dg.gemm_w4_bf16(*{**GEMM, "workspace_bytes": need - 1}.values(), stream=0, check=False) == INV
-    for bad in [(0, 10, 100), (4, 0, 100), (4, 10, 0), (-1, 10, 100), (4, (1 << 30) + 1, 100), (1 << 62, 10, 100), (4, 10, 1 << 62)]:
+    # Units of 128 columns, 256 k and 64 rows are counted in 31 bits.
+    assert dg.dg_gemm_w4_workspace_bytes(1, 1 << 30, 1 << 15) > 0
+    for bad in [(1, 1 << 30, 1 << 17), (1 << 30, 1 << 30, 1 << 30), (0, 10, 100), (4, 0, 100), (4, 10, 0), (-1, 10, 100), (4, (1 << 30) + 1, 100), (1 << 62, 10, 100), (4, 10, 1 << 62)]:
         assert dg.dg_gemm_w4_workspace_bytes(*bad) == 0
 
 
