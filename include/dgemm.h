@@ -478,8 +478,8 @@ dg_status dequantize_groups_w4(int64_t N, int64_t K, int32_t group, const uint8_
  *     range.
  *   - workspace: see above; dg_gemm_w4_workspace_bytes (0 for sizes it does not take).
  *   - Errors: negative sizes, short strides, null pointers, another c_type, a workspace that is
- *     too small DG_ERR_INVALID_ARG; a group that is not 32, 64 or 128, sizes over 2^30
- *     DG_ERR_UNSUPPORTED; X, Q or params not 16-byte or workspace not 256-byte aligned, ldx not a
+ *     too small DG_ERR_INVALID_ARG; a group that is not 32, 64 or 128, sizes over 2^30, 2^31 or
+ *     more blocks of 64 x 128 x 256 DG_ERR_UNSUPPORTED; X, Q or params not 16-byte or workspace not 256-byte aligned, ldx not a
  *     multiple of 8, ldq of 16, ldp of 4, C not aligned to its element DG_ERR_MISALIGNED.
  *     M == 0 or N == 0: nothing; K == 0: C = 0.
  */
@@ -603,9 +603,9 @@ double dg_model_quant_traffic_bytes(int64_t M, int64_t K, int64_t N, int64_t til
 /* Library version string. */
 const char* dg_version(void);
 
-/* Test hook: 0 = off.  1 = the MMA issuers of the tcgen05 tile kernel and of moe_bf16 and
- * attention_kv4's computing warps skip their stage releases, so the bounded waits expire and DG_ERR_TIMEOUT is reported (no hang,
- * no fault).  Affects launches made after the call. */
+/* Test hook: 0 = off.  1 = the MMA issuers of the tcgen05 tile kernel, of moe_bf16 and of gemm_w4_bf16 and the computing
+ * or expanding warps of attention_kv4 and attention_kv4_tree skip their stage releases, so the bounded waits expire and
+ * DG_ERR_TIMEOUT is reported (no hang, no fault).  Affects launches made after the call. */
 void dg_set_fault_injection(int32_t mode);
 
 #ifdef __cplusplus
