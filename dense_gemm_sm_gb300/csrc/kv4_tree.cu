@@ -12,12 +12,12 @@
 // The rows of the group's heads and of all nodes (row = node * group + head) share each expanded key:
 // a block of 128 of them is the MMA's M.  Per unit of 128 keys (d = 128) the tensor cores need 1040 cycles,
 // the exponentials 1024, expanding K and V 512 of the logic pipe.  Warps:
-//   0-7    softmax, two threads a row (64 keys each; they exchange the maximum), epilogue;
-//   8-11   expansion: a thread per key writes K's row, then 8 keys of V's columns, as K-major operands
+//   0-15   softmax, four threads a row (32 keys each; they exchange the maximum), epilogue;
+//   16-19  expansion: a thread per key writes K's row, then 8 keys of V's columns, as K-major operands
 //          (d in the order in which the codes come out of their words, which Q's rows follow; V's
 //          pieces hold two tokens of a column side by side, so that V comes out transposed);
-//   12     copies of records into a ring;   13  products: S_j+1 before P_j V_j, so that the softmax of
-//          one unit overlaps the product of the next.
+//   20     copies of records into a ring;   21  products: S_j+1 before P_j V_j, so that the softmax of
+//          one unit overlaps the product of the next.  P_j takes the place of S_j in tensor memory.
 // Units of all (sequence, head, block of rows) items are cut evenly over one CTA per SM.  A cut item's parts
 // go to the workspace, and a small second kernel joins them in CTA order, spread over all SMs (one
 // CTA alone would read 66 kB for each part).
@@ -36,14 +36,15 @@ namespace {
 
 constexpr int kMaxCtas = 160;    // CTAs that the workspace has room for
 constexpr int kKeys = 128, kRows = 128, kUnitRecs = kKeys / kKv4Tokens;
-constexpr int kSoftWarps = 8, kExpandWarps = 4;
+constexpr int kSoftWarps = 16, kExpandWarps = 4;
+constexpr int kParts = kSoftWarps / 4, kPartKeys = kKeys / kParts;  // of a unit's keys, one to each warp of a quadrant
 constexpr int kFirstExpand = kSoftWarps, kCopier = kFirstExpand + kExpandWarps, kIssuer = kCopier + 1;
 constexpr int kThreads = 32 * (kIssuer + 1);
 constexpr uint32_t kMinUnits = 2;   // of a CTA
 constexpr float kSlack = 8.f;       // the reference follows the maximum only when that has outgrown it by this
 constexpr int64_t kCounterBytes = 1024;  // of kv4_attention.cu's kernel, left as they are
-// Tensor memory: S (two buffers), O and the column of sums of P, P.
-constexpr uint32_t kOCol = 256, kPCol = 448, kTmemCols = 512;
+// Tensor memory: S (two buffers; P_j takes the place of S_j), O and the column of sums of P.
+constexpr uint32_t kOCol = 256, kTmemCols = 512;
 
 template <int D>
 struct Cfg {
@@ -56,7 +57,7 @@ struct Cfg {
   static constexpr uint32_t kStage = kUnitRecs * kRecStride;
   static constexpr uint32_t kSmem = 1024 + kQBytes + 2 * kKBytes + 2 * kVBytes + kStages * kStage;
   static constexpr int64_t kPart = kRows * D + 2 * kRows;      // floats: [d / 4][row] float4, references, sums
-  static_assert(kSmem + 10 * 1024 <= 227 * 1024, "shared memory, with the static part");
+  static_assert(kSmem + 16 * 1024 <= 227 * 1024, "shared memory, with the static part");
 };
 
 // A cut item, for the join.
@@ -68,18 +69,18 @@ struct Cut {
 struct Shared {
   alignas(16) float a[2][kKeys], b[2][kKeys], vs[2][kKeys], vz[2][kKeys];  // of a unit's keys
   uint32_t valid[2][kKeys / 32];
-  float top[2][2][kRows];                                      // halves' maxima
-  float l[2][kRows], z[2][kRows], q[2][kRows];
-  int32_t okay[2][2][4];
-  uint64_t cfull[4], cempty[4], kfull[2], kempty[2], vfull[2], vempty[2], nfull[2], nempty[2], sfull[2], sfree[2];
-  uint64_t pfull, odone, qfull, oread, drain;
+  float top[2][kParts][kRows];                                 // parts' maxima
+  float l[kParts][kRows], z[kParts][kRows], q[kParts][kRows];
+  alignas(16) int32_t okay[2][4][kParts];
+  uint64_t cfull[4], cempty[4], kfull[2], kempty[2], vfull[2], vempty[2], nempty[2], sfull[2], pfull[2], odone[2];
+  uint64_t qfull, oread, drain;
   uint32_t stage_mask[4];
   int32_t stage_keys[4];
   uint32_t tmem_base, abort, verdict, issued, total;
   struct Start {
     uint32_t b;
     int32_t item, u, units, blocks, len, nodes;
-  } start;
+  } start, at[kSoftWarps];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -174,16 +175,11 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
       "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_x32(uint32_t a, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st_x16(uint32_t a, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+      "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_x1(uint32_t a, uint32_t v) {
@@ -196,8 +192,8 @@ __device__ __forceinline__ uint32_t tmem_ld_x1(uint32_t a) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ void pair_bar(int quadrant) { asm volatile("bar.sync %0, 64;" ::"r"(2 + quadrant) : "memory"); }
+__device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void part_bar(int quadrant) { asm volatile("bar.sync %0, 128;" ::"r"(2 + quadrant) : "memory"); }
 
 // Codes -> BF16 pairs 16 + code: bits 3-6 of 0x4180.
 struct Magic {
@@ -245,13 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       mbar_init(smem_u32(&sh.kempty[s]), 1);
       mbar_init(smem_u32(&sh.vfull[s]), kExpandWarps);
       mbar_init(smem_u32(&sh.vempty[s]), 1);
-      mbar_init(smem_u32(&sh.nfull[s]), kExpandWarps);
       mbar_init(smem_u32(&sh.nempty[s]), kSoftWarps);
       mbar_init(smem_u32(&sh.sfull[s]), 1);
-      mbar_init(smem_u32(&sh.sfree[s]), kSoftWarps);
+      mbar_init(smem_u32(&sh.pfull[s]), kSoftWarps);
+      mbar_init(smem_u32(&sh.odone[s]), 1);
     }
-    mbar_init(smem_u32(&sh.pfull), kSoftWarps);
-    mbar_init(smem_u32(&sh.odone), 1);
     mbar_init(smem_u32(&sh.qfull), kSoftWarps);
     mbar_init(smem_u32(&sh.oread), kSoftWarps);
     mbar_init(smem_u32(&sh.drain), 1);
@@ -333,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
 
   // The pieces of items, one after the other.
   Shared::Start at = sh.start;
-  auto forward = [&](int32_t k) {  // k units on; there are more units
+  auto forward = [&](Shared::Start& at, int32_t k) {  // k units on; there are more units
     at.u += k;
     if (at.u < at.units) return;
     at.u = 0;
@@ -347,8 +341,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       at.blocks = row_blocks(at.nodes);
     } while (at.units * at.blocks == 0);
   };
-
-
 
   if (warp == kCopier) {
     // ------------------------------------------------------------ copies: a lane for each record of a unit
@@ -384,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       if (have) bulk_load(ring + s * C::kStage + lane * C::kRecStride, src, C::kRec, f);
       if (++s == C::kStages) s = 0, ph ^= 1u;
       if (i + 1 < n) {
-        forward(1);
+        forward(at, 1);
         look_up();
       }
     }
@@ -409,12 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
     auto scores = [&](uint32_t j) -> bool {
       const uint32_t b = j & 1, ph = (j >> 1) & 1;
       if (left == 0) {
-        if (j > 0) forward(at.units - at.u);
+        if (j > 0) forward(at, at.units - at.u);
         left = min(static_cast<uint32_t>(at.units - at.u), s_rest);
         if (!wait(&sh.qfull, qph)) return false;
         qph ^= 1u;
       }
-      if (!wait(&sh.kfull[b], ph) || !wait(&sh.sfree[b], ph ^ 1u)) return false;
+      // (S's place was P's of two units before, whose product comes before this one.)
+      if (!wait(&sh.kfull[b], ph)) return false;
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -433,15 +426,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       const uint32_t b = j & 1, ph = (j >> 1) & 1;
       const bool last = left == 0;  // of its piece: the next product waits for other queries
       if (!last) ok = scores(j + 1);
-      if (!ok || !wait(&sh.vfull[b], ph) || !wait(&sh.pfull, j & 1) || (first && !wait(&sh.oread, oph))) break;
+      if (!ok || !wait(&sh.vfull[b], ph) || !wait(&sh.pfull[b], ph) || (first && !wait(&sh.oread, oph))) break;
       if (first) oph ^= 1u;
       tc_fence_after();
       const uint64_t v = dV + b * (C::kVBytes >> 4);
 #pragma unroll
       for (int k = 0; k < kKeys / 16; ++k)
-        umma_ts(tmem + kOCol, tmem + kPCol + k * 8, v + (((k >> 2) * C::kVBox + (k & 3) * 32) >> 4), idO, !first || k > 0, lead);
+        umma_ts(tmem + kOCol, tmem + b * kKeys + k * 8, v + (((k >> 2) * C::kVBox + (k & 3) * 32) >> 4), idO, !first || k > 0, lead);
       commit(&sh.vempty[b], lead);
-      commit(&sh.odone, lead);
+      commit(&sh.odone[b], lead);
       first = last;
       if (last && j + 1 < n) ok = scores(j + 1);
     }
@@ -480,9 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
             st_shared_v4(out + (cc >> 1) * (kKeys * 128) + ((((cc & 1) * 4 + x) ^ (t & 7)) << 4), magic.pair<0>(ws[x]), magic.pair<1>(ws[x]),
                          magic.pair<2>(ws[x]), magic.pair<3>(ws[x]));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.kfull[b]));
         if (!wait(&sh.nempty[b], bph ^ 1u)) break;
         // A key that no query sees may hold anything.
         const float ks = valid ? lo_of(kp) : 0.f, kz = valid ? hi_of(kp) : 0.f, vs = valid ? lo_of(vp) : 0.f, vz = valid ? hi_of(vp) : 0.f;
@@ -492,8 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
         sh.vz[b][t] = fmaf(8.f, vs, vz);
         const uint32_t vote = __ballot_sync(~0u, valid);
         if (lane == 0) sh.valid[b][warp - kFirstExpand] = vote;
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.nfull[b]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.kfull[b]));
       }
       {
         // V: thread t has 8 keys (one half of a record) of d / 8 columns.
@@ -542,13 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       if (++s == C::kStages) s = 0, ph ^= 1u;
     }
   } else {
-    // ------------------------------------------------------------ softmax: a row's keys 64 half .. 64 half + 63
-    const int quadrant = warp & 3, half = warp >> 2, row = quadrant * 32 + lane;
+    // ------------------------------------------------------------ softmax: a row's keys 32 part .. 32 part + 31
+    const int quadrant = warp & 3, part = warp >> 2, row = quadrant * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quadrant * 32) << 16);
     float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kCounterBytes);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       return mbar_wait_warp(smem_u32(bar), parity, abort, p.status, kDevTimeoutEpilogue);
     };
+    Shared::Start& at = sh.at[warp];  // (in shared memory, for registers: every lane writes the same)
+    at = sh.start;
     float qsum = 0.f;
     uint64_t see = 0;  // the row's nodes
     // The piece's queries to shared memory, in the order of K's codes; rows without one are zeros.
@@ -556,35 +549,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       const int head = at.item / at.blocks, r = (at.item - head * at.blocks) * kRows + row, i = r / p.group;
       const bool live = i < at.nodes;
       const uint4* src = reinterpret_cast<const uint4*>(p.Q + static_cast<int64_t>(at.b) * p.strideQ + static_cast<int64_t>(i) * p.ldq +
-                                                        static_cast<int64_t>(head * p.group + r - i * p.group) * D + half * (D / 2));
-      uint4 w[D / 16];
+                                                        static_cast<int64_t>(head * p.group + r - i * p.group) * D + part * (D / kParts));
+      uint4 w[D / kParts / 8];
       float sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) w[x] = live ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+      for (int x = 0; x < D / kParts / 8; ++x) w[x] = live ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
       see = live ? __ldg(reinterpret_cast<const unsigned long long*>(p.mask) + static_cast<int64_t>(at.b) * p.Lq + i) : 0;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const int piece = half * (D / 16) + x;
+      for (int x = 0; x < D / kParts / 8; ++x) {
+        const int piece = part * (D / kParts / 8) + x;
         st_shared_v4(sQ + (piece >> 3) * (kRows * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4), __byte_perm(w[x].x, w[x].z, 0x5410),
                      __byte_perm(w[x].x, w[x].z, 0x7632), __byte_perm(w[x].y, w[x].w, 0x5410), __byte_perm(w[x].y, w[x].w, 0x7632));
         sum += (lo_of(w[x].x) + hi_of(w[x].x)) + (lo_of(w[x].y) + hi_of(w[x].y)) + ((lo_of(w[x].z) + hi_of(w[x].z)) + (lo_of(w[x].w) + hi_of(w[x].w)));
       }
-      sh.q[half][row] = sum;
+      sh.q[part][row] = sum;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.qfull));
     };
     if (n > 0) load_queries();
-    pair_bar(quadrant);
-    qsum = sh.q[0][row] + sh.q[1][row];
+    part_bar(quadrant);
+    qsum = (sh.q[0][row] + sh.q[1][row]) + (sh.q[2][row] + sh.q[3][row]);
     int32_t valid_cut = 0;
     uint32_t j = 0;
     while (j < n) {
-      const Shared::Start now = at;
-      const int32_t units = min(static_cast<uint32_t>(now.units - now.u), n - j);
-      const int head = now.item / now.blocks, row0 = (now.item - head * now.blocks) * kRows;
-      const int ctx = now.len - now.nodes;
-      const bool dead = row0 + quadrant * 32 >= now.nodes * p.group;
+      const int32_t units = min(static_cast<uint32_t>(at.units - at.u), n - j);
+      const int shared0 = at.len - at.nodes - at.u * kKeys - part * kPartKeys;  // keys from the first of this part's that every query sees
+      const bool dead = at.item % at.blocks * kRows + quadrant * 32 >= at.nodes * p.group;
       const uint64_t mask = see;
       const uint64_t q2 = f2(qsum, qsum);
       float ref = 0.f, l = 0.f, z = 0.f;
@@ -593,41 +584,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
 #pragma unroll 1
       for (int32_t x = 0; x < units; ++x, ++j) {
         const uint32_t b = j & 1, ph = (j >> 1) & 1;
-        ok = ok && wait(&sh.sfull[b], ph) && wait(&sh.nfull[b], ph);
-        if (dead) {  // none of the warp's rows is a query's: P is zeros
-          if (lane == 0) {
-            mbar_arrive(smem_u32(&sh.sfree[b]));
-            mbar_arrive(smem_u32(&sh.nempty[b]));
-          }
-          if (j > 0) ok = ok && wait(&sh.odone, (j - 1) & 1);
+        ok = ok && wait(&sh.sfull[b], ph);  // (what the keys bring was written before their rows of K were taken)
+        if (dead) {  // none of the warp's rows is a query's: what P has there reaches no row that is read
           if (!ok) break;
-          uint32_t zero[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) zero[k] = 0;
-          tc_fence_after();
-          tmem_st_x32(tl + kPCol + half * 32, zero);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.pfull));
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sh.nempty[b]));
+            mbar_arrive(smem_u32(&sh.pfull[b]));
+          }
           continue;
         }
-        uint32_t sv[2][32];
+        uint32_t sv[kPartKeys];
         float top = -INFINITY;
         if (ok) {
           tc_fence_after();
-          tmem_ld_32x32b_x32(tl + b * kKeys + half * 64, sv[0]);
-          tmem_ld_32x32b_x32(tl + b * kKeys + half * 64 + 32, sv[1]);
+          tmem_ld_32x32b_x32(tl + b * kKeys + part * kPartKeys, sv);
           tmem_ld_wait();
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.sfree[b]));
           // Scores in log2 units, less the reference.
           const uint64_t nref = f2(-ref, -ref);
 #pragma unroll
-          for (int k = 0; k < 64; k += 4) {
-            const ulonglong2 ka = lds_f4(&sh.a[b][half * 64 + k]), kb = lds_f4(&sh.b[b][half * 64 + k]);
-            uint32_t* v = &sv[k >> 5][k & 31];
+          for (int k = 0; k < kPartKeys; k += 4) {
+            const ulonglong2 ka = lds_f4(&sh.a[b][part * kPartKeys + k]), kb = lds_f4(&sh.b[b][part * kPartKeys + k]);
+            uint32_t* v = &sv[k];
             const uint64_t s0 = f2_fma(f2(__uint_as_float(v[0]), __uint_as_float(v[1])), ka.x, f2_fma(kb.x, q2, nref));
             const uint64_t s1 = f2_fma(f2(__uint_as_float(v[2]), __uint_as_float(v[3])), ka.y, f2_fma(kb.y, q2, nref));
             v[0] = static_cast<uint32_t>(s0);
@@ -635,34 +613,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
             v[2] = static_cast<uint32_t>(s1);
             v[3] = static_cast<uint32_t>(s1 >> 32);
           }
-          const int key0 = (now.u + x) * kKeys + half * 64;
-          const uint32_t v0 = sh.valid[b][2 * half], v1 = sh.valid[b][2 * half + 1];
-          if ((v0 & v1) != ~0u || key0 + 64 > ctx) {
+          const int shared_keys = shared0 - x * kKeys;  // of this part, visible to every query
+          const uint32_t valid = sh.valid[b][part];
+          if (valid != ~0u || shared_keys < kPartKeys) {
+            uint32_t vis = shared_keys >= 32   ? ~0u
+                           : shared_keys >= 0  ? ((1u << shared_keys) - 1) | static_cast<uint32_t>(mask << shared_keys)
+                           : shared_keys > -64 ? static_cast<uint32_t>(mask >> -shared_keys)
+                                               : 0u;
+            vis &= valid;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int shared_keys = ctx - (key0 + 32 * c);  // of this chunk, visible to every query
-              uint32_t vis = shared_keys >= 32  ? ~0u
-                             : shared_keys >= 0 ? ((1u << shared_keys) - 1) | static_cast<uint32_t>(mask << shared_keys)
-                             : shared_keys > -64 ? static_cast<uint32_t>(mask >> -shared_keys)
-                                                 : 0u;
-              vis &= c ? v1 : v0;
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((vis >> k) & 1u)) sv[c][k] = 0xFF800000u;  // -inf
-            }
+            for (int k = 0; k < kPartKeys; ++k)
+              if (!((vis >> k) & 1u)) sv[k] = 0xFF800000u;  // -inf
           }
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 64; k += 2)
-            m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(sv[k >> 5][k & 31]), __uint_as_float(sv[k >> 5][(k & 31) + 1]));
+          for (int k = 0; k < kPartKeys; k += 2) m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], __uint_as_float(sv[k]), __uint_as_float(sv[k + 1]));
           top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
         }
-        sh.top[b][half][row] = top;
-        if (lane == 0) sh.okay[b][half][quadrant] = ok;
-        pair_bar(quadrant);
-        ok = ok && sh.okay[b][half ^ 1][quadrant];
+        sh.top[b][part][row] = top;
+        if (lane == 0) sh.okay[b][quadrant][part] = ok;
+        part_bar(quadrant);
+        const int4 okay = *reinterpret_cast<const int4*>(sh.okay[b][quadrant]);
+        ok = okay.x && okay.y && okay.z && okay.w;
         if (!ok) break;
-        top = fmaxf(top, sh.top[b][half ^ 1][row]);
+        top = fmaxf(max3(sh.top[b][0][row], sh.top[b][1][row], sh.top[b][2][row]), sh.top[b][3][row]);
         // The reference moves for a maximum far above it, and to the first key's.
         const float move = top > -INFINITY && (fresh || top > kSlack) ? top : 0.f;
         const bool moves = __any_sync(~0u, move != 0.f);
@@ -673,15 +647,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
           z *= r;
           ref += move;
 #pragma unroll
-          for (int k = 0; k < 64; ++k) sv[k >> 5][k & 31] = __float_as_uint(__uint_as_float(sv[k >> 5][k & 31]) - move);
+          for (int k = 0; k < kPartKeys; ++k) sv[k] = __float_as_uint(__uint_as_float(sv[k]) - move);
         }
         // Weights, and P for the second product.
-        uint32_t pw[32];
+        uint32_t pw[kPartKeys / 2];
         uint64_t l2[2] = {0, 0}, z2[2] = {0, 0};
 #pragma unroll
-        for (int k = 0; k < 64; k += 4) {
-          const ulonglong2 va = lds_f4(&sh.vs[b][half * 64 + k]), vb = lds_f4(&sh.vz[b][half * 64 + k]);
-          const uint32_t* v = &sv[k >> 5][k & 31];
+        for (int k = 0; k < kPartKeys; k += 4) {
+          const ulonglong2 va = lds_f4(&sh.vs[b][part * kPartKeys + k]), vb = lds_f4(&sh.vz[b][part * kPartKeys + k]);
+          const uint32_t* v = &sv[k];
           const uint64_t p0 = f2(ex2(__uint_as_float(v[0])), ex2(__uint_as_float(v[1])));
           const uint64_t p1 = f2(ex2(__uint_as_float(v[2])), ex2(__uint_as_float(v[3])));
           l2[0] = f2_add(l2[0], p0);
@@ -696,24 +670,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
         z += (f2_lo(z2[0]) + f2_hi(z2[0])) + (f2_lo(z2[1]) + f2_hi(z2[1]));
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.nempty[b]));
-        // P's place is free, and O complete, once the product of the unit before is done.
-        if (j > 0 && !wait(&sh.odone, (j - 1) & 1)) {
-          ok = false;
-          continue;  // the next barrier tells the other half
-        }
         tc_fence_after();
-        tmem_st_x32(tl + kPCol + half * 32, pw);
-        if (moves && x > 0) {  // this half's columns of O, and the sums of P
+        tmem_st_x16(tl + b * kKeys + part * (kPartKeys / 2), pw);  // (past the barrier all of the quadrant's S is read)
+        if (moves && x > 0) {  // this part's columns of O, and the sums of P, once the product of the unit before is done
+          if (!wait(&sh.odone[b ^ 1], ((j - 1) >> 1) & 1)) {
+            ok = false;
+            continue;  // the next barrier tells the others
+          }
+          tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < D / 2; c += 32) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(tl + kOCol + half * (D / 2) + c, o);
+          for (int c = 0; c < D / kParts; c += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(tl + kOCol + part * (D / kParts) + c, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * r);
-            tmem_st_x32(tl + kOCol + half * (D / 2) + c, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * r);
+            tmem_st_x16(tl + kOCol + part * (D / kParts) + c, o);
           }
-          if (half) {
+          if (part == 0) {
             const uint32_t o = tmem_ld_x1(tl + kOCol + D);
             tmem_ld_wait();
             tmem_st_x1(tl + kOCol + D, __float_as_uint(__uint_as_float(o) * r));
@@ -722,24 +696,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.pfull));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[b]));
       }
       // ---- the next piece's queries: all of this one's scores are in registers
       const bool more = ok && j < n;
+      const Shared::Start now = at;
+      const int head = now.item / now.blocks, row0 = (now.item - head * now.blocks) * kRows;
       if (more) {
-        forward(units);
+        Shared::Start next = now;
+        forward(next, units);
+        __syncwarp();
+        at = next;
+        __syncwarp();
         load_queries();
       }
-      if (ok) ok = wait(&sh.odone, (j - 1) & 1);
-      sh.l[half][row] = l;
-      sh.z[half][row] = z;
-      // One decision of the eight warps, so that none is left alone in a barrier.
+      if (ok) ok = wait(&sh.odone[(j - 1) & 1], ((j - 1) >> 1) & 1);
+      sh.l[part][row] = l;
+      sh.z[part][row] = z;
+      // One decision of the warps, so that none is left alone in a barrier.
       if (!ok) *abort = 1;
       soft_bar();
       if (tid == 0) sh.verdict = *abort;
-      l = sh.l[0][row] + sh.l[1][row];
-      z = sh.z[0][row] + sh.z[1][row];
-      qsum = sh.q[0][row] + sh.q[1][row];
+      l = (sh.l[0][row] + sh.l[1][row]) + (sh.l[2][row] + sh.l[3][row]);
+      z = (sh.z[0][row] + sh.z[1][row]) + (sh.z[2][row] + sh.z[3][row]);
+      qsum = (sh.q[0][row] + sh.q[1][row]) + (sh.q[2][row] + sh.q[3][row]);
       soft_bar();
       if (sh.verdict) break;
       tc_fence_after();
@@ -750,20 +730,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       const int r = row0 + row, i = r / p.group;
       const bool live = i < now.nodes;
       uint16_t* out = p.O + static_cast<int64_t>(now.b) * p.strideO + static_cast<int64_t>(i) * p.ldo +
-                      static_cast<int64_t>(head * p.group + r - i * p.group) * D + half * (D / 2);
+                      static_cast<int64_t>(head * p.group + r - i * p.group) * D + part * (D / kParts);
       const uint32_t first = u0 + (j - units) - now.u;  // the item's first unit
       const int slot = u0 >= first ? 0 : 1;             // of the parts of a CTA: the item that it begins in, or ends in
-      float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) + slot) * C::kPart;
+      float* mine = parts + (2 * static_cast<int64_t>(blockIdx.x) + slot) * C::kPart;
       const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(tl + kOCol + half * (D / 2) + c, o);
+      for (int c = 0; c < D / kParts; c += 16) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(tl + kOCol + part * (D / kParts) + c, o);
         tmem_ld_wait();
         if (whole) {
           if (live) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
+            for (int k = 0; k < 16; k += 8) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -772,9 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
             }
           }
         } else {
-          float4* to = reinterpret_cast<float4*>(part) + (half * (D / 8) + c / 4) * kRows + row;
+          float4* to = reinterpret_cast<float4*>(mine) + (part * (D / kParts / 4) + c / 4) * kRows + row;
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
+          for (int k = 0; k < 16; k += 4)
             __stcg(to + k / 4 * kRows, make_float4(__uint_as_float(o[k]) + add, __uint_as_float(o[k + 1]) + add, __uint_as_float(o[k + 2]) + add,
                                                    __uint_as_float(o[k + 3]) + add));
         }
@@ -782,9 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.oread));
-      if (!whole && half == 0) {
-        __stcg(part + kRows * D + row, fresh ? -INFINITY : ref);
-        __stcg(part + kRows * D + kRows + row, l);
+      if (!whole && part == 0) {
+        __stcg(mine + kRows * D + row, fresh ? -INFINITY : ref);
+        __stcg(mine + kRows * D + kRows + row, l);
       }
       if (!whole && now.u == 0 && tid == 0) {  // this CTA is the first of at most one item that goes on after it
         valid_cut = 1;
