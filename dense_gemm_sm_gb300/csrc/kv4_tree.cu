@@ -76,7 +76,7 @@ struct Shared {
   uint64_t qfull, oread, drain;
   uint32_t stage_mask[4];
   int32_t stage_keys[4];
-  uint32_t tmem_base, abort, verdict, issued, total;
+  uint32_t tmem_base, abort, verdict, issued, total, item;
   struct Start {
     uint32_t b;
     int32_t item, u, units, blocks, len, nodes;
@@ -210,15 +210,34 @@ struct Magic {
   }
 };
 
-// Units cut evenly over workers, the first `rem` of them one unit longer.
-struct Split {
+// `units` cut evenly over `workers`, the first `rem` of which have one more.
+struct Even {
   uint32_t q, rem;
-  __device__ __forceinline__ Split(uint32_t units, uint32_t workers) : q(units / workers), rem(units - q * workers) {}
+  __device__ __forceinline__ Even(uint32_t units, uint32_t workers) : q(units / workers), rem(units - q * workers) {}
   __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * q + (c < rem ? c : rem); }
   __device__ __forceinline__ uint32_t worker(uint32_t x) const {  // that has unit x
     const uint32_t long_units = rem * (q + 1);
     return x < long_units ? x / (q + 1) : rem + (x - long_units) / q;
   }
+};
+// The cut of all units over CTAs.  A CTA that goes from one item to the next pays 2.7 us between them, as
+// for nearly two units: items that all have the same number of units (`item`; 0: they do not) get CTAs of their
+// own where no share grows by more than one unit by that (16 nodes over 8208 tokens: 8 items of 65 units).
+struct Split {
+  uint32_t ctas, per, item;  // per: CTAs of an item, 0: cut without regard to items
+  Even cut;
+  static __device__ __forceinline__ uint32_t ceil(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
+  __device__ __forceinline__ Split(uint32_t total, uint32_t item, uint32_t grid)
+      : ctas(min(ceil(total, kMinUnits), grid)), per(0), item(item), cut(total, max(ctas, 1u)) {
+    if (item == 0 || total == 0) return;
+    const uint32_t items = total / item, k = min(grid / items, ceil(item, kMinUnits));
+    if (k == 0 || ceil(item, k) > ceil(total, ctas) + 1) return;
+    per = k;
+    ctas = k * items;
+    cut = Even(item, k);
+  }
+  __device__ __forceinline__ uint32_t start(uint32_t c) const { return per ? c / per * item + cut.start(c % per) : cut.start(c); }
+  __device__ __forceinline__ uint32_t worker(uint32_t x) const { return per ? x / item * per + cut.worker(x % item) : cut.worker(x); }
 };
 
 template <int D>
@@ -280,13 +299,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
     // A lane takes a run of sequences, and keeps what it read of the first.
     const uint32_t per = (batch + 31) / 32, b_lo = min(lane * per, batch), b_hi = min(b_lo + per, batch);
     int32_t len0 = 0, nodes0 = 0;
-    uint32_t mine = 0;
+    uint32_t mine = 0, low = ~0u, high = 0;  // units; the fewest and the most of an item
     for (uint32_t b = b_lo; b < b_hi; ++b) {
       const int32_t n = p.lens[b], m = p.nodes ? p.nodes[b] : static_cast<int32_t>(p.Lq);
       if (blockIdx.x == 0 && (n < 0 || n > cap || m < 0 || m > p.Lq)) atomicCAS(p.index_word, 0u, kDevBadIndex);
       const int32_t len = min(max(n, 0), cap), nodes = min(max(m, 0), static_cast<int32_t>(p.Lq));
       if (b == b_lo) len0 = len, nodes0 = nodes;
-      mine += key_units(len) * row_blocks(nodes) * p.heads;
+      const uint32_t n_units = key_units(len) * row_blocks(nodes) * p.heads;
+      if (n_units) low = min(low, key_units(len)), high = max(high, key_units(len));
+      mine += n_units;
     }
     uint32_t incl = mine;
 #pragma unroll
@@ -295,10 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       if (lane >= o) incl += v;
     }
     const uint32_t total = __shfl_sync(~0u, incl, 31);
-    const uint32_t ctas = min((total + kMinUnits - 1) / kMinUnits, gridDim.x);
-    if (lane == 0) sh.total = total;
-    if (blockIdx.x < ctas) {
-      const uint32_t r = Split(total, ctas).start(blockIdx.x);
+    low = __reduce_min_sync(~0u, low);
+    high = __reduce_max_sync(~0u, high);
+    const uint32_t same = low == high ? high : 0;
+    const Split split(total, same, gridDim.x);
+    if (lane == 0) sh.total = total, sh.item = same;
+    if (blockIdx.x < split.ctas) {
+      const uint32_t r = split.start(blockIdx.x);
       const int owner = __ffs(__ballot_sync(~0u, r < incl)) - 1;
       if (lane == owner) {
         uint32_t at = incl - mine, b = b_lo;
@@ -320,9 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, sh.tmem_base, 0);
-  const uint32_t total = sh.total, ctas = min((total + kMinUnits - 1) / kMinUnits, gridDim.x);
-  const bool active = blockIdx.x < ctas;
-  const Split split(total, active ? ctas : 1);
+  const Split split(sh.total, sh.item, gridDim.x);
+  const bool active = blockIdx.x < split.ctas;
   const uint32_t u0 = active ? split.start(blockIdx.x) : 0, n = active ? split.start(blockIdx.x + 1) - u0 : 0;
 
   // The pieces of items, one after the other.
