@@ -40,7 +40,7 @@ constexpr int kSoftWarps = 16, kExpandWarps = 4;
 constexpr int kParts = kSoftWarps / 4, kPartKeys = kKeys / kParts;  // of a unit's keys, one to each warp of a quadrant
 constexpr int kFirstExpand = kSoftWarps, kCopier = kFirstExpand + kExpandWarps, kIssuer = kCopier + 1;
 constexpr int kThreads = 32 * (kIssuer + 1);
-constexpr uint32_t kMinUnits = 2;   // of a CTA
+constexpr uint32_t kMinUnits = 1;   // of a CTA (2: one sequence of 512 tokens 14.4 -> 15.2 us)
 constexpr float kSlack = 8.f;       // the reference follows the maximum only when that has outgrown it by this
 constexpr int64_t kCounterBytes = 1024;  // of kv4_attention.cu's kernel, left as they are
 // Tensor memory: S (two buffers; P_j takes the place of S_j), O and the column of sums of P.
@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) kv4_tree_join_kernel(const Kv
   for (int w = 0; w < kMaxCtas / 32; ++w) items += __popc(votes[w]);
   const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.ws) + kCounterBytes);
   const int row = tid % kRows, share = tid / kRows;
-  const bool shared = items * (D / 4 / kJoinShare) < static_cast<int>(gridDim.x);
+  const bool shared = items * (D / 4) <= static_cast<int>(gridDim.x);  // (all at once)
   const int pieces = shared ? D / 4 : D / 4 / kJoinShare, step = shared ? kJoinShare : 1;
 #pragma unroll 1
   for (int t = blockIdx.x; t < items * pieces; t += gridDim.x) {
