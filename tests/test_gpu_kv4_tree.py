@@ -180,6 +180,69 @@ def test_tree_long_contexts_in_one_workspace(torch, lens, lq, hq, heads, d):
         check(torch, lens, nodes, lq, hq, heads, d, 64, seed=seed, ws=ws)
 
 
+# Items (sequence, cache head, 128 query rows) of one size, which get CTAs of their own where no CTA's
+# share grows by more than a unit of 128 keys, and of nearly one size; few items of many parts, which
+# threads share, many of few.
+@pytest.mark.parametrize("batch,length,other,lq,hq,heads,d", [
+    (1, 8208, 8208, 16, 16, 8, 128), (1, 19500, 19500, 40, 1, 1, 64), (1, 19500, 19500, 60, 8, 1, 128), (3, 512, 512, 20, 8, 4, 64),
+    (3, 512, 400, 20, 8, 4, 64), (19, 1000, 1000, 18, 2, 2, 128), (40, 300, 300, 20, 4, 4, 64), (75, 130, 257, 33, 2, 2, 64), (150, 129, 1, 17, 1, 1, 128)])
+def test_items_of_one_size(torch, batch, length, other, lq, hq, heads, d):
+    check(torch, [length] * (batch - 1) + [other], None if other >= lq else [lq] * (batch - 1) + [other], lq, hq, heads, d, 64, std=4.0)
+
+
+@pytest.mark.parametrize("lq", [3, 40])
+def test_trees_and_tokens_in_one_workspace(torch, lq):
+    """A workspace that attention_kv4 and attention_kv4_tree use in turn."""
+    rng = np.random.default_rng(9)
+    lens, hq, heads, d = [1500, 700], 8, 2, 128
+    pool, data, table = build(torch, rng, lens, 64, heads, d)
+    q = ref.bf16(rng.standard_normal((2, lq, hq, d))).astype(np.float64)
+    mask = trees(rng, 2, lq)
+    scale = float(np.float32(0.09))
+    ws = torch.zeros(dg.dg_attention_kv4_workspace_bytes(2, lq, hq, heads, d), dtype=torch.uint8, device="cuda")
+    want, bound = oracle(pool, q, table, lens, scale, ref.tree_sees(lens, [lq] * 2, mask))
+    plain, plain_bound = oracle(pool, q, table, lens, scale)
+    cache = dg.dg_kv4_cache(data, pool.pages, 64, heads, d)
+    Q = dev(torch, q.astype(np.float32).reshape(2, -1))
+    T, L = torch.from_numpy(table.astype(np.int32)).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        got = attend(torch, pool, data, table, lens, None, mask, q, scale, ws=ws)
+        assert np.all(np.abs(got - want) <= bound)
+        O = torch.zeros_like(Q)
+        dg.attention_kv4(cache, 2, lq, hq, scale, Q, hq * d, lq * hq * d, T, table.shape[1], L, O, hq * d, lq * hq * d, ws, ws.numel())
+        sync(torch)
+        assert np.all(np.abs(O.float().cpu().numpy().reshape(plain.shape) - plain) <= plain_bound)
+
+
+@pytest.mark.parametrize("lq", [3, 40])
+def test_two_streams_of_trees(torch, lq):
+    """Calls on two streams at once, each with a workspace of its own, on one cache."""
+    rng = np.random.default_rng(10)
+    lens, hq, heads, d = [3000, 900, 20], 8, 2, 64
+    pool, data, table = build(torch, rng, lens, 48, heads, d)
+    cache = dg.dg_kv4_cache(data, pool.pages, 48, heads, d)
+    T, L = torch.from_numpy(table.astype(np.int32)).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    calls = []
+    for _ in range(2):
+        q = ref.bf16(rng.standard_normal((3, lq, hq, d))).astype(np.float64)
+        n = [min(lq, k) for k in lens]
+        mask = trees(rng, 3, lq)
+        Q = dev(torch, q.astype(np.float32).reshape(3, -1))
+        calls.append((torch.cuda.Stream(), Q, torch.zeros((8,) + tuple(Q.shape), dtype=Q.dtype, device="cuda"), torch.from_numpy(mask.view(np.int64)).cuda(),
+                      torch.tensor(n, dtype=torch.int32, device="cuda"),
+                      torch.zeros(dg.dg_attention_kv4_workspace_bytes(3, lq, hq, heads, d), dtype=torch.uint8, device="cuda"),
+                      oracle(pool, q, table, lens, float(np.float32(0.125)), ref.tree_sees(lens, n, mask))))
+    torch.cuda.synchronize()
+    for k in range(8):
+        for stream, Q, O, M, N, ws, _ in calls:
+            dg.attention_kv4_tree(cache, 3, lq, hq, 0.125, Q, hq * d, lq * hq * d, T, table.shape[1], L, N, M, O[k], hq * d, lq * hq * d, ws, ws.numel(),
+                                  stream=stream)
+    sync(torch)
+    for _, _, O, _, _, _, (want, bound) in calls:
+        for k in range(8):
+            assert np.all(np.abs(O[k].float().cpu().numpy().reshape(want.shape) - want) <= bound)
+
+
 @pytest.mark.parametrize("lq", [6, 40])
 def test_tree_repeats_bit_for_bit_and_in_a_graph(torch, lq):
     rng = np.random.default_rng(12)
