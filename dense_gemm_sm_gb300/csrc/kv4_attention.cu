@@ -1111,16 +1111,18 @@ int64_t kv4_attention_ws_bytes(int64_t Lq, int64_t heads_q, int64_t heads_kv, in
   return nt == 1 ? ws_bytes<64, 1>() : nt == 2 ? ws_bytes<64, 2>() : ws_bytes<64, 4>();
 }
 
+template <int D, bool TREE>
+cudaError_t launch_rows_d(const Kv4AttnParams& p, int sms, cudaStream_t s) {
+  const int nt = tiles_of(p.Lq * p.group);
+  if (nt == 1) return launch_variant<D, 1, TREE>(p, sms, s);
+  if constexpr (!TREE)  // (trees of more than 16 rows do not come here)
+    if (nt == 4) return launch_variant<D, 4, false>(p, sms, s);
+  return launch_variant<D, 2, TREE>(p, sms, s);
+}
+
 template <bool TREE>
 cudaError_t launch_rows(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) {
-  const int nt = tiles_of(p.Lq * p.group);
-  if (d == 128)
-    return nt == 1   ? launch_variant<128, 1, TREE>(p, sms, s)
-           : nt == 2 ? launch_variant<128, 2, TREE>(p, sms, s)
-                     : launch_variant<128, 4, TREE>(p, sms, s);
-  return nt == 1   ? launch_variant<64, 1, TREE>(p, sms, s)
-         : nt == 2 ? launch_variant<64, 2, TREE>(p, sms, s)
-                   : launch_variant<64, 4, TREE>(p, sms, s);
+  return d == 128 ? launch_rows_d<128, TREE>(p, sms, s) : launch_rows_d<64, TREE>(p, sms, s);
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) {

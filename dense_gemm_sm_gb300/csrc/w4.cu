@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_w4_kernel(const W4RowsPar
 // Warps: 0-3 groups' sums and joins (a thread per column), 4-11 expansion (a warpgroup for each half of a
 // unit), 12 copies, 13 issues products, 14-15 sums of X.
 // Measured: 16 rows times 100003 columns of 4096 in 54 us, 4.1 TB/s; without the expansion's arithmetic 49, with
-// copies alone 42 (timing copies).  A third expanding warpgroup (56 us) and rings of their own for codes, X and
+// copies alone 42 (measured on altered copies of this kernel).  A third expanding warpgroup (56 us) and rings of their own for codes, X and
 // parameters (59) were slower: more warps share the same logic pipe.
 constexpr int kMaxCtas = 160;               // CTAs that the workspace has room for
 constexpr int kUnitK = 256, kHalfK = 128;

@@ -416,7 +416,7 @@ dg_status attention_kv4_tree(const dg_kv4_cache* cache, int64_t batch, int64_t L
  *     A sequence with lens outside [0, ldt * page_size], nodes outside [0, min(Lq, lens)] or
  *     counts outside [0, n] is left as it is, new_lens[b] = lens[b].  All of these are reported
  *     (DG_ERR_BAD_INDEX from dg_device_status).
- *   - Errors: null pointers, ldp < Lq DG_ERR_INVALID_ARG; Lq > 64, batch > 65536, ldt * page_size
+ *   - Errors: null pointers, ldp < Lq (of several sequences) DG_ERR_INVALID_ARG; Lq > 64, batch > 65536, ldt * page_size
  *     over 2^28 DG_ERR_UNSUPPORTED; pointers not 4-byte aligned DG_ERR_MISALIGNED; the cache's as
  *     kv4_append.  batch == 0: nothing.
  */
