@@ -93,23 +93,27 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // The same for a whole warp, whose lanes may name different barriers: returns when all of their phases have
-// completed.  The loop's branches are uniform, so that the warp stays converged: what follows may be a
-// `.aligned` instruction, which lanes that leave a loop of their own one after the other reach apart.
+// completed.  What a lane's barrier orders is ordered for that lane alone, and a vote orders no memory: the
+// __syncwarp hands it on, so that every lane may use what any of them waited for.  The loop's branches are
+// uniform, so that the warp stays converged: what follows may be a `.aligned` instruction, which lanes that
+// leave a loop of their own one after the other reach apart.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort,
                                                uint32_t* status, uint32_t code) {
-  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    if ((i & 31u) == 0) {
-      if (__any_sync(0xFFFFFFFFu, *abort != 0)) return false;
-      if (__any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > kWaitLimitNs)) {
-        *abort = 1;
-        atomicCAS(status, 0u, code);
-        return false;
+  if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1; !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++i) {
+      if ((i & 31u) == 0) {
+        if (__any_sync(0xFFFFFFFFu, *abort != 0)) return false;
+        if (__any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > kWaitLimitNs)) {
+          *abort = 1;
+          atomicCAS(status, 0u, code);
+          return false;
+        }
       }
     }
   }
+  __syncwarp();
+  return true;
 }
 
 // Drops the 128-byte L2 line at `line` (128-byte aligned) without writing it back: for

@@ -238,6 +238,26 @@ def test_product_repeats_bit_for_bit_and_in_a_graph(torch, m):
     assert np.array_equal(C.cpu().numpy(), 2 * first)
 
 
+@pytest.mark.parametrize("m,n,k,group", [(1, 1000, 2048, 128), (16, 3000, 1024, 32), (30, 1000, 2048, 64), (61, 3000, 1024, 128)])
+def test_stages_are_used_after_they_have_come(torch, m, n, k, group):
+    # Lanes of a warp wait for different barriers of a stage and use what the others waited for.  All sums are
+    # exact, and two inputs take turns in rings and tensor memory: what is used too early is another call's.
+    rng = np.random.default_rng(m)
+    ws = torch.zeros(dg.dg_gemm_w4_workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
+    turns = []
+    for _ in range(2):
+        w = Weights(torch, rng, n, k, group, exact=True)
+        x = rng.integers(-2, 3, (m, k)).astype(np.float32)
+        turns.append((w, dev(torch, x), torch.from_numpy((x.astype(np.float64) @ ref.w4_value(w.codes, w.scale, w.zero, group).T)).cuda(),
+                      torch.zeros((50, m, n), device="cuda")))
+    for i in range(50):
+        for w, x, _, c in turns:
+            dg.gemm_w4_bf16(m, n, k, group, x, k, w.Q, w.ldq, w.P, w.ldp, c[i], n, dg.DG_OUT_F32, ws, ws.numel())
+    sync(torch)
+    for _, _, want, c in turns:
+        assert bool((c.double() == want).all())
+
+
 def test_two_streams_with_their_own_workspaces(torch):
     rng = np.random.default_rng(9)
     w = [Weights(torch, rng, 3000, 4096, 128), Weights(torch, rng, 5000, 1024, 32)]
