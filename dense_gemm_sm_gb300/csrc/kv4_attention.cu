@@ -631,7 +631,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
               for (int i = 0; i < 2; ++i) {
                 const int k = key0 + r * kKv4Tokens + 8 * i + g;
                 const bool in = ((have >> r) & 1u) && k < seg.len;
-                if (!in) vp[r][i] = 0;  // a row that no query sees may hold anything
+                // A row that no query sees may hold anything.  A query that does not see one that others may see
+                // weighs it by 0: V's numbers that are not finite become 0 there, and scores NaN for those that see it.
+                if (!in) vp[r][i] = 0;
+                const bool wild = k >= shared_keys && !(fabsf(fmaf(8.f, lo_of(vp[r][i]), hi_of(vp[r][i]))) < INFINITY);
+                if (wild) vp[r][i] = 0;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -644,6 +648,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
                       seen = k <= seg.len - static_cast<int>(p.Lq) + (row0 + nt * 8 + 2 * t + e) / p.group;
                     }
                     if (!in || !seen) sc[r][nt][2 * i + e] = -INFINITY;
+                    else if (wild) sc[r][nt][2 * i + e] = __uint_as_float(0x7FC00000u);
                   }
               }
           }

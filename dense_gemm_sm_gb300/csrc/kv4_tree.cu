@@ -79,7 +79,7 @@ struct Shared {
   uint64_t cfull[4], cempty[4], kfull[2], kempty[2], vfull[2], vempty[2], nempty[2], sfull[2], pfull[2], odone[2];
   uint64_t qfull, oread, drain;
   uint32_t stage_mask[4];
-  int32_t stage_keys[4];
+  int32_t stage_keys[4], stage_shared[4];  // keys of a stage's unit, keys before the first that not every query sees
   uint32_t tmem_base, abort, verdict, issued, total, item;
   struct Start {
     uint32_t b;
@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       if (lane == 0) {
         sh.stage_mask[s] = mask;
         sh.stage_keys[s] = keys;
+        sh.stage_shared[s] = at.len - at.nodes - at.u * kKeys;
         mbar_arrive_expect_tx(f, __popc(mask) * C::kRec);
       }
       __syncwarp();
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
         const int rec = t >> 4, u = t & 15;
         const uint32_t row = st + rec * C::kRecStride + u * (D / 2), r = st + rec * C::kRecStride + 16 * D + u * 4;
         const uint32_t kp = lds32(r), vp = lds32(r + 64);
-        const bool valid = ((sh.stage_mask[s] >> rec) & 1u) && t < sh.stage_keys[s];
+        const bool valid = ((sh.stage_mask[s] >> rec) & 1u) && t < sh.stage_keys[s], drafted = t >= sh.stage_shared[s];
         if (!wait(&sh.kempty[b], bph ^ 1u)) break;
         const uint32_t out = sK + b * C::kKBytes + t * 128;
 #pragma unroll
@@ -501,12 +502,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
                          magic.pair<2>(ws[x]), magic.pair<3>(ws[x]));
         }
         if (!wait(&sh.nempty[b], bph ^ 1u)) break;
-        // A key that no query sees may hold anything.
+        // A slot past the sequence or the cache may hold anything, and so may one of a drafted token, which a query
+        // that does not see it weighs by 0: numbers of V that are not finite there become 0, and the score NaN, which
+        // the queries that see the key keep and the others replace.
         const float ks = valid ? lo_of(kp) : 0.f, kz = valid ? hi_of(kp) : 0.f, vs = valid ? lo_of(vp) : 0.f, vz = valid ? hi_of(vp) : 0.f;
+        const float v8 = fmaf(8.f, vs, vz);
+        const bool wild = drafted && !(fabsf(v8) < INFINITY);
         sh.a[b][t] = ks * p.c_log2;
-        sh.b[b][t] = fmaf(-16.f, ks, kz) * p.c_log2;
-        sh.vs[b][t] = vs;
-        sh.vz[b][t] = fmaf(8.f, vs, vz);
+        sh.b[b][t] = wild ? __uint_as_float(0x7FC00000u) : fmaf(-16.f, ks, kz) * p.c_log2;
+        sh.vs[b][t] = wild ? 0.f : vs;
+        sh.vz[b][t] = wild ? 0.f : v8;
         const uint32_t vote = __ballot_sync(~0u, valid);
         if (lane == 0) sh.valid[b][warp - kFirstExpand] = vote;
         fence_proxy_async_smem();

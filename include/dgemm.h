@@ -354,7 +354,9 @@ dg_status kv4_gather(const dg_kv4_cache* cache, int64_t tokens, const int64_t* s
  *     O[b][i][h] = sum_j softmax_j(scale * Q[b][i][h] . K_j) V_j,   j <= lens[b] - Lq + i,
  * K and V of head h / (heads_q / cache->heads).  The tokens are in the cache already: query i
  * of sequence b sits at position lens[b] - Lq + i.  A query that sees no key (lens[b] - Lq + i
- * < 0) gets 0; one that sees keys and holds NaN or Inf gets NaN.  FP32 scores, weights and sums; the weights times V's scale are rounded to BF16
+ * < 0) gets 0; one that sees keys and holds NaN or Inf gets NaN.  A key that not every query sees and
+ * whose V has a scale or zero that is not finite gives NaN to the queries that see it, and the others
+ * nothing.  FP32 scores, weights and sums; the weights times V's scale are rounded to BF16
  * for the second product; O rounded once to BF16.  Those sums reach 2^16 times V's scale per
  * key: rows of V whose max - min, times the number of keys, passes 5e34 are not supported.
  *   - Q: element (b, i, h, c) at Q[b * strideQ + i * ldq + h * d + c], likewise O.
@@ -387,7 +389,9 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
  * query i < n is node i and sees
  *     every key j < base, and key base + t where bit t of mask[b * Lq + i] is set, t < n
  * (its ancestors and itself, for a tree; no bit is taken for granted).  A query that sees no key
- * gets 0, and so do queries i >= n.  base may be negative: positions below 0 have no key.
+ * gets 0, and so do queries i >= n.  base may be negative: positions below 0 have no key.  What the
+ * slot of a node holds that a query does not see is nothing to it: a node that no mask names (the
+ * padding of a tree, or one whose row was never written) may hold anything, NaN and Inf too.
  *   - nodes: int32 [batch] on the device, or null; a value outside [0, Lq] is taken as the nearest
  *     bound and reported (DG_ERR_BAD_INDEX from dg_device_status).  mask: uint64 [batch][Lq] on
  *     the device.  All else, the workspace (dg_attention_kv4_workspace_bytes) among it, as
