@@ -529,6 +529,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         }
         sum += __shfl_xor_sync(~0u, sum, 1);
         sum += __shfl_xor_sync(~0u, sum, 2);
+        // An infinite sum becomes NaN: codes and zeros may both pull all scores to -Inf, and a row without a score
+        // above that is one that sees no key.
+        sum = fmaf(0.f, sum, sum);
 #pragma unroll
         for (int e = 0; e < 2; ++e) qsum[nt][e] = __shfl_sync(~0u, sum, (2 * t + e) * 4);
       }

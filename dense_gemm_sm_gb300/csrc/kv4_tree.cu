@@ -575,6 +575,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
     Shared::Start& at = sh.at[warp];  // (in shared memory, for registers: every lane writes the same)
     at = sh.start;
     float qsum = 0.f;
+    // The sum of a row's elements.  An infinite one becomes NaN: codes and zeros may both pull all scores to -Inf,
+    // and a row without a score above that is one that sees no key.
+    auto sum_of_queries = [&]() {
+      const float sum = (sh.q[0][row] + sh.q[1][row]) + (sh.q[2][row] + sh.q[3][row]);
+      return fmaf(0.f, sum, sum);
+    };
     uint64_t see = 0;  // the row's nodes
     // The piece's queries to shared memory, in the order of K's codes; rows without one are zeros.
     auto load_queries = [&]() {
@@ -601,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
     };
     if (n > 0) load_queries();
     part_bar(quadrant);
-    qsum = (sh.q[0][row] + sh.q[1][row]) + (sh.q[2][row] + sh.q[3][row]);
+    qsum = sum_of_queries();
     int32_t valid_cut = 0;
     uint32_t j = 0;
     while (j < n) {
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const Kv4AttnPara
       if (tid == 0) sh.verdict = *abort;
       l = (sh.l[0][row] + sh.l[1][row]) + (sh.l[2][row] + sh.l[3][row]);
       z = (sh.z[0][row] + sh.z[1][row]) + (sh.z[2][row] + sh.z[3][row]);
-      qsum = (sh.q[0][row] + sh.q[1][row]) + (sh.q[2][row] + sh.q[3][row]);
+      qsum = sum_of_queries();
       soft_bar();
       if (sh.verdict) break;
       tc_fence_after();

@@ -1,5 +1,5 @@
 """Attention over the 4-bit cache where drafted keys are not finite: they touch the queries that see them and
-no others."""
+no others; and where queries hold an infinity: they give NaN whatever the signs."""
 import numpy as np
 import pytest
 
@@ -97,3 +97,51 @@ def test_newest_tokens_that_are_not_finite(torch, lq, hq, heads, d, lens):
             assert close[~sees].all(), f"{which} {s:x} {z:x}: {(~close[~sees]).sum()} of {close[~sees].size}"
             if which == 1 and s != HUGE:
                 assert not np.isfinite(got[sees]).any()
+
+
+@pytest.mark.parametrize("lq,hq,heads,d,lens", FORMS)
+def test_infinite_queries_over_keys_far_from_zero(torch, lq, hq, heads, d, lens):
+    # Keys whose smallest element is far above their range: codes and zeros pull a score the same way, and with
+    # -Inf in the query every score is -Inf.
+    rng = np.random.default_rng(lq + d)
+    pool = ref.Kv4Pool(sum(-(-n // 32) for n in lens), 32, heads, d)
+    table, first = np.full((len(lens), max(-(-n // 32) for n in lens)), -1, np.int64), 0
+    for b, n in enumerate(lens):
+        need = -(-n // 32)
+        table[b, :need] = np.arange(first, first + need)
+        k = ref.bf16(100 + rng.standard_normal((n, heads, d)).astype(np.float32))
+        pool.append(k, rows(rng, (n, heads, d)), first * 32 + np.arange(n))
+        first += need
+    assert (pool.zero[0][pool.scale[0] > 0] > 128 * pool.scale[0][pool.scale[0] > 0]).all()
+    data = torch.from_numpy(pool.pack()).cuda()
+    q = ref.bf16(0.1 * rng.standard_normal((len(lens), lq, hq, d))).astype(np.float64)
+    mask = trees(rng, len(lens), lq)
+    mask[2, 1] = 0                                            # sees the context, where there is one
+    bad = np.zeros((len(lens), lq, hq), bool)
+    for b, i, h in [(0, 0, 0), (0, lq - 1, hq - 1), (1, 2, 1), (2, 1, 0), (2, 1, 1)]:
+        bad[b, i, h] = True
+    hit = q.copy()
+    hit[..., d // 2 + 3] = np.where(bad, -np.inf, hit[..., d // 2 + 3])
+    scale = float(np.float32(1 / np.sqrt(d)))
+
+    def run(queries, tree):
+        T, L = torch.from_numpy(table.astype(np.int32)).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+        Q = torch.from_numpy(queries.astype(np.float32)).to(torch.bfloat16).cuda()
+        O = torch.full_like(Q, -3.0)
+        ws = torch.zeros(dg.dg_attention_kv4_workspace_bytes(len(lens), lq, hq, heads, d), dtype=torch.uint8, device="cuda")
+        cache = dg.dg_kv4_cache(data, pool.pages, 32, heads, d)
+        if tree:
+            dg.attention_kv4_tree(cache, len(lens), lq, hq, scale, Q, hq * d, lq * hq * d, T, table.shape[1], L, None,
+                                  torch.from_numpy(mask.view(np.int64)).cuda(), O, hq * d, lq * hq * d, ws, ws.numel())
+        else:
+            dg.attention_kv4(cache, len(lens), lq, hq, scale, Q, hq * d, lq * hq * d, T, table.shape[1], L, O, hq * d, lq * hq * d, ws, ws.numel())
+        sync(torch)
+        return O.float().cpu().numpy()
+    for tree in (True, False):
+        good, got = run(q, tree), run(hit, tree)
+        sees = bad.copy()
+        if tree and lens[2] == lq:                            # no context and an empty mask: no key
+            sees[2, 1] = False
+            assert not got[2, 1, :2].any()
+        assert np.isnan(got[sees]).all(), tree
+        assert np.array_equal(got[~bad], good[~bad])
