@@ -1115,8 +1115,11 @@ constexpr int64_t ws_bytes() {
 
 int64_t kv4_attention_ws_bytes(int64_t Lq, int64_t heads_q, int64_t heads_kv, int d) {
   const int nt = tiles_of(Lq * (heads_q / heads_kv));
-  if (d == 128) return nt == 1 ? ws_bytes<128, 1>() : nt == 2 ? ws_bytes<128, 2>() : ws_bytes<128, 4>();
-  return nt == 1 ? ws_bytes<64, 1>() : nt == 2 ? ws_bytes<64, 2>() : ws_bytes<64, 4>();
+  const int64_t rows = d == 128 ? (nt == 1 ? ws_bytes<128, 1>() : nt == 2 ? ws_bytes<128, 2>() : ws_bytes<128, 4>())
+                                : (nt == 1 ? ws_bytes<64, 1>() : nt == 2 ? ws_bytes<64, 2>() : ws_bytes<64, 4>());
+  // Trees of more than 16 rows take the other kernel, which has parts of its own.
+  const int64_t tree = nt == 4 ? kv4_tree_ws_bytes(d) : 0;
+  return rows > tree ? rows : tree;
 }
 
 template <int D, bool TREE>
@@ -1135,7 +1138,7 @@ cudaError_t launch_rows(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) 
 
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s) {
   if (!p.mask) return launch_rows<false>(p, d, sms, s);
-  // Trees of more than 16 query rows a cache head (which the workspace then has room for).  8 heads, d = 128,
+  // Trees of more than 16 query rows a cache head.  8 heads, d = 128,
   // us here and there: one sequence of 8208 tokens 8 rows 14.6 and 18.1, 16 rows 22.5 and 18.2, 32 rows 37.6 and
   // 18.2; 8 of them 16 rows 32.7 and 58.3, 32 rows 56.0 and 58.5; 64 of 600 tokens 16 rows 24.8 and 54.6, 32 rows
   // 47.8 and 55.9.

@@ -101,6 +101,7 @@ struct Kv4AttnParams {
   const int32_t* nodes;
   const uint64_t* mask;
 };
+// Of all kernels that a call of these sizes may take.
 int64_t kv4_attention_ws_bytes(int64_t Lq, int64_t heads_q, int64_t heads_kv, int d);
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, int d, int sms, cudaStream_t s);
 // Trees of more than 16 query rows a cache head.

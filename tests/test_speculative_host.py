@@ -40,6 +40,14 @@ def test_tree_workspace_is_the_attention_s():
     assert dg.attention_kv4_tree(cache(), *{**TREE, "workspace_bytes": need - 1}.values(), stream=0, check=False) == INV
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lq,hq,heads", [(17, 1, 1), (5, 8, 2), (64, 32, 8), (1, 68, 4)])
+def test_workspace_has_room_for_every_tree(lq, hq, heads, d):
+    # More than 16 query rows a cache head: two parts of 128 rows (outputs, reference and sum in FP32) and a
+    # record of 32 bytes for each of 160 CTAs, behind 1024 bytes of counters.
+    assert dg.dg_attention_kv4_workspace_bytes(3, lq, hq, heads, d) >= 1024 + 160 * (2 * 128 * (d + 2) * 4 + 32)
+
+
 ACCEPT = dict(batch=3, Lq=4, page_table=P, ldt=4, lens=P, nodes=P, path=P, ldp=4, counts=P, new_lens=P)
 
 
