@@ -203,9 +203,10 @@ __global__ void __launch_bounds__(kThreads) dequantize_w4_kernel(const W4RowsPar
 //     least offset that keeps all four bits of c in a mantissa, and the layout has neighbouring k in
 //     the two halves of a word, so that pairs come out in the operand's order.
 //   * A group's sums stay apart: D = sum x (16 + c) is read from tensor memory when its group ends, and
-//     acc += s D + (z - 16 s) S, S = sum x, in FP32.  S comes from two warps of their own (mma.sync with an
-//     operand of ones); for 64 rows that would take them 2000 cycles a unit, and S comes from the same pipe as D,
-//     by products with ones in tensor memory.  Codes and x are exact in BF16, so no weight is rounded.
+//     acc += s D + (z / 16 - s) S, S = sum 16 x, in FP32 (16 s may be past its range where s is not).  S comes
+//     from two warps of their own (mma.sync with an operand of 16 throughout); for 64 rows that would take them 2000
+//     cycles a unit, and S comes from the same pipe as D, by products with 16 in tensor memory.  Codes and x are
+//     exact in BF16, so no weight is rounded.
 // Units of 128 columns x 256 k of all column tiles are cut evenly over one CTA per SM; a tile cut between
 // CTAs is finished by the last of them to arrive, which adds the parts in CTA order (results do not depend on
 // arrival).  More than 64 rows of X: each column tile is computed for one block of 64 after the other,
@@ -220,29 +221,30 @@ constexpr int kUnitK = 256, kHalfK = 128;
 constexpr uint32_t kCodeBytes = 128 * kUnitK / 2;
 constexpr int kEpiWarps = 4;
 constexpr uint32_t kMinUnits = 2;           // of a CTA
-// Tensor memory: 256 columns of D (and S), buffers of an expanded half of a unit, ones.
-constexpr uint32_t kACol = 256, kOnesCol = 448, kTmemCols = 512;
+// Tensor memory: 256 columns of D (and S), buffers of an expanded half of a unit, the operand of S.
+constexpr uint32_t kSixteens = 0x41804180u;  // two BF16
+constexpr uint32_t kACol = 256, kSumCol = 448, kTmemCols = 512;
 constexpr int64_t kCounterBytes = 1024;
 static_assert(kMaxCtas * 4 <= kCounterBytes, "counters");
 
 template <int NTOK, int GROUP>
 struct Cfg {
-  static constexpr bool kOnes = NTOK == 64;                  // S by the same pipe as D
-  static constexpr int kSumWarps = kOnes ? 0 : 2;
+  static constexpr bool kSumsByTile = NTOK == 64;            // S by the same pipe as D
+  static constexpr int kSumWarps = kSumsByTile ? 0 : 2;
   static constexpr int kProducer = kEpiWarps + 8, kIssuer = kProducer + 1, kFirstSum = kIssuer + 1;
   static constexpr int kThreads = 32 * (kFirstSum + kSumWarps);
-  static constexpr int kABuffers = kOnes ? 3 : 4;
+  static constexpr int kABuffers = kSumsByTile ? 3 : 4;
   static constexpr int kStages = NTOK == 16 ? 7 : NTOK == 32 ? 6 : 4;
   static constexpr int kGroups = kUnitK / GROUP;             // of a unit
   // Groups whose D is read together: all of a unit where they are at most 128 columns.
-  static constexpr int kMost = 128 / NTOK / (kOnes ? 2 : 1), kTogether = kGroups < kMost ? kGroups : kMost;
+  static constexpr int kMost = 128 / NTOK / (kSumsByTile ? 2 : 1), kTogether = kGroups < kMost ? kGroups : kMost;
   static constexpr int kReads = kGroups / kTogether;         // of a unit
-  static constexpr int kSlot = kTogether * NTOK * (kOnes ? 2 : 1);  // columns of one
+  static constexpr int kSlot = kTogether * NTOK * (kSumsByTile ? 2 : 1);  // columns of one
   static constexpr int kSlots = 256 / kSlot < 8 ? 256 / kSlot : 8;
   static_assert(kSlots >= 2 && (kReads == 1 || kReads % 2 == 0), "reads");
   static constexpr uint32_t kXBox = NTOK * 128, kXBytes = 4 * kXBox, kParamBytes = kGroups * 512;
   static constexpr uint32_t kStage = kCodeBytes + kXBytes + 4096;
-  static constexpr uint32_t kSumBytes = kOnes ? 0 : kGroups * NTOK * 4;  // of a stage
+  static constexpr uint32_t kSumBytes = kSumsByTile ? 0 : kGroups * NTOK * 4;  // of a stage
   static constexpr uint32_t kSmem = 1024 + kStages * (kStage + kSumBytes);
   static_assert(kStage % 1024 == 0 && kParamBytes <= 4096 && kSmem + 1024 <= 227 * 1024, "shared memory, with the static part");
 };
@@ -343,11 +345,11 @@ struct Magic {
   }
 };
 
-// The sums of eight rows of X over 16 k: a row of the product with ones.
-__device__ __forceinline__ void mma_ones(float (&c)[4], uint32_t b0, uint32_t b1) {
+// 16 times the sums of eight rows of X over 16 k: a row of the product with 16 throughout.
+__device__ __forceinline__ void mma_sums(float (&c)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%4,%4,%4}, {%5,%6}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(0x3F803F80u), "r"(b0), "r"(b1));
+      : "r"(kSixteens), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void ldmatrix_x4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&ctl.full[s]), 1);
       mbar_init(smem_u32(&ctl.empty[s]), 1 + kEpiWarps);
-      if (!C::kOnes) mbar_init(smem_u32(&ctl.sums[s]), C::kSumWarps);
+      if (!C::kSumsByTile) mbar_init(smem_u32(&ctl.sums[s]), C::kSumWarps);
     }
     for (int a = 0; a < kABuffers; ++a) {
       mbar_init(smem_u32(&ctl.afull[a]), 4);
@@ -391,9 +393,9 @@ __global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(~0u, ctl.tmem_base, 0);
   const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);  // this warp's lanes
-  if constexpr (C::kOnes) {
+  if constexpr (C::kSumsByTile) {
     if (warp < kEpiWarps) {
-      tmem_st_x8(tl + kOnesCol, 0x3F803F80u);
+      tmem_st_x8(tl + kSumCol, kSixteens);
       tmem_st_wait();
     }
     tc_fence_before();
@@ -459,14 +461,14 @@ __global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(
           if (j % kSteps == 0) umma_ts<false>(d + j / kSteps * NTOK, at, b, idesc, lead);
           else umma_ts<true>(d + j / kSteps * NTOK, at, b, idesc, lead);
         }
-        if constexpr (C::kOnes) {
+        if constexpr (C::kSumsByTile) {
           static_assert(C::kTogether == 1, "S lies behind its D");
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) {
             const int step = r * kSteps + j;
             const uint64_t b = x + ((step >> 2) * C::kXBox + (step & 3) * 32) / 16;
-            if (j == 0) umma_ts<false>(d + NTOK, tmem + kOnesCol, b, idesc, lead);
-            else umma_ts<true>(d + NTOK, tmem + kOnesCol, b, idesc, lead);
+            if (j == 0) umma_ts<false>(d + NTOK, tmem + kSumCol, b, idesc, lead);
+            else umma_ts<true>(d + NTOK, tmem + kSumCol, b, idesc, lead);
           }
         }
         commit(&ctl.dfull[slot], lead);
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(
     __syncwarp();
   } else if (warp >= kFirstSum) {
     // ------------------------------------------------------------ sums of X: a warp takes every other eight rows
-    if constexpr (!C::kOnes) {
+    if constexpr (!C::kSumsByTile) {
     constexpr int kTiles = NTOK / 8 / C::kSumWarps;
     const int w = warp - kFirstSum, r8 = lane & 7, piece = lane >> 3;
     uint32_t s = 0, ph = 0;
@@ -508,8 +510,8 @@ __global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(
         for (int t = 0; t < kTiles; ++t) {
           uint32_t b[4];
           ldmatrix_x4(x + (step >> 1) * C::kXBox + (t * C::kSumWarps + w) * 1024 + ((((step & 1) * 4 + piece) ^ r8) << 4), b);
-          mma_ones(c[t][0], b[0], b[1]);
-          mma_ones(c[t][1], b[2], b[3]);
+          mma_sums(c[t][0], b[0], b[1]);
+          mma_sums(c[t][1], b[2], b[3]);
         }
         if (step % (GROUP / 32) == GROUP / 32 - 1 && lane < 4) {  // rows of the product are alike
 #pragma unroll
@@ -578,19 +580,19 @@ __global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(
 #pragma unroll
         for (int r = 0; r < C::kReads; ++r) {
           // The stage (its parameters), the sums of X, D.
-          const bool first = r == 0 && lane < (C::kOnes ? 1 : 2);
+          const bool first = r == 0 && lane < (C::kSumsByTile ? 1 : 2);
           const uint32_t bar = first ? (lane == 0 ? smem_u32(&ctl.full[s]) : smem_u32(&ctl.sums[s])) : smem_u32(&ctl.dfull[slot]);
           ok = mbar_wait_warp(bar, first ? ph : dph, abort, p.status, kDevTimeoutEpilogue);
           if (!ok) break;
           tc_fence_after();
-          constexpr int kCols = C::kTogether * NTOK, kAtOnce = kCols < 32 || C::kOnes ? 16 : 32;
+          constexpr int kCols = C::kTogether * NTOK, kAtOnce = kCols < 32 || C::kSumsByTile ? 16 : 32;
           const uint32_t d = tl + slot * C::kSlot;
 #pragma unroll
           for (int c = 0; c < kCols; c += kAtOnce) {
-            uint32_t dv[kAtOnce], sv[C::kOnes ? kAtOnce : 1];
+            uint32_t dv[kAtOnce], sv[C::kSumsByTile ? kAtOnce : 1];
             if constexpr (kAtOnce == 16) tmem_ld_32x32b_x16(d + c, dv);
             else tmem_ld_32x32b_x32(d + c, dv);
-            if constexpr (C::kOnes) tmem_ld_32x32b_x16(d + NTOK + c, sv);
+            if constexpr (C::kSumsByTile) tmem_ld_32x32b_x16(d + NTOK + c, sv);
             tmem_ld_wait();
             if (c + kAtOnce == kCols) {
               tc_fence_before();
@@ -601,9 +603,9 @@ __global__ void __launch_bounds__(Cfg<NTOK, GROUP>::kThreads, 1) gemm_w4_kernel(
             for (int t = 0; t < kAtOnce; t += 4) {
               const int g = r * C::kTogether + (c + t) / NTOK, tok = (c + t) % NTOK;
               const uint32_t prm = lds32(ring + s * C::kStage + kCodeBytes + C::kXBytes + g * 512 + col * 4);
-              const float scale = lo_of(prm), zero = fmaf(-16.f, scale, hi_of(prm));
+              const float scale = lo_of(prm), zero = hi_of(prm) * 0.0625f - scale;
               uint4 x;
-              if constexpr (C::kOnes) x = make_uint4(sv[t], sv[t + 1], sv[t + 2], sv[t + 3]);
+              if constexpr (C::kSumsByTile) x = make_uint4(sv[t], sv[t + 1], sv[t + 2], sv[t + 3]);
               else x = lds128(sum_ring + s * C::kSumBytes + (g * NTOK + tok) * 4);
               acc[tok] = fmaf(scale, __uint_as_float(dv[t]), fmaf(zero, __uint_as_float(x.x), acc[tok]));
               acc[tok + 1] = fmaf(scale, __uint_as_float(dv[t + 1]), fmaf(zero, __uint_as_float(x.y), acc[tok + 1]));

@@ -478,8 +478,8 @@ dg_status dequantize_groups_w4(int64_t N, int64_t K, int32_t group, const uint8_
  *   - X: M x K BF16, row stride ldx.  C: M x N of c_type, row stride ldc.  Any M; the kernel is
  *     made for few rows (the weights are read once for each 64 of them).
  *   - A row of X that holds Inf or NaN gives values that are not finite (NaN where the definition
- *     has Inf, it may be), in that row only.  Sums of |X| over a group times 31 stay below FP32's
- *     range.
+ *     has Inf, it may be), in that row only.  Sums of |X| over a group times 31, these times the
+ *     group's scale, and the sums times its zero stay below FP32's range.
  *   - workspace: see above; dg_gemm_w4_workspace_bytes (0 for sizes it does not take).
  *   - Errors: negative sizes, short strides, null pointers, another c_type, a workspace that is
  *     too small DG_ERR_INVALID_ARG; a group that is not 32, 64 or 128, sizes over 2^30, 2^31 or

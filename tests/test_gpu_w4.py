@@ -313,3 +313,19 @@ def test_offsets_past_32_bits(torch):
     last = at >= n - 5
     rows = torch.from_numpy(at[last] - (n - 5)).cuda()
     assert np.array_equal(back[rows].float().cpu().numpy(), ref.bf16(ref.w4_value(codes[last], np.full_like(zero[last], 0.25), zero[last], group).astype(np.float32)))
+
+
+# ------------------------------------------------------------------ the ends of the range
+@pytest.mark.parametrize("m,group", [(3, 128), (30, 64), (40, 128), (64, 32)])
+def test_product_with_weights_near_the_end_of_the_range(torch, m, group):
+    # 16 times the largest scale is past FP32's range, as is 16 scale - zero.
+    rng = np.random.default_rng(m)
+    n, k = 150, 600
+    w = Weights(torch, rng, n, k, group)
+    w.scale[:, ::2] = ref.bf16(np.float32(2.25e37))
+    w.zero[:, ::2] = ref.bf16(np.float32(-1.68e38))
+    w.P = words(torch, ref.w4_params(w.scale, w.zero, w.ldp))
+    x = ref.bf16((1e-6 * rng.standard_normal((m, k))).astype(np.float32))
+    got = w.times(torch, x, True)
+    want, bound = ref.w4_gemm(x, w.codes, w.scale, w.zero, group, ref.F32)
+    assert np.all(np.abs(got - want) <= bound)
