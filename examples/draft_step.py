@@ -9,7 +9,8 @@ of drafted tokens goes through an attention layer and the vocabulary, and what t
 Node 0 of a tree is the last token that is certain, the others are guesses for what follows their parent.
 Weights and drafts are random here (every node's token is made a likely one, so that paths are
 found).  fork() gives a sequence's cache to another one: full pages are shared through the page
-tables, the page that both would write next is copied.
+tables, the page that both would write next is copied.  The host counts each page's users, so that
+no sequence writes into a page that another one reads.
 
     python examples/draft_step.py [--batch 8] [--nodes 16] [--context 4000] [--steps 4]
 """
@@ -60,6 +61,7 @@ class DraftStep:
         self.cache = dg.dg_kv4_cache(self.pool, pages, page_size, heads_kv, d)
         # Every sequence has pages for max_tokens (a program would hand them out as sequences grow).
         self.table = torch.randperm(pages, generator=g, device="cuda", dtype=torch.int32).view(batch, -1)
+        self.users, self.free = [1] * pages, []                   # sequences whose tables name a page; pages that none names
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
 
         def buf(*shape, dtype=torch.bfloat16):
@@ -126,13 +128,25 @@ class DraftStep:
         dg.kv4_accept(self.cache, b, t, self.table, self.table_width, self.lens, None, self.path, t, self.counts, self.lens)
 
     def fork(self, src, dst):
-        """Sequence dst goes on from what src has (lists of sequences; what dst had is gone)."""
+        """Sequence dst goes on from what src has (lists of sequences, one pair after the other; what dst had is gone)."""
         for a, b in zip(src, dst):
+            if a == b:
+                continue
             n = int(self.lens[a])
             full = n // self.page_size
+            old, source = self.table[b].tolist(), self.table[a].tolist()
+            for page in old:
+                self.users[page] -= 1
+                if self.users[page] == 0:
+                    self.free.append(page)
+            # Full pages are shared; the others are dst's own.  (The other tables name at most all pages but a
+            # table's width of them, so there are enough.)
+            new = source[:full] + [self.free.pop() for _ in range(full, self.table_width)]
+            for page in new:
+                self.users[page] += 1
+            self.table[b].copy_(torch.tensor(new, dtype=torch.int32))
             if n % self.page_size:
                 dg.kv4_copy_pages(self.cache, 1, self.table[a, full:full + 1].contiguous(), self.table[b, full:full + 1].contiguous())
-            self.table[b, :full] = self.table[a, :full]  # (dst's own full pages would go back to a program's free list)
             self.lens[b] = n
 
     def capture(self):

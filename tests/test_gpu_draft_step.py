@@ -152,6 +152,51 @@ def test_a_fork_goes_on_by_itself(example):
     assert int(a) != int(b)
 
 
+def kept(s, b):
+    """Sequence b's rows of K and V as they stand in the cache."""
+    torch = torch_mod()
+    n, w = int(s.lens[b]), s.heads_kv * s.d
+    at = torch.arange(n, device="cuda")
+    slots = s.table[b].long()[at // s.page_size] * s.page_size + at % s.page_size
+    k, v = (torch.empty((n, w), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dg.kv4_gather(s.cache, n, slots, k, w, v, w)
+    return k, v
+
+
+@pytest.mark.parametrize("forks", [
+    [(0, 2), (1, 2)],                                         # into a former copy, from a shorter sequence
+    [(0, 2), (1, 0)],                                         # into a former source
+    [(0, 2), (0, 1), (3, 0), (2, 3)],
+    [(0, 2), (2, 0), (1, 1)],                                 # back again; to itself
+])
+def test_forks_of_forks_write_into_no_shared_page(example, forks):
+    torch = torch_mod()
+    s = example.DraftStep(4, 5, 128, 4, 2, 64, 200, 32, 16, max_tokens=96)
+    k, v = (torch.randn((4, 41, 128), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    s.prompt(k, v)
+    s.lens.copy_(torch.tensor([41, 20, 33, 16]))              # contexts of different lengths, one that ends with its page
+    rows = {b: kept(s, b) for b in range(4)}
+    for a, b in forks:
+        s.fork([a], [b])
+        rows[b] = rows[a]
+    for step in range(2):
+        before = s.lens.tolist()
+        table = s.table.tolist()
+        for b in range(4):                                    # where b writes nobody else reads
+            others = [p for c in range(4) if c != b for p in table[c]]
+            assert len(set(table[b])) == len(table[b]) and not set(table[b][before[b] // 16:]) & set(others)
+        parent, token = example.random_trees(4, 5, 200)
+        s.draft(parent, token)
+        s.x.copy_(torch.randn_like(s.x))
+        s.verify()
+        s.accept()
+        torch.cuda.synchronize()
+        assert dg.dg_device_status() == dg.DG_OK
+        for b in range(4):
+            for x, y in zip(kept(s, b), rows[b]):
+                assert torch.equal(x[:len(y)], y)
+
+
 def test_the_command_runs(example):
     r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "draft_step.py"), "--batch", "2", "--nodes", "6", "--context", "100",
                         "--steps", "2"], capture_output=True, text=True, timeout=300)
