@@ -393,7 +393,8 @@ dg_status attention_kv4(const dg_kv4_cache* cache, int64_t batch, int64_t Lq, in
  * slot of a node holds that a query does not see is nothing to it: a node that no mask names (the
  * padding of a tree, or one whose row was never written) may hold anything, NaN and Inf too.
  *   - nodes: int32 [batch] on the device, or null; a value outside [0, Lq] is taken as the nearest
- *     bound and reported (DG_ERR_BAD_INDEX from dg_device_status).  mask: uint64 [batch][Lq] on
+ *     bound and reported (DG_ERR_BAD_INDEX from dg_device_status).  Of a sequence without a node
+ *     nothing is read.  mask: uint64 [batch][Lq] on
  *     the device.  All else, the workspace (dg_attention_kv4_workspace_bytes) among it, as
  *     attention_kv4.
  *   - Errors: as attention_kv4, and a null mask DG_ERR_INVALID_ARG; Lq > 64 DG_ERR_UNSUPPORTED;

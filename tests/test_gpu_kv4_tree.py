@@ -109,6 +109,29 @@ def test_trees_of_different_sizes(torch, lq, hq):
     check(torch, lens, nodes, lq, hq, 2, 64, 32, seed=4)
 
 
+@pytest.mark.parametrize("lq,hq", [(2, 4), (4, 8), (8, 4), (6, 16)])
+@pytest.mark.parametrize("nodes,lens", [([0, 2, 0, 1], [3000, 40, 500, 2]), ([1, 0], [33, 1500]), ([0, 0, 0], [100, 0, 700]),
+                                        ([2] + [0, 1, 0, 2, 0] * 30, [50] + [700, 90, 33, 64, 1] * 30)])
+def test_sequences_without_a_draft(torch, lq, hq, nodes, lens):
+    # Contexts without a query among others: zeros, and the others as ever.
+    check(torch, lens, nodes, lq, hq, 2, 128 if len(lens) < 5 else 64, 32, seed=lq)
+
+
+@pytest.mark.parametrize("lq", [2, 40])
+def test_context_without_a_draft_is_not_read(torch, lq):
+    # Not a page of it, which a page outside the cache would tell.
+    rng = np.random.default_rng(lq)
+    lens, nodes = [300, 600, 70], [lq, 0, lq]
+    pool, data, table = build(torch, rng, lens, 16, 2, 64)
+    table[1] = pool.pages
+    q = ref.bf16(rng.standard_normal((3, lq, 4, 64))).astype(np.float64)
+    mask = trees(rng, 3, lq)
+    got = attend(torch, pool, data, table, lens, nodes, mask, q, 0.125)
+    sync(torch)
+    want, bound = oracle(pool, q, table, lens, 0.125, ref.tree_sees(lens, nodes, mask))
+    assert np.all(np.abs(got - want) <= bound) and not got[1].any()
+
+
 @pytest.mark.parametrize("hq", [2, 16])
 def test_tree_longer_than_its_sequence(torch, hq):
     # The first nodes would lie before position 0: there are no such keys.
