@@ -79,10 +79,12 @@ class DraftStep:
         self.gemm_ws = buf(max(dg.dg_gemm_w4_workspace_bytes(m, w.n, w.k) for w in (self.wqkv, self.wo, self.wh)), dtype=torch.uint8)
 
     def slots(self, tokens):
-        """Slots of the next `tokens` tokens of every sequence."""
+        """Slots of the next `tokens` tokens of every sequence; past its pages -1, which kv4_append passes over (and
+        attention_kv4_tree reports the length)."""
         at = torch.arange(tokens, device="cuda")[None] + self.lens.long()[:, None]
-        page = torch.gather(self.table.long(), 1, at // self.page_size)
-        return (page * self.page_size + at % self.page_size).flatten()
+        nth = at // self.page_size
+        page = torch.gather(self.table.long(), 1, nth.clamp(max=self.table_width - 1))
+        return torch.where(nth < self.table_width, page * self.page_size + at % self.page_size, -1).flatten()
 
     def prompt(self, k, v):
         """Writes a prompt's keys and values, [batch, tokens, heads_kv * d] BF16, to the cache."""
@@ -134,6 +136,8 @@ class DraftStep:
                 continue
             n = int(self.lens[a])
             full = n // self.page_size
+            if n > self.table_width * self.page_size:
+                raise ValueError(f"sequence {a} has outgrown its pages")
             old, source = self.table[b].tolist(), self.table[a].tolist()
             for page in old:
                 self.users[page] -= 1

@@ -197,6 +197,25 @@ def test_forks_of_forks_write_into_no_shared_page(example, forks):
                 assert torch.equal(x[:len(y)], y)
 
 
+def test_a_sequence_that_outgrows_its_pages_is_reported(example):
+    torch = torch_mod()
+    s = example.DraftStep(2, 5, 128, 4, 2, 64, 200, 32, 16, max_tokens=48)
+    k, v = (torch.randn((2, 44, 128), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    s.prompt(k, v)
+    s.lens[1] = 20
+    first = kept(s, 0)
+    assert s.slots(5)[4] == -1 and (s.slots(5)[:4] >= 0).all() and (s.slots(5)[5:] >= 0).all()
+    s.draft(*example.random_trees(2, 5, 200))
+    s.verify()                                                # 49 tokens in 48 places
+    torch.cuda.synchronize()
+    assert dg.dg_device_status() == dg.DG_ERR_BAD_INDEX
+    with pytest.raises(ValueError):
+        s.fork([0], [1])
+    s.lens.copy_(torch.tensor([44, 20]))
+    for x, y in zip(kept(s, 0), first):
+        assert torch.equal(x, y)
+
+
 def test_the_command_runs(example):
     r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "draft_step.py"), "--batch", "2", "--nodes", "6", "--context", "100",
                         "--steps", "2"], capture_output=True, text=True, timeout=300)
