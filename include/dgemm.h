@@ -450,8 +450,8 @@ dg_status kv4_copy_pages(const dg_kv4_cache* cache, int64_t n, const int32_t* sr
  * k of one n, the last of a row may be shorter:
  *     zero = min w,  scale = bf16((max w - min w) / 15),
  *     code = clamp(round_half_even((w - zero) / scale), 0, 15),   w ~ zero + scale * code
- * (IEEE FP32 operations; a constant group has scale 0 and codes 0; W and max - min of a group must
- * be finite).
+ * (IEEE FP32 operations; where the scale is 0, in a constant group or one whose range is at most 7
+ * times BF16's least number, codes are 0; W and max - min of a group must be finite).
  *   - Q: row n at Q + n * ldq (bytes), 32-bit words of 8 codes: code k in word k / 8, at bit
  *     4 * (k % 8 / 2) of its low half where k is even, of its high half where k is odd.  Codes past
  *     K in a row's last word are written as 0 and may be anything when read.

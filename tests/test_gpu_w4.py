@@ -316,6 +316,33 @@ def test_offsets_past_32_bits(torch):
 
 
 # ------------------------------------------------------------------ the ends of the range
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_rows_of_tiny_weights(torch, group):
+    # Ranges from one subnormal BF16 step (2^-133) to 2^-96, across 1e-30, where quotients are taken another way.
+    # Where the scale rounds to 0 codes are 0.
+    rng = np.random.default_rng(group)
+    n, k = 160, 2 * group + 9
+    w = np.ldexp(rng.standard_normal((n, k)).astype(np.float32), -rng.integers(96, 134, (n, 1)))
+    w[0] = 0
+    w[0, 3] = 2.0 ** -133
+    w[1] = np.ldexp(rng.integers(0, 20, k).astype(np.float32), -133)
+    w[2] = 2.0 ** -126 + np.ldexp(rng.integers(0, 2, k).astype(np.float32), -133)
+    w[3:40] += ref.bf16(np.float32(1e-30) * (1 + rng.standard_normal((37, k)).astype(np.float32) * 0.3))
+    w = ref.bf16(w)
+    codes, scale, zero = ref.w4_quantise(w, group)
+    assert (scale == 0).any() and ((scale > 0) & (scale < 2.0 ** -126)).any()
+    ldq, ldp = -(-k // 32) * 16, n
+    Q, P = torch.zeros((n, ldq), dtype=torch.uint8, device="cuda"), torch.zeros((scale.shape[1], ldp), dtype=torch.int32, device="cuda")
+    dg.quantize_groups_w4(n, k, group, dev(torch, w), k, Q, ldq, P, ldp)
+    sync(torch)
+    assert np.array_equal(P.cpu().numpy().view(np.uint32), ref.w4_params(scale, zero, ldp))
+    assert np.array_equal(Q.cpu().numpy(), ref.w4_pack(codes, ldq))
+    back = torch.full((n, k), 3.0, dtype=torch.bfloat16, device="cuda")
+    dg.dequantize_groups_w4(n, k, group, Q, ldq, P, ldp, back, k)
+    sync(torch)
+    assert np.array_equal(back.float().cpu().numpy(), ref.bf16(ref.w4_value(codes, scale, zero, group).astype(np.float32)))
+
+
 @pytest.mark.parametrize("m,group", [(3, 128), (30, 64), (40, 128), (64, 32)])
 def test_product_with_weights_near_the_end_of_the_range(torch, m, group):
     # 16 times the largest scale is past FP32's range, as is 16 scale - zero.
