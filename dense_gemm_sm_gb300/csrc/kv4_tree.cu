@@ -21,8 +21,8 @@
 // Units of all (sequence, head, block of rows) items are cut evenly over one CTA per SM.  A cut item's parts
 // go to the workspace, and a small second kernel joins them in CTA order, spread over all SMs (one
 // CTA alone would read 66 kB for each part).
-// Measured: 4 sequences of 24064 tokens, 64 nodes, 32 heads over 8, d = 128: 153 us, 1.9 us a unit, of shared memory's wavefronts
-// 75 % (most are the four numbers that a key brings, read for each row), of the tensor pipe 30 %.  Eight softmax
+// Measured: 4 sequences of 24064 tokens, 64 nodes, 32 heads over 8, d = 128: 150 us, 1.9 us a unit, of shared memory's wavefronts
+// 73 % (most are the four numbers that a key brings, read for each row), of the tensor pipe 30 %.  Eight softmax
 // warps of 64 keys 172; sixteen that keep four rows in a thread, so that a key's numbers are read once for 16
 // rows, 177 (tcgen05.ld and st of 16 lanes); four more warps that expand V alone 159.
 #include <cuda_bf16.h>
