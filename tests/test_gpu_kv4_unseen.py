@@ -8,7 +8,7 @@ from oracle import serving as ref
 
 from .helpers import torch_mod
 from .test_gpu_kv4 import attend as attend_newest
-from .test_gpu_kv4 import build, dev, rows, sync
+from .test_gpu_kv4 import build, rows, sync
 from .test_gpu_kv4_tree import attend, trees
 
 pytestmark = pytest.mark.gpu
